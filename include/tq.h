@@ -325,6 +325,88 @@ tq_status tq_attn_decode_append_paged(const tq_plan *plan, const void *q, const 
                                       float scale, float sparse_v_threshold, float *out, void *workspace,
                                       size_t workspace_bytes, tq_stream_t stream);
 
+/* ---------------------------------------------------- upkeep of the pages
+ * The pages of a paged cache as a serving loop keeps them: which sequence row
+ * holds which pages, branches that share pages, growth, ends, and closing up
+ * the pool.  All of it on the device, so that a step needs no answer from it.
+ * (The pages of the method have no counterpart: they stop at one layer's
+ * paged write and read.)
+ *
+ * Books, caller-owned device memory:
+ *   block_table [n_seqs][max_pages]  page ids; row i's first
+ *                                    ceil(lens[i] / page_size) entries count
+ *   lens        [n_seqs]             positions in use, 0 for an empty row
+ *   refs        [n_pages]            rows (or other holders) of a page; 0: free
+ * A model's layers share the books; `layers` is a host array of n_layers
+ * caches of one geometry (n_pages, page_size), and wherever a page is copied
+ * it is copied in every layer.  Pages are taken lowest id first, in row order,
+ * so the results depend on the inputs alone.
+ * `in` is not written unless `out` is the same three pointers (not for
+ * tq_pages_fork, whose rows exchange places); otherwise they must not overlap.
+ * info: [2] int32, device.  Fork and resize: pages taken from the pool, and
+ * the number of pages missing.  A call that misses pages changes nothing: out
+ * is a copy of in and no page is copied.  A call whose books or arguments are
+ * out of range (a length outside [0, max_pages * page_size], a counted page id
+ * outside [0, n_pages), a parent outside [-1, n_seqs), for the compaction also
+ * a counted page without holder) changes nothing either; info is {0, -1} and
+ * the device status word 61.
+ * workspace: tq_pages_workspace_bytes(n_seqs, max_pages, n_pages) bytes.
+ * Alignment: 16 bytes for every cache array (norms too) and the workspace, 4
+ * for the books.  d is a power of two in [32, 256]; n_pages < 2^31.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, bits, page_size),
+ * TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
+typedef struct {
+    int32_t *block_table;
+    int32_t *lens;
+    int32_t *refs;
+} tq_page_table;
+
+/* Workspace bytes of the calls below (tq_pages_copy: n_seqs 0 and the
+ * destination's n_pages); 0 for invalid sizes. */
+size_t tq_pages_workspace_bytes(int n_seqs, int max_pages, int64_t n_pages);
+
+/* Copy page src_ids[i] of the layers `src` to page dst_ids[i] of the layers
+ * `dst`, i < n, in every layer; src and dst may be one pool.  A pair with a
+ * negative id is skipped.  So is one with an id past the pool's end (device
+ * status word 61), one whose destination an earlier pair has (the earlier one
+ * is copied), and within one pool one whose destination is some pair's source
+ * (status word 62).  n <= dst[0].n_pages.  Layer l of src and of dst are the
+ * same memory for all l, or no layers overlap (TQ_ERR_INVALID_ARG). */
+tq_status tq_pages_copy(const tq_paged_cache *src, const tq_paged_cache *dst, int n_layers, int Hkv,
+                        int d, int k_bits, int v_bits, const int32_t *src_ids, const int32_t *dst_ids,
+                        int64_t n, void *workspace, size_t workspace_bytes, tq_stream_t stream);
+
+/* Rows branched and reordered: row i of `out` becomes row parents[i] of `in`
+ * ([n_seqs] int32, device; -1: an empty row).  Pages are shared (refs count
+ * the rows), but a last page that is partly filled has one writer: it stays
+ * with row p itself if parents[p] = p, else with the first row whose parent p
+ * is, and every other child takes a free page with a copy of it.  Rows of
+ * `in` without children give their pages back before any page is taken. */
+tq_status tq_pages_fork(tq_page_table in, const int32_t *parents, tq_page_table out, int n_seqs,
+                        int max_pages, const tq_paged_cache *layers, int n_layers, int Hkv, int d,
+                        int k_bits, int v_bits, int32_t *info, void *workspace, size_t workspace_bytes,
+                        tq_stream_t stream);
+
+/* Rows grown, cut back or freed: row i gets the length new_lens[i] ([n_seqs]
+ * int32, device; negative: as it is).  First the pages past the new lengths
+ * are given back.  Then, in row order, a row that grows takes the pages it
+ * lacks; where it goes on inside a partly filled last page that other rows
+ * hold too, it takes a page with a private copy of that one first (the last
+ * holder keeps the page). */
+tq_status tq_pages_resize(tq_page_table in, const int32_t *new_lens, tq_page_table out, int n_seqs,
+                          int max_pages, const tq_paged_cache *layers, int n_layers, int Hkv, int d,
+                          int k_bits, int v_bits, int32_t *info, void *workspace, size_t workspace_bytes,
+                          tq_stream_t stream);
+
+/* The pool closed up: with L held pages, every held page with an id >= L moves
+ * to a free page with an id < L, in ascending order of both, and the table and
+ * holders follow.  moved_to: [n_pages] int32, device: each page's new id, -1
+ * for pages that were free.  info: L, and the number of pages moved. */
+tq_status tq_pages_compact(tq_page_table in, tq_page_table out, int32_t *moved_to, int n_seqs,
+                           int max_pages, const tq_paged_cache *layers, int n_layers, int Hkv, int d,
+                           int k_bits, int v_bits, int32_t *info, void *workspace, size_t workspace_bytes,
+                           tq_stream_t stream);
+
 /* Workspace bytes tq_attn_prefill needs for a cache of capacity `cap`: 32 KB
  * for the query rotation matrix, then the expanded K/V tiles, 99332 bytes per
  * 128 cache positions per sequence and KV head (about 6.5 times the packed

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
@@ -29,7 +30,8 @@ EXPORTS = ("tq_codebook_init", "tq_plan_create", "tq_plan_destroy", "tq_plan_sig
            "tq_attn_decode_noalloc", "tq_attn_decode_ex", "tq_append_paged", "tq_attn_decode_paged",
            "tq_attn_decode_append_paged", "tq_plan_create_ex", "tq_plan_signs2", "tq_codebook_init_gaussian",
            "tq_attn_prefill_workspace_bytes", "tq_attn_prefill", "tq_qjl_matrix", "tq_encode_qjl",
-           "tq_decode_qjl", "tq_attn_qjl_workspace_bytes", "tq_attn_decode_qjl")
+           "tq_decode_qjl", "tq_attn_qjl_workspace_bytes", "tq_attn_decode_qjl",
+           "tq_pages_workspace_bytes", "tq_pages_copy", "tq_pages_fork", "tq_pages_resize", "tq_pages_compact")
 
 
 class TQError(RuntimeError):
@@ -52,6 +54,10 @@ class PagedCacheView(ctypes.Structure):
     _fields_ = [("k_packed", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
                 ("v_packed", ctypes.c_void_p), ("v_norm", ctypes.c_void_p),
                 ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
+
+
+class PageTableView(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
 
 
 @lru_cache(maxsize=1)
@@ -96,6 +102,14 @@ def lib() -> ctypes.CDLL:
         ("tq_attn_prefill_workspace_bytes", ctypes.c_size_t, [i32, i32, i32, i32, i64, i32]),
         ("tq_attn_prefill", i32, [vp, vp, i32, i32, i32, i32, CacheView, vp, i32, i32, f32, vp, vp,
                                   ctypes.c_size_t, vp]),
+        ("tq_pages_workspace_bytes", ctypes.c_size_t, [i32, i32, i64]),
+        ("tq_pages_copy", i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp, ctypes.c_size_t, vp]),
+        ("tq_pages_fork", i32, [PageTableView, vp, PageTableView, i32, i32, vp, i32, i32, i32, i32, i32, vp, vp,
+                                ctypes.c_size_t, vp]),
+        ("tq_pages_resize", i32, [PageTableView, vp, PageTableView, i32, i32, vp, i32, i32, i32, i32, i32, vp, vp,
+                                  ctypes.c_size_t, vp]),
+        ("tq_pages_compact", i32, [PageTableView, PageTableView, vp, i32, i32, vp, i32, i32, i32, i32, i32, vp, vp,
+                                   ctypes.c_size_t, vp]),
         ("tq_status_string", ctypes.c_char_p, [i32]),
         ("tq_last_cuda_error", i32, []),
         ("tq_device_status", i32, [i32, ctypes.POINTER(i32)]),
@@ -466,6 +480,169 @@ def tq_attn_prefill(plan: Plan, q: torch.Tensor, cache: Cache, q_start: torch.Te
         cache.v_bits, ctypes.c_float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _stream(q)))
     return out
+
+
+# ------------------------------------------------------------ upkeep of the pages
+
+class PagedLayers:
+    """The layers of one pool: paged caches of one geometry that share a block
+    table.  Holds their addresses, so that a call passes them as they are."""
+
+    def __init__(self, layers):
+        layers = [layers] if isinstance(layers, PagedCache) else list(layers)
+        if not layers:
+            raise ValueError("at least one layer")
+        c = layers[0]
+        for x in layers:
+            for t in (x.k_packed, x.k_norm, x.v_packed, x.v_norm):
+                _cuda(t)
+                if t.device != c.k_norm.device:
+                    raise ValueError("the layers must be on one device")
+            if (x.k_packed.dtype, x.v_packed.dtype) != (torch.uint8,) * 2 or \
+                    (x.k_norm.dtype, x.v_norm.dtype) != (torch.float32,) * 2:
+                raise TypeError("packed rows must be uint8 and norms fp32")
+            if (x.k_packed.shape, x.v_packed.shape, x.k_norm.shape, x.v_norm.shape, x.k_bits, x.v_bits) != \
+                    (c.k_packed.shape, c.v_packed.shape, c.k_norm.shape, c.k_norm.shape, c.k_bits, c.v_bits):
+                raise ValueError("the layers must have one geometry")
+        self.layers = layers  # keeps the tensors alive
+        self.k_bits, self.v_bits, self.device = c.k_bits, c.v_bits, c.k_norm.device
+        self.n_pages, self.Hkv, self.page_size = c.k_norm.shape
+        self.d = c.k_packed.shape[-1] * 8 // c.k_bits
+        if tuple(c.k_packed.shape) != (*c.k_norm.shape, self.d * c.k_bits // 8) or \
+                tuple(c.v_packed.shape) != (*c.k_norm.shape, self.d * c.v_bits // 8):
+            raise ValueError("packed rows must be [n_pages, Hkv, page_size, d*bits/8]")
+        self.views = (PagedCacheView * len(layers))(*(x.view() for x in layers))
+        self.args = (self.Hkv, self.d, self.k_bits, self.v_bits)
+
+
+@dataclass
+class PageTable:
+    """The books of a paged cache's pages (caller-owned device tensors, int32)."""
+    block_table: torch.Tensor  # [n_seqs, max_pages]: page ids, -1 past a row's pages
+    lens: torch.Tensor         # [n_seqs]: positions in use
+    refs: torch.Tensor         # [n_pages]: holders of a page, 0 for a free one
+
+    @staticmethod
+    def empty(n_seqs, max_pages, n_pages, device="cuda"):
+        return PageTable(torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                         torch.zeros(n_seqs, dtype=torch.int32, device=device),
+                         torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+    def _view(self, layers: PagedLayers) -> PageTableView:
+        for name, t in (("block_table", self.block_table), ("lens", self.lens), ("refs", self.refs)):
+            _i32(t, name)
+        if self.block_table.dim() != 2 or self.lens.numel() != self.block_table.shape[0] or \
+                self.refs.numel() != layers.n_pages:
+            raise ValueError("block_table [n_seqs, max_pages], lens [n_seqs], refs [n_pages] expected")
+        _same_device(layers.device, self.block_table, self.lens, self.refs)
+        return PageTableView(self.block_table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr())
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _on(device):
+    """The device made current for a call, where it is not."""
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else nullcontext()
+
+
+def _layers(x) -> PagedLayers:
+    return x if isinstance(x, PagedLayers) else PagedLayers(x)
+
+
+def _scratch(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _cuda(workspace)
+    _same_device(device, workspace)
+    return workspace
+
+
+def tq_pages_workspace_bytes(n_seqs: int, max_pages: int, n_pages: int) -> int:
+    return int(lib().tq_pages_workspace_bytes(n_seqs, max_pages, n_pages))
+
+
+def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                  workspace: torch.Tensor | None = None):
+    """Copy page src_ids[i] of `src` to page dst_ids[i] of `dst` (PagedLayers,
+    a PagedCache or a list of them; one pool or two) in every layer.  Pairs
+    with a negative id are skipped; a destination given twice, or that is also
+    a source within one pool, is refused pair by pair (device status 62)."""
+    src, dst = _layers(src), _layers(dst)
+    if len(src.views) != len(dst.views) or src.args != dst.args or src.page_size != dst.page_size:
+        raise ValueError("src and dst must have the same number of layers and geometry")
+    _i32(src_ids, "src_ids")
+    _i32(dst_ids, "dst_ids")
+    if src_ids.numel() != dst_ids.numel():
+        raise ValueError("src_ids and dst_ids must have one length")
+    _same_device(dst.device, src.layers[0].k_norm, src_ids, dst_ids)
+    with _on(dst.device):
+        ws = _scratch(workspace, tq_pages_workspace_bytes(0, 0, dst.n_pages), dst.device)
+        _check("tq_pages_copy", lib().tq_pages_copy(
+            src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(),
+            src_ids.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dst_ids)))
+
+
+def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
+    layers = _layers(layers)
+    n_seqs, max_pages = table.block_table.shape
+    dev = layers.device
+    with _on(dev):
+        if out is None:
+            out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
+        if info is None:
+            info = torch.empty(2, dtype=torch.int32, device=dev)
+        _i32(info, "info")
+        if info.numel() != 2 or out.block_table.shape != table.block_table.shape:
+            raise ValueError("info must have 2 entries and out the table's shape")
+        _same_device(dev, info)
+        if arg is not None:
+            _i32(arg, "parents / new_lens")
+            _same_device(dev, arg)
+            if arg.numel() != n_seqs:
+                raise ValueError("one entry per row expected")
+        views = (table._view(layers), out._view(layers))
+        ws = _scratch(workspace, tq_pages_workspace_bytes(n_seqs, max_pages, layers.n_pages), dev)
+        middle = (views[0], arg.data_ptr(), views[1]) if arg is not None else (*views, moved.data_ptr())
+        _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,
+                                      info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(info)))
+    return out, info
+
+
+def tq_pages_fork(table: PageTable, parents: torch.Tensor, layers, out: PageTable | None = None,
+                  info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Row i of the result is row parents[i] of `table` (int32; -1: empty):
+    full pages shared, a partly filled last page copied for all children but
+    one.  Returns (table, info [2]: pages taken, pages missing)."""
+    return _pages("tq_pages_fork", table, parents, layers, out, None, info, workspace)
+
+
+def tq_pages_resize(table: PageTable, new_lens: torch.Tensor, layers, out: PageTable | None = None,
+                    info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Row i gets the length new_lens[i] (int32; negative: unchanged): pages
+    past it are given back, missing ones taken, and a shared last page that
+    the row goes on in replaced by a private copy.  `out` may be `table`.
+    Returns (table, info [2]: pages taken, pages missing)."""
+    return _pages("tq_pages_resize", table, new_lens, layers, out, None, info, workspace)
+
+
+def tq_pages_compact(table: PageTable, layers, out: PageTable | None = None, moved_to: torch.Tensor | None = None,
+                     info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """The held pages moved to the lowest ids.  `out` may be `table`.  Returns
+    (table, moved_to [n_pages]: each page's new id or -1, info [2]: pages
+    held, pages moved)."""
+    layers = _layers(layers)
+    if moved_to is None:
+        moved_to = torch.empty(layers.n_pages, dtype=torch.int32, device=layers.device)
+    _i32(moved_to, "moved_to")
+    _same_device(layers.device, moved_to)
+    if moved_to.numel() != layers.n_pages:
+        raise ValueError("moved_to must have n_pages entries")
+    out, info = _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
+    return out, moved_to, info
 
 
 def tq_device_status(reset: bool = False) -> int:

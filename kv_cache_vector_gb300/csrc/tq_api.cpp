@@ -878,6 +878,175 @@ tq_status tq_attn_decode_append_paged(const tq_plan* plan, const void* q, const 
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
+// ------------------------------------------------------------ upkeep of the pages
+
+size_t tq_pages_workspace_bytes(int n_seqs, int max_pages, int64_t n_pages) {
+    if (n_seqs < 0 || max_pages < 0 || n_pages < 1 || n_pages > INT32_MAX) return 0;
+    return tq::pages_workspace_bytes(n_seqs, n_pages);
+}
+
+namespace {
+struct Span {
+    uintptr_t at;
+    uint64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) { return a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
+
+// The layers of one pool: geometry, pointers and alignment.
+tq_status check_layers(const tq_paged_cache* layers, int n_layers, int Hkv, int d, int k_bits, int v_bits) {
+    if (!layers || n_layers < 1 || Hkv < 1) return TQ_ERR_INVALID_ARG;
+    if (!valid_bits(k_bits) || !valid_bits(v_bits) || d < 32 || d > tq::kMaxD || !is_pow2(d)) return TQ_ERR_UNSUPPORTED;
+    const int shift = page_shift_of(layers[0].page_size);
+    if (shift < 0) return TQ_ERR_UNSUPPORTED;
+    if (layers[0].n_pages < 1 || layers[0].n_pages > INT32_MAX) return TQ_ERR_INVALID_ARG;
+    // a page's 16-byte words are counted in 32 bits
+    if (((int64_t)Hkv << shift) * (d / 2 + 8) * 2 > (int64_t(1) << 31)) return TQ_ERR_UNSUPPORTED;
+    for (int l = 0; l < n_layers; ++l) {
+        const tq_paged_cache& c = layers[l];
+        if (c.n_pages != layers[0].n_pages || c.page_size != layers[0].page_size || !paged_pointers_ok(c))
+            return TQ_ERR_INVALID_ARG;
+        if (!paged_aligned(c) || !aligned16(c.k_norm) || !aligned16(c.v_norm)) return TQ_ERR_ALIGNMENT;
+    }
+    return TQ_OK;
+}
+
+// Bytes of array a (0 packed K, 1 K norms, 2 packed V, 3 V norms) of a layer.
+Span layer_span(const tq_paged_cache& c, int a, int Hkv, int d, int k_bits, int v_bits) {
+    const uint64_t rows = (uint64_t)c.n_pages * Hkv * c.page_size;
+    const void* p = a == 0 ? (const void*)c.k_packed : a == 1 ? (const void*)c.k_norm : a == 2 ? (const void*)c.v_packed : (const void*)c.v_norm;
+    return {reinterpret_cast<uintptr_t>(p), rows * (a == 0 ? d * k_bits / 8 : a == 2 ? d * v_bits / 8 : 4)};
+}
+
+// Fork, resize and compaction: the checks they share, then the launch.
+tq_status pages_call(int op, tq_page_table in, tq_page_table out, const int32_t* arg, int32_t* moved, int n_seqs,
+                     int max_pages, const tq_paged_cache* layers, int n_layers, int Hkv, int d, int k_bits,
+                     int v_bits, int32_t* info, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+    if (n_seqs < 1 || max_pages < 1) return TQ_ERR_INVALID_ARG;
+    const tq_status st = check_layers(layers, n_layers, Hkv, d, k_bits, v_bits);
+    if (st != TQ_OK) return st;
+    const bool needs_arg = op != tq::kPagesCompact;
+    if (!in.block_table || !in.lens || !in.refs || !out.block_table || !out.lens || !out.refs || !info ||
+        (needs_arg && !arg) || (!needs_arg && !moved))
+        return TQ_ERR_INVALID_ARG;
+    if (!aligned4(in.block_table) || !aligned4(in.lens) || !aligned4(in.refs) || !aligned4(out.block_table) ||
+        !aligned4(out.lens) || !aligned4(out.refs) || !aligned4(info) || !aligned4(arg) || !aligned4(moved))
+        return TQ_ERR_ALIGNMENT;
+    const int shift = page_shift_of(layers[0].page_size);
+    if (((int64_t)max_pages << shift) > INT32_MAX) return TQ_ERR_UNSUPPORTED;  // lengths are int32
+    const int64_t n_pages = layers[0].n_pages;
+    if (!workspace || workspace_bytes < tq::pages_workspace_bytes(n_seqs, n_pages)) return TQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+    // what is read and what is written: apart, except that a resize and a
+    // compaction may work in place
+    auto span = [](const void* p, uint64_t n) { return Span{reinterpret_cast<uintptr_t>(p), 4 * n}; };
+    const uint64_t cells = (uint64_t)n_seqs * max_pages;
+    const Span rd[4] = {span(in.block_table, cells), span(in.lens, n_seqs), span(in.refs, n_pages),
+                        span(arg, arg ? n_seqs : 0)};
+    const Span wr[6] = {span(out.block_table, cells), span(out.lens, n_seqs), span(out.refs, n_pages),
+                        span(info, 2), span(moved, moved ? n_pages : 0),
+                        {reinterpret_cast<uintptr_t>(workspace), tq::pages_workspace_bytes(n_seqs, n_pages)}};
+    const bool in_place = in.block_table == out.block_table && in.lens == out.lens && in.refs == out.refs;
+    if (in_place && op == tq::kPagesFork) return TQ_ERR_INVALID_ARG;
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap(wr[i], rd[j]) && !(in_place && i == j)) return TQ_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(wr[i], wr[j])) return TQ_ERR_INVALID_ARG;
+    }
+    if (!device_accessible(in.block_table) || !device_accessible(in.lens) || !device_accessible(in.refs) ||
+        !device_accessible(out.block_table) || !device_accessible(out.lens) || !device_accessible(out.refs) ||
+        !device_accessible(info) || !device_accessible(workspace) || (arg && !device_accessible(arg)) ||
+        (moved && !device_accessible(moved)) || !paged_accessible(layers[0]))
+        return TQ_ERR_INVALID_ARG;
+    tq::PagesCall c = {};
+    c.in = in;
+    c.out = out;
+    c.arg = arg;
+    c.moved = moved;
+    c.info = info;
+    c.ws = workspace;
+    c.n_seqs = n_seqs;
+    c.max_pages = max_pages;
+    c.page_shift = shift;
+    c.src = c.dst = layers;
+    c.n_layers = n_layers;
+    c.Hkv = Hkv;
+    c.d = d;
+    c.k_bits = k_bits;
+    c.v_bits = v_bits;
+    const cudaError_t e = tq::launch_pages(op, c, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+}  // namespace
+
+tq_status tq_pages_copy(const tq_paged_cache* src, const tq_paged_cache* dst, int n_layers, int Hkv, int d,
+                        int k_bits, int v_bits, const int32_t* src_ids, const int32_t* dst_ids, int64_t n,
+                        void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+    if (n < 0) return TQ_ERR_INVALID_ARG;
+    tq_status st = check_layers(src, n_layers, Hkv, d, k_bits, v_bits);
+    if (st == TQ_OK) st = check_layers(dst, n_layers, Hkv, d, k_bits, v_bits);
+    if (st != TQ_OK) return st;
+    if (src[0].page_size != dst[0].page_size || n > dst[0].n_pages) return TQ_ERR_INVALID_ARG;
+    // one pool, layer by layer, or two that share nothing
+    const bool same = src[0].k_packed == dst[0].k_packed;
+    for (int l = 0; l < n_layers; ++l) {
+        const tq_paged_cache &a = src[l], &b = dst[l];
+        if (same && (a.k_packed != b.k_packed || a.k_norm != b.k_norm || a.v_packed != b.v_packed ||
+                     a.v_norm != b.v_norm || a.n_pages != b.n_pages))
+            return TQ_ERR_INVALID_ARG;
+        if (!same)
+            for (int m = 0; m < n_layers; ++m)
+                for (int k = 0; k < 4; ++k)
+                    if (overlap(layer_span(a, k, Hkv, d, k_bits, v_bits), layer_span(dst[m], k, Hkv, d, k_bits, v_bits)))
+                        return TQ_ERR_INVALID_ARG;
+    }
+    if (n == 0) return TQ_OK;
+    if (!src_ids || !dst_ids) return TQ_ERR_INVALID_ARG;
+    if (!aligned4(src_ids) || !aligned4(dst_ids)) return TQ_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < tq::pages_workspace_bytes(0, dst[0].n_pages)) return TQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+    if (!device_accessible(src_ids) || !device_accessible(dst_ids) || !device_accessible(workspace) ||
+        !paged_accessible(src[0]) || !paged_accessible(dst[0]))
+        return TQ_ERR_INVALID_ARG;
+    tq::PagesCall c = {};
+    c.arg = src_ids;
+    c.arg2 = dst_ids;
+    c.ws = workspace;
+    c.n = n;
+    c.page_shift = page_shift_of(dst[0].page_size);
+    c.same = same ? 1 : 0;
+    c.src = src;
+    c.dst = dst;
+    c.n_layers = n_layers;
+    c.Hkv = Hkv;
+    c.d = d;
+    c.k_bits = k_bits;
+    c.v_bits = v_bits;
+    const cudaError_t e = tq::launch_pages(tq::kPagesCopy, c, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
+tq_status tq_pages_fork(tq_page_table in, const int32_t* parents, tq_page_table out, int n_seqs, int max_pages,
+                        const tq_paged_cache* layers, int n_layers, int Hkv, int d, int k_bits, int v_bits,
+                        int32_t* info, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+    return pages_call(tq::kPagesFork, in, out, parents, nullptr, n_seqs, max_pages, layers, n_layers, Hkv, d, k_bits,
+                      v_bits, info, workspace, workspace_bytes, stream);
+}
+
+tq_status tq_pages_resize(tq_page_table in, const int32_t* new_lens, tq_page_table out, int n_seqs, int max_pages,
+                          const tq_paged_cache* layers, int n_layers, int Hkv, int d, int k_bits, int v_bits,
+                          int32_t* info, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+    return pages_call(tq::kPagesResize, in, out, new_lens, nullptr, n_seqs, max_pages, layers, n_layers, Hkv, d,
+                      k_bits, v_bits, info, workspace, workspace_bytes, stream);
+}
+
+tq_status tq_pages_compact(tq_page_table in, tq_page_table out, int32_t* moved_to, int n_seqs, int max_pages,
+                           const tq_paged_cache* layers, int n_layers, int Hkv, int d, int k_bits, int v_bits,
+                           int32_t* info, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+    return pages_call(tq::kPagesCompact, in, out, nullptr, moved_to, n_seqs, max_pages, layers, n_layers, Hkv, d,
+                      k_bits, v_bits, info, workspace, workspace_bytes, stream);
+}
+
 size_t tq_attn_prefill_workspace_bytes(int B, int T, int Hq, int Hkv, int64_t cap, int d) {
     if (B < 0 || T < 1 || Hq <= 0 || Hkv <= 0 || cap < T || d != 128) return 0;
     return tq::attn_prefill_ws_bytes(B, Hkv, cap);

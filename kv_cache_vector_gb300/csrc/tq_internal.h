@@ -348,6 +348,25 @@ cudaError_t launch_append_paged_d(int k_bits, int v_bits, tq_dtype dt, const voi
                                   const PagedArgs& pa, const RowParams& PK, const RowParams& PV,
                                   cudaStream_t s);
 
+// Upkeep of the pages (tq_pages.cu): arguments checked by the caller.  src
+// and dst are the same layers except for the copy.
+enum { kPagesCopy = 0, kPagesFork = 1, kPagesResize = 2, kPagesCompact = 3 };
+struct PagesCall {
+    tq_page_table in, out;
+    const int32_t* arg;   // parents, new lengths, or source ids
+    const int32_t* arg2;  // destination ids
+    int32_t* moved;
+    int32_t* info;
+    void* ws;
+    int64_t n;
+    int n_seqs, max_pages, page_shift, same;
+    const tq_paged_cache* src;
+    const tq_paged_cache* dst;
+    int n_layers, Hkv, d, k_bits, v_bits;
+};
+size_t pages_workspace_bytes(int n_seqs, int64_t n_pages);
+cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s);
+
 // Shared launch helpers (tq_launch.cpp).
 int num_sms();
 int blocks_per_sm(const void* kernel, int block_threads, size_t dyn_smem);

@@ -1,0 +1,156 @@
+"""The sequential restatement of the page operators keeps a page table sound:
+random sequences of fork, resize and compaction, with each row's positions
+holding values of their own, checked against plain Python lists of what every
+row has written.  And the entry points' refusals, which come before any launch."""
+import ctypes
+import random
+
+import numpy as np
+import pytest
+
+from kv_cache_vector_gb300 import abi
+from oracle import pages as OP
+
+
+def _apply(pool, pairs):
+    """Copies of a call read the pages as they were before it."""
+    new = pool.copy()
+    for s, t in pairs:
+        new[t] = pool[s]
+    return new
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_books_stay_sound(seed):
+    rng = random.Random(seed)
+    page, n, max_pages, n_pages = 32, 7, 6, 40
+    table = np.full((n, max_pages), -1, np.int32)
+    lens, refs = np.zeros(n, np.int32), np.zeros(n_pages, np.int32)
+    pool = np.zeros((n_pages, page), np.int64)
+    rows, stamp = [[] for _ in range(n)], 0
+    for _ in range(150):
+        op = rng.choice(("fork", "resize", "resize", "compact"))
+        if op == "fork":
+            parents = np.array([rng.choice((i, i, rng.randrange(-1, n))) for i in range(n)], np.int32)
+            t, l, r, pairs, info = OP.fork(table, lens, refs, parents, page)
+            if info[1] == 0:
+                rows = [list(rows[p]) if p >= 0 else [] for p in parents]
+        elif op == "resize":
+            to = np.array([rng.choice((-1, 0, rng.randrange(0, max_pages * page + 1),
+                                       min(max_pages * page, int(k) + rng.randrange(20)))) for k in lens], np.int32)
+            t, l, r, pairs, info = OP.resize(table, lens, refs, to, page)
+        else:
+            t, l, r, pairs, _, info = OP.compact(table, lens, refs, page)
+        assert info[1] >= 0
+        pool = _apply(pool, pairs)
+        if op == "resize" and info[1] == 0:  # the rows write their new positions
+            for i in range(n):
+                rows[i] = rows[i][:l[i]]
+                for p in range(len(rows[i]), l[i]):
+                    stamp += 1
+                    rows[i].append(stamp)
+                    pool[t[i, p // page], p % page] = stamp
+        table, lens, refs = t, l, r
+        count = np.zeros(n_pages, np.int32)
+        for i in range(n):
+            used = -(-int(lens[i]) // page)
+            assert (table[i, used:] == -1).all()
+            for e in table[i, :used]:
+                count[e] += 1
+            assert [pool[table[i, p // page], p % page] for p in range(lens[i])] == rows[i]
+        assert np.array_equal(count, refs)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from kv_cache_vector_gb300 import build
+    build.build()
+    return abi.lib()
+
+
+def _cache(at=1 << 32, n_pages=4, page_size=64):
+    return abi.PagedCacheView(at, at + (1 << 24), at + (2 << 24), at + (3 << 24), n_pages, page_size)
+
+
+def _layers(*caches):
+    return (abi.PagedCacheView * len(caches))(*caches)
+
+
+def test_refusals_of_the_books(L):
+    A, W = 1 << 20, 1 << 28
+    tab = lambda a, t=None: abi.PageTableView(a, a + 4096, a + 8192 if t is None else t)  # noqa: E731
+    a, b, arg, info = tab(A), tab(A + (1 << 16)), A + (1 << 18), A + (1 << 19)
+    ly = _layers(_cache())
+    need = L.tq_pages_workspace_bytes(4, 8, 4)
+    assert need >= 4 * (5 * 4 + 3 * 4)
+    assert L.tq_pages_workspace_bytes(-1, 8, 4) == 0
+    assert L.tq_pages_workspace_bytes(4, 8, 0) == 0
+    assert L.tq_pages_workspace_bytes(4, 8, 1 << 31) == 0
+
+    def fork(i=a, p=arg, o=b, n=4, mp=8, layers=ly, nl=1, hkv=2, d=128, kb=4, vb=3, inf=info, ws=W, size=need):
+        return L.tq_pages_fork(i, p, o, n, mp, layers, nl, hkv, d, kb, vb, inf, ws, size, None)
+
+    assert fork(n=0) == 1
+    assert fork(mp=0) == 1
+    assert fork(layers=None) == 1
+    assert fork(nl=0) == 1
+    assert fork(hkv=0) == 1
+    assert fork(d=96) == 2
+    assert fork(d=16) == 2
+    assert fork(kb=5) == 2
+    assert fork(vb=1) == 2
+    assert fork(layers=_layers(_cache(page_size=48))) == 2
+    assert fork(layers=_layers(_cache(page_size=16))) == 2
+    assert fork(mp=1 << 26) == 2                                   # lengths past int32
+    assert fork(layers=_layers(_cache(n_pages=0))) == 1
+    assert fork(layers=_layers(_cache(n_pages=1 << 31))) == 1
+    assert fork(layers=_layers(_cache(), _cache(1 << 36, 5)), nl=2) == 1    # another geometry
+    assert fork(layers=_layers(abi.PagedCacheView(1 << 32, (1 << 33) + 4, 1 << 34, 1 << 35, 4, 64))) == 3
+    assert fork(p=None) == 1
+    assert fork(inf=None) == 1
+    assert fork(i=abi.PageTableView(A, None, A + 8192)) == 1
+    assert fork(p=arg + 2) == 3
+    assert fork(ws=None) == 5
+    assert fork(size=need - 1) == 5
+    assert fork(ws=W + 4) == 3
+    assert fork(o=a) == 1                                          # rows exchange places: not in place
+    assert fork(o=tab(A, A + (1 << 17))) == 1                      # partly the input
+    assert fork(inf=A + 4) == 1                                    # info inside the table
+    assert fork(p=A + (1 << 16) + 4) == 1                          # parents inside the output
+    resize = lambda o: L.tq_pages_resize(a, arg, o, 4, 8, ly, 1, 2, 128, 4, 3, info, W, need, None)  # noqa: E731
+    assert resize(tab(A + 4)) == 1                                 # neither in place nor apart
+    assert L.tq_pages_resize(a, None, b, 4, 8, ly, 1, 2, 128, 4, 3, info, W, need, None) == 1
+    assert L.tq_pages_compact(a, b, None, 4, 8, ly, 1, 2, 128, 4, 3, info, W, need, None) == 1
+    assert L.tq_pages_compact(a, b, A + 8192, 4, 8, ly, 1, 2, 128, 4, 3, info, W, need, None) == 1  # moved_to on refs
+
+
+def test_refusals_of_the_copy(L):
+    ids, W = 1 << 20, 1 << 28
+    one, two = _layers(_cache()), _layers(_cache(1 << 36))
+    need = L.tq_pages_workspace_bytes(0, 0, 4)
+
+    def copy(s=one, t=two, nl=1, hkv=2, d=128, kb=4, vb=3, si=ids, ti=ids + 4096, n=2, ws=W, size=need):
+        return L.tq_pages_copy(s, t, nl, hkv, d, kb, vb, si, ti, n, ws, size, None)
+
+    assert copy(n=0) == 0 and copy(n=0, si=None, ti=None, ws=None) == 0   # nothing to copy
+    assert copy(n=-1) == 1
+    assert copy(n=5) == 1                                                  # more than the pool has
+    assert copy(s=None) == 1 and copy(t=None) == 1
+    assert copy(t=_layers(_cache(1 << 36, 4, 128))) == 1                   # another page size
+    assert copy(t=_layers(_cache((1 << 32) + 4096))) == 1                  # overlapping pools
+    assert copy(s=_layers(_cache(), _cache(1 << 36)), t=_layers(_cache(1 << 36), _cache(1 << 40)), nl=2) == 1
+    assert copy(s=_layers(_cache(), _cache(1 << 36)), t=_layers(_cache(), _cache(1 << 40)), nl=2) == 1
+    assert copy(d=48) == 2 and copy(kb=1) == 2
+    assert copy(si=None) == 1 and copy(ti=ids + 2) == 3
+    assert copy(ws=None) == 5 and copy(size=need - 1) == 5 and copy(ws=W + 8) == 3
+
+
+def test_python_layer_refusals():
+    import torch
+    z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt)  # noqa: E731
+    with pytest.raises(ValueError):
+        abi.PagedLayers([])
+    with pytest.raises(ValueError):  # host tensors
+        abi.PagedLayers(abi.PagedCache(z(4, 2, 32, 64), z(4, 2, 32, dt=torch.float32), z(4, 2, 32, 48),
+                                       z(4, 2, 32, dt=torch.float32), 4, 3))
+    assert ctypes.sizeof(abi.PageTableView) == 24
