@@ -325,6 +325,40 @@ tq_status tq_attn_decode_append_paged(const tq_plan *plan, const void *q, const 
                                       float scale, float sparse_v_threshold, float *out, void *workspace,
                                       size_t workspace_bytes, tq_stream_t stream);
 
+/* Workspace bytes tq_attn_prefill_paged needs on the current device (parts of
+ * items that are split over SMs; no length enters); 0 for invalid sizes. */
+size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
+
+/* Attention of several query tokens per sequence over a paged cache: prompt
+ * chunks, drafted tokens to be checked, and single tokens, ragged in one batch
+ * ("TurboQuant KV Cache Compression -- Spec", fa_tq_attention_cached;
+ * Optimization: Fused dequant-dot).  Sequence b's n_b = cu_q[b + 1] - cu_q[b]
+ * query tokens are the last n_b of its ctx_lens[b] positions (their K and V
+ * rows are in the cache already): token t sits at p = ctx_lens[b] - n_b + t
+ * and attends over positions max(0, p - window + 1) .. p (window 0: 0 .. p).
+ * A token with p < 0 attends to nothing and gets a zero row.
+ *   q:   [n_q][Hq][d] bf16, device;  out: [n_q][Hq][d] out_dtype, device
+ *   cu_q: [B + 1] int32, device, ascending from cu_q[0] >= 0 to cu_q[B] <= n_q;
+ *     rows outside every sequence are not read and not written
+ *   ctx_lens: [B] int32, device, at most max_pages * page_size
+ *   block_table: [B][max_pages] int32, device
+ * d in {32, 64, 128, 256}, Hq / Hkv up to 128.  Both products run on the
+ * tensor cores with fp16 operands and fp32 sums; norms up to 2^100.  Positions
+ * past a row's range do not reach it, whatever their rows hold.
+ * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
+ * rows are not written) and sets the device status word to 71.  A page id
+ * outside [0, n_pages) is not read: its positions count as rows of norm 0 and
+ * the device status word is set to 72.  73: a bounded wait gave up.
+ * workspace: tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte
+ * aligned like q, out and every array of the cache.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (also max_pages * page_size
+ * above 2^30), TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
+tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
+                                tq_paged_cache cache, const int32_t *block_table, int max_pages,
+                                const int32_t *cu_q, const int32_t *ctx_lens, int window, int k_bits,
+                                int v_bits, float scale, void *out, tq_dtype out_dtype, void *workspace,
+                                size_t workspace_bytes, tq_stream_t stream);
+
 /* ---------------------------------------------------- upkeep of the pages
  * The pages of a paged cache as a serving loop keeps them: which sequence row
  * holds which pages, branches that share pages, growth, ends, and closing up

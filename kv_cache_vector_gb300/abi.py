@@ -31,6 +31,7 @@ EXPORTS = ("tq_codebook_init", "tq_plan_create", "tq_plan_destroy", "tq_plan_sig
            "tq_attn_decode_append_paged", "tq_plan_create_ex", "tq_plan_signs2", "tq_codebook_init_gaussian",
            "tq_attn_prefill_workspace_bytes", "tq_attn_prefill", "tq_qjl_matrix", "tq_encode_qjl",
            "tq_decode_qjl", "tq_attn_qjl_workspace_bytes", "tq_attn_decode_qjl",
+           "tq_attn_prefill_paged_workspace_bytes", "tq_attn_prefill_paged",
            "tq_pages_workspace_bytes", "tq_pages_copy", "tq_pages_fork", "tq_pages_resize", "tq_pages_compact")
 
 
@@ -102,6 +103,9 @@ def lib() -> ctypes.CDLL:
         ("tq_attn_prefill_workspace_bytes", ctypes.c_size_t, [i32, i32, i32, i32, i64, i32]),
         ("tq_attn_prefill", i32, [vp, vp, i32, i32, i32, i32, CacheView, vp, i32, i32, f32, vp, vp,
                                   ctypes.c_size_t, vp]),
+        ("tq_attn_prefill_paged_workspace_bytes", ctypes.c_size_t, [i32, i32, i32]),
+        ("tq_attn_prefill_paged", i32, [vp, vp, i64, i32, i32, i32, PagedCacheView, vp, i32, vp, vp, i32, i32, i32,
+                                        f32, vp, i32, vp, ctypes.c_size_t, vp]),
         ("tq_pages_workspace_bytes", ctypes.c_size_t, [i32, i32, i64]),
         ("tq_pages_copy", i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp, ctypes.c_size_t, vp]),
         ("tq_pages_fork", i32, [PageTableView, vp, PageTableView, i32, i32, vp, i32, i32, i32, i32, i32, vp, vp,
@@ -479,6 +483,48 @@ def tq_attn_prefill(plan: Plan, q: torch.Tensor, cache: Cache, q_start: torch.Te
         plan.handle, q.contiguous().data_ptr(), B, T, Hq, Hkv, cache.view(), q_start.data_ptr(), cache.k_bits,
         cache.v_bits, ctypes.c_float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _stream(q)))
+    return out
+
+
+def tq_attn_prefill_paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d))
+
+
+def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache: PagedCache,
+                          block_table: torch.Tensor, ctx_lens: torch.Tensor, scale: float, window: int = 0,
+                          out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """q: [n_q, Hq, d] bf16, the query tokens of all sequences one after the
+    other; cu_q [B + 1] int32: sequence b's are rows cu_q[b] .. cu_q[b + 1] - 1
+    and sit at the end of its ctx_lens[b] positions, each attending causally
+    (over the last `window` positions, 0: all) -> out [n_q, Hq, d] bf16 or
+    fp32.  Rows outside every sequence keep what `out` held (zeros if none is
+    passed)."""
+    n_q, Hq, d = q.shape
+    B = ctx_lens.numel()
+    if d != plan.d or cache.k_packed.shape[-1] * 8 != d * cache.k_bits:
+        raise ValueError("q and cache must have the plan's head dimension")
+    if cu_q.numel() != B + 1 or block_table.shape[0] != B:
+        raise ValueError("cu_q [B + 1], ctx_lens [B] and block_table [B, max_pages] expected")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16")
+    _cuda(q)
+    _i32(cu_q, "cu_q")
+    _i32(block_table, "block_table")
+    _i32(ctx_lens, "ctx_lens")
+    _same_device(q.device, cu_q, block_table, ctx_lens, cache.k_norm)
+    with _on(q.device):
+        if out is None:
+            out = torch.zeros(n_q, Hq, d, dtype=out_dtype, device=q.device)
+        _cuda(out)
+        _same_device(q.device, out)
+        if out.shape != q.shape:
+            raise ValueError("out must be [n_q, Hq, d]")
+        ws = _scratch(workspace, tq_attn_prefill_paged_workspace_bytes(Hq, cache.Hkv, d), q.device)
+        _check("tq_attn_prefill_paged", lib().tq_attn_prefill_paged(
+            plan.handle, q.data_ptr(), n_q, B, Hq, cache.Hkv, cache.view(), block_table.data_ptr(),
+            block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), window, cache.k_bits, cache.v_bits,
+            scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(q)))
     return out
 
 

@@ -28,7 +28,8 @@ UNITS = ([("tq_api.cpp", {}), ("tq_launch.cu", {}), ("tq_noalloc.cu", {}), ("tq_
          + [("tq_attn.cu", {"D": 128, "KB": kb}) for kb in (2, 3, 4)]
          + [("tq_attn_generic.cu", {"D": d, "KB": kb}) for d in ATTN_DIMS for kb in (2, 3, 4)]
          + [("tq_prefill.cu", {"KB": kb}) for kb in (2, 3, 4)]
-         + [("tq_qjl.cu", {"D": d}) for d in (32, 64, 128)])
+         + [("tq_qjl.cu", {"D": d}) for d in (32, 64, 128)]
+         + [("tq_prefill_paged.cu", {"D": d}) for d in ATTN_DIMS])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -8,6 +8,8 @@
 #include <new>
 #include <type_traits>
 
+#include <cuda_fp16.h>
+
 #include "tq_internal.h"
 
 namespace {
@@ -1045,6 +1047,82 @@ tq_status tq_pages_compact(tq_page_table in, tq_page_table out, int32_t* moved_t
                            int32_t* info, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
     return pages_call(tq::kPagesCompact, in, out, nullptr, moved_to, n_seqs, max_pages, layers, n_layers, Hkv, d,
                       k_bits, v_bits, info, workspace, workspace_bytes, stream);
+}
+
+size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d) {
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 32 && d != 64 && d != 128 && d != 256)) return 0;
+    return tq::prefill_paged_ws_bytes(d, tq::num_sms());
+}
+
+namespace {
+// The levels c * s as fp16 bytes for the byte-permute lookups; s is the
+// plan's scale where it has one (then every c * s is close to an fp16 value).
+void level_bytes(const tq::Plan& P, int bits, uint32_t* w) {
+    const double s = P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0;
+    const int first = bits == 4 ? 8 : 0, n = bits == 2 ? 4 : 8;
+    for (int i = 0; i < 8; ++i) w[i] = 0u;
+    for (int i = 0; i < n; ++i) {
+        const uint32_t h = __half_as_ushort(__float2half_rn((float)((double)P.c32[bits][first + i] * s)));
+        w[i >> 2] |= (h >> 8) << (8 * (i & 3));
+        w[4 + (i >> 2)] |= (h & 0xFFu) << (8 * (i & 3));
+    }
+}
+}  // namespace
+
+tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
+                                tq_paged_cache cache, const int32_t* block_table, int max_pages,
+                                const int32_t* cu_q, const int32_t* ctx_lens, int window, int k_bits, int v_bits,
+                                float scale, void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                tq_stream_t stream) {
+    if (!plan || B < 0 || n_q < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_pages < 1 || cache.n_pages < 1 ||
+        window < 0 || !std::isfinite(scale))
+        return TQ_ERR_INVALID_ARG;
+    const tq::Plan* P = reinterpret_cast<const tq::Plan*>(plan);
+    const int shift = page_shift_of(cache.page_size);
+    if (!valid_bits(k_bits) || !valid_bits(v_bits) || !valid_dtype(out_dtype) || shift < 0 ||
+        (P->d != 32 && P->d != 64 && P->d != 128 && P->d != 256) || Hq / Hkv > 128)
+        return TQ_ERR_UNSUPPORTED;
+    // positions, rows of a KV head and page ids are 32-bit numbers
+    if (((int64_t)max_pages << shift) > (int64_t(1) << 30) || n_q > INT32_MAX / (Hq / Hkv) - 256 ||
+        cache.n_pages > INT32_MAX || B > (1 << 20))
+        return TQ_ERR_UNSUPPORTED;
+    if (B == 0 || n_q == 0) return TQ_OK;
+    if (!q || !out || !block_table || !cu_q || !ctx_lens || !paged_pointers_ok(cache)) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(block_table) || !aligned4(cu_q) || !aligned4(ctx_lens) ||
+        !paged_aligned(cache) || !aligned16(cache.k_norm) || !aligned16(cache.v_norm))
+        return TQ_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < tq::prefill_paged_ws_bytes(P->d, tq::num_sms())) return TQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+    if (!device_accessible(q) || !device_accessible(out) || !device_accessible(block_table) ||
+        !device_accessible(cu_q) || !device_accessible(ctx_lens) || !device_accessible(workspace) ||
+        !paged_accessible(cache))
+        return TQ_ERR_INVALID_ARG;
+    tq::AttnParams A;
+    tq::fill_attn_params(*P, k_bits, v_bits, scale, 0.0f, A);
+    tq::PagedPrefillCall c = {};
+    c.q = q;
+    c.out = out;
+    c.cu_q = cu_q;
+    c.ctx_lens = ctx_lens;
+    c.block_table = block_table;
+    c.cache = cache;
+    c.workspace = workspace;
+    c.n_q = n_q;
+    c.B = B;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.max_pages = max_pages;
+    c.page_shift = shift;
+    c.window = window;
+    c.k_bits = k_bits;
+    c.v_bits = v_bits;
+    c.out_bf16 = out_dtype == TQ_BF16;
+    level_bytes(*P, k_bits, c.k_levels);
+    level_bytes(*P, v_bits, c.v_levels);
+    const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
+        return tq::launch_prefill_paged<decltype(D)::value>(c, A, reinterpret_cast<cudaStream_t>(stream));
+    });
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
 size_t tq_attn_prefill_workspace_bytes(int B, int T, int Hq, int Hkv, int64_t cap, int d) {

@@ -341,6 +341,36 @@ cudaError_t launch_attn_prefill(int v_bits, const void* q, int B, int T, int Hq,
 cudaError_t launch_prefill_attention(const void* q, int B, int T, int Hq, int Hkv, const int32_t* q_start,
                                      const tq_cache_view& cache, float* out, void* workspace,
                                      const AttnParams& P, cudaStream_t s);
+// Attention of several query tokens per sequence over the paged cache
+// (tq_prefill_paged.cu, one unit per head dimension).  The work is cut into
+// one share per SM; a share leaves at most two parts of items in the
+// workspace: per part the output sums [d / 4][kRows] (float4), then the rows'
+// maxima, sums and exponents; after the parts 8 words per share.
+template <int D>
+struct PagedPrefillGeo {
+    static constexpr int kRows = D == 256 ? 128 : 256;  // query rows of an item
+    static constexpr int64_t kPartFloats = (int64_t)(D + 3) * kRows;
+};
+inline size_t prefill_paged_ws_bytes(int d, int sms) {
+    return (size_t)sms * (2 * (size_t)(d + 3) * (d == 256 ? 128 : 256) * 4 + 32);
+}
+struct PagedPrefillCall {
+    const void* q;
+    void* out;
+    const int32_t* cu_q;
+    const int32_t* ctx_lens;
+    const int32_t* block_table;
+    tq_paged_cache cache;
+    void* workspace;
+    int64_t n_q;
+    int B, Hq, Hkv, max_pages, page_shift, window, k_bits, v_bits, out_bf16;
+    // the levels as fp16 bytes: high bytes of eight levels in words 0 and 1,
+    // their low bytes in words 4 and 5 (4 bits: the eight positive ones)
+    uint32_t k_levels[8], v_levels[8];
+};
+template <int D>
+cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P, cudaStream_t s);
+
 // Paged append of one token per sequence, d >= 32 (tq_codec.cu).
 template <int D>
 cudaError_t launch_append_paged_d(int k_bits, int v_bits, tq_dtype dt, const void* k_new,

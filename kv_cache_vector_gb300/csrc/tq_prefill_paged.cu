@@ -1,0 +1,1257 @@
+// tq_prefill_paged.cu -- attention of several query tokens per sequence over
+// the paged packed cache, ragged chunks, on the 5th-generation tensor cores.
+//
+// Sequence b has n_b query tokens (rows cu_q[b] .. cu_q[b + 1] - 1 of q), the
+// last n_b of its ctx_b positions; token t sits at p = ctx_b - n_b + t and
+// attends over positions max(0, p - window + 1) .. p:
+//   out = R^-1 ( sum_j p_j n^v_j c[v_j] ),  p = softmax_j( scale n^k_j <R q, c[k_j]> )
+// with R the codec's rotation, c the codebook's levels and n the rows' norms.
+//
+// The packed rows are expanded inside the kernel, straight from the pages
+// into the shared-memory tiles that the tensor cores read: no expanded copy of
+// the cache passes through memory.  A CTA's query tile is 256 rows (tokens
+// times the query heads of one KV head; 128 at d = 256), so that one expansion
+// serves two MMA row tiles.
+//
+//   warps 0-7    softmax, one thread per query row (4 warps at d = 256)
+//   8 warps      expansion: bytes -> fp16 levels times the row's norm
+//   1 warp       MMAs (one thread)
+//   1 warp       copies of packed rows and norms from the pages (bulk copies)
+//
+// The work is cut into equal shares, one per SM, along a line of all (query
+// tile, KV head, block of positions) units: a share may end inside an item.
+// The two (or more) parts of such an item go to the workspace and
+// k_prefill_paged_join adds them up in order.  All lengths are read on the
+// device: the launch is the same for every batch.
+//
+// Two streams of steps keep the tensor cores and the softmax warps busy at
+// once (d <= 128): with more than 128 query rows, stream g takes row tile g
+// and both take every block; with at most 128 rows, the streams take the
+// blocks in turn for the same rows and are merged at the end.  At d = 256 the
+// output fills tensor memory: one stream, with two score buffers.
+//
+// Numbers.  fp16 operands, fp32 sums.  A block's K rows are scaled by a power
+// of two 2^-Ek (its largest norm is below 2^Ek), its V rows by 2^-Ev; Ek goes
+// into the factor of the scores, Ev into the exponent of the probabilities,
+//   P' = 2^(s + Ev - M),  M a running maximum of s + Ev,
+// so that O = sum P' V' keeps its precision however the norms vary from block
+// to block, and the denominator sums P' 2^(Eb - Ev) in fp32 (Eb: Ev of the
+// first block).  M moves only when it grows by more than 8, so P' < 2^8.
+// Each operand is rounded to fp16 once after its fp32 (query, P) or fp16
+// (level times norm) value: 2^-11 relative steps, an eighth of the bf16
+// output's.  A non-finite norm makes the scores of its row NaN (only rows
+// that attend to it see them) and its V row zero.
+//
+// Every wait on an mbarrier is bounded (2 s); one that gives up sets the
+// device status word and a flag that ends the others.  The softmax warps go
+// on through their (then failing) waits so that their barriers stay paired;
+// no output is written after the flag.
+#include <cfloat>
+
+#include "tq_async.cuh"
+#include "tq_device.cuh"
+#include "tq_tmem.cuh"
+#include "tq_umma.cuh"
+
+#if !defined(TQ_UNIT_D)
+#error "compile once per head dimension with -DTQ_UNIT_D=<d>"
+#endif
+
+namespace tq {
+namespace dev {
+
+constexpr int kPpStatusRange = 71;  // cu_q or ctx_lens outside their ranges
+constexpr int kPpStatusPage = 72;   // a page id outside [0, n_pages)
+constexpr int kPpStatusWait = 73;   // a wait gave up
+constexpr int kPpStatusAlign = 74;  // shared memory not 1024-byte aligned
+
+// Sizes for head dimension D.
+template <int D>
+struct PpGeo {
+    static constexpr int kD = D < 64 ? 64 : D;        // tile width: d = 32 is padded with zeros
+    static constexpr int kN = D == 256 ? 64 : 128;    // positions per block
+    static constexpr int kRows = PagedPrefillGeo<D>::kRows;
+    static constexpr int kStreams = D == 256 ? 1 : 2;
+    static constexpr int kSoftWarps = 4 * kStreams;
+    static constexpr int kWarps = kSoftWarps + 10;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kStages = D <= 64 ? 4 : 2;   // staged packed blocks
+    static constexpr uint32_t kTile = kN * kD * 2;    // an expanded K or V tile
+    static constexpr uint32_t kQTile = 128 * kD * 2;
+    static constexpr uint32_t kStage = kN * D + 8 * kN;  // 4-bit K and V rows, norms
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kRing = kQ + kStreams * kQTile;  // 4 tiles: K, V of two blocks
+    static constexpr uint32_t kStg = kRing + 4 * kTile;
+    static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [4] float2: 2^Ek, Ev
+    static constexpr uint32_t kSegs = kMeta + 32;               // [kStages] segments staged
+    static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
+    static constexpr uint32_t kRedBytes = 18 * 8 + 16;
+    static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
+    static constexpr uint32_t kBar = kCur + 64;
+    static constexpr int kBars = 2 * kStages + 4 + 4 + 4 + 2 + 2 + 2 + 1 + 1;
+    static constexpr uint32_t kMisc = kBar + 8 * kBars;  // tensor-memory base, abort flag
+    static constexpr uint32_t kSmem = (kMisc + 8 + 127) / 128 * 128;
+    static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // buffer b at kN b; output g at 128 g further
+};
+
+struct PpArgs {
+    const __nv_bfloat16* q;
+    void* out;
+    const int32_t* cu;
+    const int32_t* ctx;
+    const int32_t* bt;
+    tq_paged_cache c;
+    float* part;   // [shares][2] parts
+    int32_t* meta;  // [shares][kPpMeta]
+    int64_t n_q;
+    int B, Hq, Hkv, max_pages, shift, window, k_bits, v_bits, out_bf16;
+    uint32_t khi[4], klo[4], vhi[4], vlo[4];  // level bytes (see expand)
+};
+enum { kMetaOwner = 0, kMetaB, kMetaI, kMetaH, kMetaLast, kMetaHas0, kMetaHas1, kPpMeta = 8 };
+
+// Where a share starts or goes on: sequence, row tile, KV head, and the units
+// of the item that belong to earlier shares.
+struct PpCursor {
+    int b, i, h;
+    int64_t off;
+    int64_t left;  // units of this share from here on
+};
+
+// Weights and ranges of sequence b's items.  A unit line position is only an
+// estimate of cost: any consistent weight gives a correct cut.
+template <int D>
+struct PpSeq {
+    using Z = PpGeo<D>;
+    int n, ctx, tiles, rows;
+    int64_t base, cap, kstar, over;
+    int G;
+
+    __device__ void load(const PpArgs& A, int b, int* status) {
+        G = A.Hq / A.Hkv;
+        const int64_t c0 = __ldg(A.cu + b), c1 = __ldg(A.cu + b + 1);
+        ctx = __ldg(A.ctx + b);
+        if (c0 < 0 || c1 < c0 || c1 > A.n_q || ctx < 0 || ctx > ((int64_t)A.max_pages << A.shift) ||
+            (c1 - c0) * G > INT32_MAX) {
+            if (status) report_timeout(status, kPpStatusRange);
+            n = ctx = 0;
+        } else {
+            n = (int)(c1 - c0);
+        }
+        rows = n * G;
+        tiles = (rows + Z::kRows - 1) / Z::kRows;
+        base = ctx > n ? (int64_t)(ctx - n) * G : 0;
+        cap = A.window > 0 ? (int64_t)A.window * G + Z::kRows : INT64_MAX;
+        // tiles before the window's cap binds: base + (k + 1) kRows < cap
+        kstar = cap == INT64_MAX ? INT32_MAX : (cap - base - 1) / Z::kRows;
+        if (cap - base - 1 < 0) kstar = 0;
+        over = 2 * (int64_t)Z::kN * G;
+    }
+    __device__ int factor(int i) const {
+        return Z::kStreams == 2 && rows - (int64_t)i * Z::kRows > 128 ? 2 : 1;
+    }
+    __device__ int64_t weight(int i) const {
+        int64_t e = base + min((int64_t)(i + 1) * Z::kRows, (int64_t)rows);
+        return factor(i) * min(e, cap) + over;
+    }
+    // sum of the weights of tiles 0 .. i - 1
+    __device__ int64_t before(int i) const {
+        if (i <= 0) return 0;
+        if (i == tiles) return before(i - 1) + weight(i - 1);
+        const int64_t m = min((int64_t)i, kstar);
+        int64_t s = m * base + (int64_t)Z::kRows * (m * (m + 1) / 2);
+        if (i > m) s += (i - m) * cap;
+        return Z::kStreams * s + i * over;
+    }
+};
+
+// One part of an item: blocks [blk0, blk1) of the item's nblk, its first
+// position and the share's bookkeeping.
+struct PpPart {
+    int b, i, h;
+    int row0, rows;      // first row within (sequence, KV head); valid rows
+    int lo_blk;          // first block of the item
+    int blk0, blk1, nblk;
+    int kv_end;
+    int pair;            // the two streams take two row tiles
+    bool head, whole;    // part starts the item; covers it
+};
+
+__device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w) {
+    return off >= w ? nblk : (int)((int64_t)nblk * off / w);
+}
+
+// Blocks of row tile i, the first of them, and the end of its positions.
+template <int D>
+__device__ __forceinline__ int pp_blocks(const PpArgs& A, const PpSeq<D>& q, int i, int* lo_blk = nullptr,
+                                         int* kv_end = nullptr) {
+    using Z = PpGeo<D>;
+    const int row0 = i * Z::kRows, rows = min(Z::kRows, q.rows - row0);
+    const int first_pos = q.ctx - q.n + row0 / q.G;
+    const int end = max(0, q.ctx - q.n + (row0 + rows - 1) / q.G + 1);
+    const int lo = (A.window > 0 ? max(0, first_pos - A.window + 1) : 0) / Z::kN;
+    if (lo_blk) *lo_blk = lo;
+    if (kv_end) *kv_end = end;
+    return max(0, (end + Z::kN - 1) / Z::kN - lo);
+}
+
+// The share's next part with work in it; advances the cursor.  False at the
+// end of the share.  Items without blocks (no position to attend to) come as
+// a whole part with blk0 == blk1, to the share that holds their start.
+template <int D>
+__device__ bool pp_next(const PpArgs& A, PpCursor& c, PpSeq<D>& q, PpPart& p) {
+    using Z = PpGeo<D>;
+    while (c.left > 0) {
+        while (c.i >= q.tiles) {  // next sequence with rows
+            if (++c.b >= A.B) {
+                c.left = 0;
+                return false;
+            }
+            q.load(A, c.b, nullptr);
+            c.i = 0;
+            c.h = 0;
+        }
+        const int64_t w = q.weight(c.i);
+        const int64_t end = min(w, c.off + c.left);
+        p.b = c.b;
+        p.i = c.i;
+        p.h = c.h;
+        p.row0 = c.i * Z::kRows;
+        p.rows = min(Z::kRows, q.rows - p.row0);
+        p.pair = Z::kStreams == 2 && p.rows > 128;
+        p.nblk = pp_blocks<D>(A, q, c.i, &p.lo_blk, &p.kv_end);
+        p.blk0 = pp_cut(p.nblk, c.off, w);
+        p.blk1 = pp_cut(p.nblk, end, w);
+        p.head = c.off == 0;
+        p.whole = p.nblk == 0 ? p.head : (p.blk0 == 0 && p.blk1 == p.nblk);
+        c.left -= end - c.off;
+        c.off = end;
+        if (c.off >= w) {  // on to the next item
+            c.off = 0;
+            if (++c.h >= A.Hkv) {
+                c.h = 0;
+                ++c.i;
+            }
+        }
+        if (p.whole || p.blk1 > p.blk0) return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ uint32_t pp_chunk(uint32_t half_bytes, int row, int k8) {
+    return (uint32_t)(k8 >> 3) * half_bytes + (uint32_t)row * 128 + (((k8 & 7) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ float pp_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ float pp_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bounded wait; gives up at once when the CTA's abort flag is set.
+__device__ __forceinline__ bool pp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_f, int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_f) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort_f = 1;
+            report_timeout(status, kPpStatusWait);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory descriptor of the V tile as an N-major B operand (N = dims):
+// 128-byte swizzle, 64-dim columns `lbo` bytes apart (leading offset), groups
+// of 8 positions 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kIdescBTransposed = 1u << 16;
+
+// ------------------------------------------------------------------ expansion
+
+// Four fp16 levels from four 4-bit selectors (nibbles of sel's low half) and
+// the level bytes: two byte permutes pick the high and the low bytes, two
+// interleave them.  4-bit indices: hi/lo hold the 8 positive levels; x has a 1
+// in the nibble of every positive index, and the sign byte is permuted from
+// it.  Narrower indices: hi/lo hold all levels with their signs.
+template <int BITS>
+__device__ __forceinline__ void pp_levels4(uint32_t sel, uint32_t x, const uint32_t* hi, const uint32_t* lo,
+                                           uint32_t& p01, uint32_t& p23) {
+    uint32_t h = __byte_perm(hi[0], hi[1], sel);
+    const uint32_t l = __byte_perm(lo[0], lo[1], sel);
+    if constexpr (BITS == 4) h ^= __byte_perm(0x00000080u, 0u, x);
+    p01 = __byte_perm(l, h, 0x5140);
+    p23 = __byte_perm(l, h, 0x7362);
+}
+
+// 32 indices (BITS words) -> 32 fp16 values times r, four 16-byte chunks at
+// k8 = 4 quarter .. + 3 of the tile row.
+template <int BITS>
+__device__ __forceinline__ void pp_expand32(const uint32_t* w, __half2 r, const uint32_t* hi, const uint32_t* lo,
+                                            unsigned char* tile, uint32_t half_bytes, int row, int quarter) {
+    unsigned char* base = tile + (uint32_t)(quarter >> 1) * half_bytes + (uint32_t)row * 128;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t sel, x = 0;
+        if constexpr (BITS == 4) {
+            // an index with its top bit set is positive level (index - 8), one
+            // without is the negative of level 7 - index
+            const uint32_t t = w[c] & 0x88888888u;
+            x = t >> 3;
+            sel = (w[c] ^ ~(t - x)) & 0x77777777u;
+        } else if constexpr (BITS == 3) {
+            const int bit = 24 * c;
+            const uint32_t f = bit % 32 == 0 ? w[bit / 32]
+                                             : __funnelshift_r(w[bit / 32], bit / 32 + 1 < 3 ? w[bit / 32 + 1] : 0u, bit % 32);
+            sel = (f & 0xFFFu) | ((f << 4) & 0x0FFF0000u);
+            sel = (sel & 0x003F003Fu) | ((sel << 2) & 0x3F003F00u);
+            sel = (sel & 0x07070707u) | ((sel << 1) & 0x70707070u);
+        } else {
+            const uint32_t f = w[c >> 1] >> (16 * (c & 1));
+            sel = (f & 0xFFu) | ((f << 8) & 0x00FF0000u);
+            sel = (sel & 0x000F000Fu) | ((sel << 4) & 0x0F000F00u);
+            sel = (sel & 0x03030303u) | ((sel << 2) & 0x30303030u);
+        }
+        uint32_t v[4];
+        pp_levels4<BITS>(sel, x, hi, lo, v[0], v[1]);
+        pp_levels4<BITS>(sel >> 16, x >> 16, hi, lo, v[2], v[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[k]), r);
+            v[k] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        const int k8 = 4 * (quarter & 1) + c;
+        *reinterpret_cast<uint4*>(base + ((k8 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// This thread's quarters (32 indices each) of one staged row.  Which quarter
+// comes first is rotated by the row so that the staged words of a warp's rows
+// sit in different banks.
+template <int BITS, int D, int TPR>
+__device__ __forceinline__ void pp_expand_row(const unsigned char* rows, float rf, const uint32_t* hi,
+                                              const uint32_t* lo, unsigned char* tile, uint32_t half_bytes, int row,
+                                              int sub) {
+    constexpr int NQ = D / 32;                                       // quarters per row
+    constexpr int EACH = (NQ + TPR - 1) / TPR;
+    constexpr int SPREAD = BITS == 4 ? 8 : (BITS == 3 ? 32 : 16);    // lanes per conflict-free group
+    constexpr int SH = SPREAD / NQ == 32 ? 5 : SPREAD / NQ == 16 ? 4 : SPREAD / NQ == 8 ? 3 : SPREAD / NQ == 4 ? 2 : SPREAD / NQ == 2 ? 1 : 0;
+    const __half2 r = __float2half2_rn(rf);
+    const unsigned char* src = rows + row * (D * BITS / 8);
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int qi = sub * EACH + e;
+        if (NQ < TPR && qi >= NQ) return;
+        const int qq = NQ > 1 ? (qi + (row >> SH)) & (NQ - 1) : 0;
+        uint32_t w[4];
+        const unsigned char* s = src + qq * (4 * BITS);
+        if constexpr (BITS == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(s);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else if constexpr (BITS == 3) {
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(s);
+            w[0] = u[0], w[1] = u[1], w[2] = u[2];
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(s);
+            w[0] = u.x, w[1] = u.y;
+        }
+        pp_expand32<BITS>(w, r, hi, lo, tile, half_bytes, row, qq);
+    }
+}
+
+template <int D, int TPR>
+__device__ __forceinline__ void pp_expand(int bits, const unsigned char* rows, float rf, const uint32_t* hi,
+                                          const uint32_t* lo, unsigned char* tile, uint32_t half_bytes, int row,
+                                          int sub) {
+    if (bits == 4) pp_expand_row<4, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+    else if (bits == 3) pp_expand_row<3, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+    else pp_expand_row<2, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+__global__ void __launch_bounds__(PpGeo<D>::kThreads, 1)
+k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnParams P, int* status) {
+    using Z = PpGeo<D>;
+    constexpr int N = Z::kN, W = Z::kD, SW = Z::kSoftWarps, NS = Z::kStages;
+    constexpr int PARTS = D < 64 ? 1 : D / 64;  // register-sized pieces of a row
+    constexpr int E = D < 64 ? D : 64;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t sa = smem_addr(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Z::kBar);
+    uint64_t* stage_full = bars;              // [NS] the block's packed rows have landed
+    uint64_t* stage_free = stage_full + NS;   // [NS] the expansion has read them
+    uint64_t* kv_full = stage_free + NS;      // [4] a tile is expanded
+    uint64_t* kv_free = kv_full + 4;          // [4] its products are done
+    uint64_t* meta_full = kv_free + 4;        // [4] the block's powers of two are written
+    uint64_t* s_full = meta_full + 4;         // [2] scores of the buffer's step are done
+    uint64_t* p_full = s_full + 2;            // [2] the softmax warps wrote P over them
+    uint64_t* pv_done = p_full + 2;           // [2] its PV product is done
+    uint64_t* q_full = pv_done + 2;           // the item's queries are in shared memory
+    uint64_t* drain = q_full + 1;             // products in flight, on the abort path
+    volatile int* abort_f = reinterpret_cast<volatile int*>(sm + Z::kMisc + 4);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(sm + Z::kMisc);
+    PpCursor* start = reinterpret_cast<PpCursor*>(sm + Z::kCur);
+    long long* share = reinterpret_cast<long long*>(sm + Z::kCur + 48);  // units of a share
+    long long* red = reinterpret_cast<long long*>(sm + Z::kRed);
+
+    if (sa & 1023u) {  // the tiles' swizzle needs it; the whole grid leaves
+        if (tid == 0) report_timeout(status, kPpStatusAlign);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&stage_full[i], 1);
+            mbar_init(&stage_free[i], 8);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&kv_full[i], 8);
+            mbar_init(&kv_free[i], 1);
+            mbar_init(&meta_full[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_full, SW);
+        mbar_init(drain, 1);
+        *abort_f = 0;
+        mbar_fence_init();
+        start->left = 0;
+    }
+    if (warp == SW + 8) tmem_alloc<512>(slot);
+
+    // ---- this CTA's share: the sequences' weights, scanned over the block
+    {
+        const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
+        const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            PpSeq<D> q;
+            q.load(A, b, blockIdx.x == 0 ? status : nullptr);
+            mine += (long long)A.Hkv * q.before(q.tiles);
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        long long total = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < Z::kWarps; ++w) {
+            if (w < warp) before += red[w];
+            total += red[w];
+        }
+        before += incl - mine;
+        const long long per = (total + gridDim.x - 1) / gridDim.x;
+        const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+        if (tid == 0) *share = per;
+        if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
+            long long v = u0 - before;
+            PpSeq<D> q;
+            int b = b0;
+            for (;; ++b) {
+                q.load(A, b, nullptr);
+                const long long w = (long long)A.Hkv * q.before(q.tiles);
+                if (v < w) break;
+                v -= w;
+            }
+            int lo = 0, hi = q.tiles - 1;  // the last tile whose units start at or before v
+            while (lo < hi) {
+                const int m = (lo + hi + 1) / 2;
+                if ((long long)A.Hkv * q.before(m) <= v) lo = m;
+                else hi = m - 1;
+            }
+            v -= (long long)A.Hkv * q.before(lo);
+            const long long w = q.weight(lo);
+            start->b = b;
+            start->i = lo;
+            start->h = (int)(v / w);
+            start->off = v % w;
+            start->left = u1 - u0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    PpCursor cur = *start;
+    PpSeq<D> seq;
+    if (cur.left > 0) seq.load(A, cur.b, nullptr);
+    PpPart p;
+
+    if (warp == SW + 9) {
+        // ---- copies: lane 4 s + a brings array a of segment s (min(page, N)
+        // positions) of a block
+        const int seg = min(1 << A.shift, N), nseg = N / seg;
+        const int s = lane >> 2, a = lane & 3;
+        const uint32_t row_bytes = a == 0 ? D * A.k_bits / 8 : a == 1 ? D * A.v_bits / 8 : 4u;
+        const unsigned char* arr = reinterpret_cast<const unsigned char*>(
+            a == 0 ? (const void*)A.c.k_packed : a == 1 ? (const void*)A.c.v_packed : a == 2 ? (const void*)A.c.k_norm
+                                                                                             : (const void*)A.c.v_norm);
+        const uint32_t at = a == 0 ? 0u : a == 1 ? N * D / 2 : a == 2 ? N * D : N * D + 4 * N;
+        uint32_t tc = 0;
+        bool ok = true;
+        while (ok && pp_next<D>(A, cur, seq, p)) {
+            for (int j = p.blk0; j < p.blk1; ++j, ++tc) {
+                const int st = tc % NS;
+                const int pos = (p.lo_blk + j) * N + s * seg;
+                bool have = s < nseg && pos < p.kv_end;
+                int64_t src = 0;
+                if (have) {
+                    const int page = __ldg(A.bt + (int64_t)p.b * A.max_pages + (pos >> A.shift));
+                    if (page < 0 || page >= A.c.n_pages) {
+                        report_timeout(status, kPpStatusPage);
+                        have = false;
+                    }
+                    src = (((int64_t)page * A.Hkv + p.h) << A.shift) + (pos & ((1 << A.shift) - 1));
+                }
+                if (tc >= (uint32_t)NS) ok = pp_wait(&stage_free[st], (tc / NS - 1) & 1, abort_f, status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t bytes = have ? row_bytes * seg : 0u;
+                uint32_t all = bytes;
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, have && a == 0);
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t*>(sm + Z::kSegs)[st] = mask;  // bit 4 s: segment s is there
+                    mbar_arrive_expect_tx(&stage_full[st], all);
+                }
+                __syncwarp();
+                if (have)
+                    bulk_load(sa + Z::kStg + st * Z::kStage + at + s * seg * row_bytes, arr + src * row_bytes, bytes,
+                              &stage_full[st]);
+            }
+        }
+        // the copies issued have landed before the CTA leaves (bounded)
+        if (lane == 0 && tc > 0)
+            for (uint32_t t = tc > (uint32_t)NS ? tc - NS : 0; t < tc; ++t) mbar_wait(&stage_full[t % NS], (t / NS) & 1);
+    } else if (warp == SW + 8) {
+        // ---- MMAs
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = umma_idesc_f16(128, N, false);
+            constexpr uint32_t idesc_o = umma_idesc_f16(128, W, false) | kIdescBTransposed;
+            uint32_t tc0 = 0, items = 0;
+            uint32_t np[2] = {0, 0}, npv[2] = {0, 0};  // P waits and PV products per buffer
+            bool ok = true;
+            while (ok && pp_next<D>(A, cur, seq, p)) {
+                const int nb = p.blk1 - p.blk0;
+                if (nb == 0) continue;
+                ok = pp_wait(q_full, items & 1, abort_f, status);
+                ++items;
+                const int T = p.pair ? 2 * nb : nb;
+                for (int t = 0; ok && t < T + 2; ++t) {
+                    const int g = t & 1;
+                    if (t >= 2) {
+                        const int u = t - 2, j = p.pair ? u >> 1 : u;
+                        const uint32_t tc = tc0 + j, sl = (2 * tc + 1) & 3;
+                        ok = pp_wait(&p_full[g], np[g] & 1, abort_f, status) &&
+                             pp_wait(&kv_full[sl], (tc >> 1) & 1, abort_f, status);
+                        if (!ok) break;
+                        ++np[g];
+                        tc_fence_after();
+                        const uint32_t vt = sa + Z::kRing + sl * Z::kTile;
+                        const uint32_t o = tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0);
+                        const bool first = Z::kStreams == 2 ? u < 2 : u == 0;  // the output's first product
+#pragma unroll
+                        for (int kk = 0; kk < N / 16; ++kk)
+                            umma_f16_ts(o, tmem + Z::kTmemS + N * g + 8 * kk,
+                                        umma_desc_sw128_mn(vt + kk * 2048, N * 128), idesc_o,
+                                        (!first || kk > 0) ? 1u : 0u);
+                        umma_commit(&pv_done[g]);
+                        if (!p.pair || g == 1) umma_commit(&kv_free[sl]);
+                        ++npv[g];
+                        if (t < T) ok = pp_wait(&pv_done[g], (npv[g] - 1) & 1, abort_f, status);
+                        if (!ok) break;
+                    }
+                    if (t < T) {
+                        const int j = p.pair ? t >> 1 : t;
+                        const uint32_t tc = tc0 + j, sl = (2 * tc) & 3;
+                        ok = pp_wait(&kv_full[sl], (tc >> 1) & 1, abort_f, status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t kt = sa + Z::kRing + sl * Z::kTile;
+                        const uint32_t qt = sa + Z::kQ + (p.pair ? g * Z::kQTile : 0);
+                        const uint32_t d = tmem + Z::kTmemS + N * g;
+#pragma unroll
+                        for (int kk = 0; kk < W / 16; ++kk)
+                            umma_f16(d, umma_desc_sw128(qt + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                     umma_desc_sw128(kt + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc_s,
+                                     kk > 0 ? 1u : 0u);
+                        umma_commit(&s_full[g]);
+                        if (!p.pair || g == 1) umma_commit(&kv_free[sl]);
+                    }
+                }
+                tc0 += nb;
+            }
+            if (!ok) {  // products in flight finish before the tensor memory is freed (bounded)
+                umma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+        }
+    } else if (warp >= SW) {
+        // ---- expansion: thread = (row, sub) of the block
+        constexpr int TPR = 256 / N;
+        const int dt = tid - 32 * SW;
+        const int row = dt % N, sub = dt / N;
+        if (D < 64) {  // the padded half of the tiles stays zero
+            for (uint32_t i = dt; i < 4 * Z::kTile / 16; i += 256)
+                reinterpret_cast<uint4*>(sm + Z::kRing)[i] = make_uint4(0, 0, 0, 0);
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+        }
+        uint32_t tc = 0;
+        bool ok = true;
+        while (ok && pp_next<D>(A, cur, seq, p)) {
+            int eprev = 0, emax = -1000;
+            for (int j = p.blk0; j < p.blk1; ++j, ++tc) {
+                const int st = tc % NS;
+                const unsigned char* stg = sm + Z::kStg + st * Z::kStage;
+                const float* knp = reinterpret_cast<const float*>(stg + N * D);
+                const float* vnp = knp + N;
+                ok = pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
+                const int t0 = (p.lo_blk + j) * N;
+                const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
+                auto there = [&](int k) { return t0 + k < p.kv_end && ((segs >> (4 * (k >> seg_sh))) & 1u); };
+                // the block's largest finite norms (each warp for itself)
+                float mk = 0.f, mv = 0.f;
+#pragma unroll
+                for (int k = 0; k < N / 32; ++k) {
+                    const int kk = 32 * k + lane;
+                    if (there(kk)) {
+                        const float x = fabsf(knp[kk]), y = fabsf(vnp[kk]);
+                        if (x <= FLT_MAX) mk = fmaxf(mk, x);
+                        if (y <= FLT_MAX) mv = fmaxf(mv, y);
+                    }
+                }
+                mk = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mk)));
+                mv = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mv)));
+                // below 2^e; the range keeps every factor of the kernel a normal fp32
+                auto exponent = [](float m) { return min(100, max(-100, (int)(__float_as_uint(m) >> 23) - 126)); };
+                const int ek = mk > 0.f ? exponent(mk) : 0;
+                int ev = mv > 0.f ? exponent(mv) : eprev;
+                if (mv > 0.f) {
+                    // a block of far smaller values rides on the largest so far
+                    ev = max(ev, emax - 60);
+                    emax = max(emax, ev);
+                    eprev = ev;
+                }
+                float rk = 0.f, rv = 0.f;
+                if (there(row)) {
+                    const float kn = knp[row], vn = vnp[row];
+                    rk = fmaf(vn, 0.f, kn * pp_pow2(-ek));  // NaN if either norm is not finite
+                    rv = fabsf(vn) <= FLT_MAX ? vn * pp_pow2(-ev) : 0.f;
+                }
+                const uint32_t slk = (2 * tc) & 3, slv = (2 * tc + 1) & 3;
+                if (tc >= 2) ok = pp_wait(&kv_free[slk], ((tc >> 1) - 1) & 1, abort_f, status);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (dt == 0) {
+                    reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 3] = make_float2(pp_pow2(ek), (float)ev);
+                    mbar_arrive(&meta_full[tc & 3]);
+                }
+                pp_expand<D, TPR>(A.k_bits, stg, rk, A.khi, A.klo, sm + Z::kRing + slk * Z::kTile, N * 128, row, sub);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[slk]);
+                if (tc >= 2) ok = pp_wait(&kv_free[slv], ((tc >> 1) - 1) & 1, abort_f, status);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                pp_expand<D, TPR>(A.v_bits, stg + N * D / 2, rv, A.vhi, A.vlo, sm + Z::kRing + slv * Z::kTile, N * 128,
+                                  row, sub);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&kv_full[slv]);
+                    mbar_arrive(&stage_free[st]);
+                }
+            }
+        }
+    } else {
+        // ---- softmax: stream g, row r of its tile
+        const int g = warp >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t t_out = t_lane + Z::kTmemO + 128 * g;
+        const int G = A.Hq / A.Hkv;
+        const float q_sign = P.q_mul > 0.f ? 1.f : (P.q_mul < 0.f ? -1.f : 0.f);
+        const float q_abs = P.q_mul == 0.f ? 1.f : fabsf(P.q_mul);
+        uint32_t ns[2] = {0, 0}, npv[2] = {0, 0}, tc0 = 0;
+        int part_no = 0;
+        while (pp_next<D>(A, cur, seq, p)) {
+            const int nb = p.blk1 - p.blk0;
+            // the row of this thread: in split mode both streams have row r
+            const int lrow = p.pair ? 128 * g + r : r;
+            const bool rvalid = lrow < p.rows;
+            const int grow = p.row0 + lrow;
+            const int tok = rvalid ? grow / G : 0, hd = rvalid ? grow - tok * G : 0;
+            const int64_t qrow = ((int64_t)__ldg(A.cu + p.b) + tok) * A.Hq + (int64_t)p.h * G + hd;
+            const int pos = rvalid ? seq.ctx - seq.n + tok : -1;
+            const int lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
+            // ---- queries: rotated in registers and tensor memory (the output
+            // columns, free until the item's first product), 64 dims at a time,
+            // and rounded to fp16 under a power of two per row
+            float cq = q_abs;
+            if (nb > 0 && (p.pair || g == 0)) {
+                float amax = 0.f;
+                const uint4* src = reinterpret_cast<const uint4*>(A.q + qrow * D);
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h) {
+                    float y[E];
+#pragma unroll
+                    for (int k = 0; k < E / 8; ++k) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (rvalid) u = __ldg(src + (64 * h) / 8 + k);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            y[8 * k + 2 * c] = __uint_as_float((uu[c] << 16) ^ P.sgn[64 * h + 8 * k + 2 * c]);
+                            y[8 * k + 2 * c + 1] =
+                                __uint_as_float((uu[c] & 0xFFFF0000u) ^ P.sgn[64 * h + 8 * k + 2 * c + 1]);
+                            amax = fmaxf(amax, fmaxf(fabsf(y[8 * k + 2 * c]), fabsf(y[8 * k + 2 * c + 1])));
+                        }
+                    }
+                    fwht_reg2<E>(y);
+                    uint32_t o[32];
+#pragma unroll
+                    for (int c = 0; c < E / 32; ++c) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[32 * c + k]);
+                        tmem_st32(t_out + 64 * h + 32 * c, o);
+                    }
+                }
+                tmem_wait_st();
+                // |rotated| <= D amax: below 2^14 after the scaling by 2^-e
+                int e = 0;
+                if (amax > 0.f && amax <= FLT_MAX) {
+                    constexpr int LD = D == 32 ? 5 : D == 64 ? 6 : D == 128 ? 7 : 8;
+                    e = min(100, max(-100, (int)(__float_as_uint(amax) >> 23) - 126 + LD - 14));
+                }
+                cq = q_abs * pp_pow2(e);
+                const float inv = q_sign * pp_pow2(-e);
+                unsigned char* qt = sm + Z::kQ + (p.pair ? g * Z::kQTile : 0);
+#pragma unroll
+                for (int c = 0; c < E / 16; ++c) {
+                    uint32_t y[PARTS][16];
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) tmem_ld16(t_out + 64 * h + 16 * c, y[h]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int len = 1; len < PARTS; len *= 2)
+#pragma unroll
+                        for (int h = 0; h < PARTS; ++h)
+                            if (!(h & len)) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const float u = __uint_as_float(y[h][k]), v = __uint_as_float(y[h + len][k]);
+                                    y[h][k] = __float_as_uint(u + v);
+                                    y[h + len][k] = __float_as_uint(u - v);
+                                }
+                            }
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int j = 64 * h + 16 * c + 2 * k;
+                            float v0 = __uint_as_float(y[h][2 * k]) * inv, v1 = __uint_as_float(y[h][2 * k + 1]) * inv;
+                            if (P.two_sided) {
+                                v0 = __uint_as_float(__float_as_uint(v0) ^ P.sgn2[j]);
+                                v1 = __uint_as_float(__float_as_uint(v1) ^ P.sgn2[j + 1]);
+                            }
+                            const __half2 hh = __floats2half2_rn(v0, v1);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                        }
+                        const int k8 = 8 * h + 2 * c;
+                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                if constexpr (D < 64) {
+#pragma unroll
+                    for (int k8 = D / 8; k8 < 8; ++k8)
+                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            if (Z::kStreams == 2 && !p.pair && nb > 0) {
+                // stream 1 has the same rows: it takes their factor from stream 0
+                float* xs = reinterpret_cast<float*>(sm + Z::kQ + Z::kQTile);
+                if (g == 0) xs[r] = cq;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (g == 1) cq = xs[r];
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && nb > 0) mbar_arrive(q_full);
+
+            // ---- the steps
+            float M = -INFINITY, l = 0.f, eb = 0.f;
+            int lastb = -1;  // buffer of this stream's last step
+            for (int j = (Z::kStreams == 2 && !p.pair) ? g : 0; j < nb; j += (Z::kStreams == 2 && !p.pair) ? 2 : 1) {
+                const int buf = Z::kStreams == 2 ? g : (j & 1);
+                const uint32_t tc = tc0 + j;
+                pp_wait(&meta_full[tc & 3], (tc >> 2) & 1, abort_f, status);
+                const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 3);
+                const float2 meta = make_float2(mp[0], mp[1]);
+                if (lastb < 0) eb = meta.y;
+                pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
+                ++ns[buf];
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
+                const int t0 = (p.lo_blk + p.blk0 + j) * N;
+                // columns [c0, c1) of the block are this row's
+                const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
+                const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_wait_ld();
+                    if (full) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int col = 32 * c + k;
+                            if (col >= c0 && col < c1) mx = fmaxf(mx, __uint_as_float(s[k]));
+                        }
+                    }
+                }
+                const float cs = cq * meta.x;
+                const float cand = mx * cs + meta.y;  // -inf where nothing is attended
+                const bool move = cand > M + 8.f || (M == -INFINITY && cand > -INFINITY);
+                const bool rescale = move && M != -INFINITY;
+                if (__any_sync(0xFFFFFFFFu, rescale)) {
+                    const float alpha = rescale ? pp_exp2(M - cand) : 1.f;
+                    if (Z::kStreams == 1)  // the other buffer's product wrote the output last
+                        pp_wait(&pv_done[buf ^ 1], (npv[buf ^ 1] - 1) & 1, abort_f, status);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < W / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(t_out + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st32(t_out + 32 * c, o);
+                    }
+                    l *= alpha;
+                }
+                if (move) M = cand;
+                const float off = M == -INFINITY ? 0.f : meta.y - M;
+                const F2 CS = f2(cs, cs), OFF = f2(off, off);
+                F2 sum = f2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_wait_ld();
+                    if (!full) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int col = 32 * c + k;
+                            if (!(col >= c0 && col < c1)) s[k] = 0xFF800000u;  // -inf
+                        }
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float a0, a1;
+                        f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), CS, OFF), a0, a1);
+                        a0 = pp_exp2(a0);
+                        a1 = pp_exp2(a1);
+                        sum = f2_add(sum, f2(a0, a1));
+                        const __half2 hh = __floats2half2_rn(a0, a1);
+                        w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                    }
+                    tmem_st16(t_s + 16 * c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[buf]);
+                ++npv[buf];
+                float s0, s1;
+                f2_split(sum, s0, s1);
+                l = fmaf(s0 + s1, pp_exp2(eb - meta.y), l);
+                lastb = buf;
+            }
+            if (lastb >= 0) {
+                if (Z::kStreams == 1 && nb > 1) pp_wait(&pv_done[lastb ^ 1], (npv[lastb ^ 1] - 1) & 1, abort_f, status);
+                pp_wait(&pv_done[lastb], (npv[lastb] - 1) & 1, abort_f, status);
+            }
+            __syncwarp();
+            tc_fence_after();
+            // ---- split mode: stream 0 adds stream 1's output and sums to its own
+            if (Z::kStreams == 2 && !p.pair && nb > 0) {
+                float* xs = reinterpret_cast<float*>(sm + Z::kQ + Z::kQTile);
+                if (g == 1) {
+                    xs[r] = M;
+                    xs[128 + r] = l;
+                    xs[256 + r] = eb;
+                }
+                tc_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tc_fence_after();
+                if (g == 0 && nb > 1) {
+                    const float M1 = xs[r], l1 = xs[128 + r], eb1 = xs[256 + r];
+                    const float Mx = fmaxf(M, M1);
+                    const float a0 = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = M1 == -INFINITY ? 0.f : pp_exp2(M1 - Mx);
+#pragma unroll
+                    for (int c = 0; c < W / 32; ++c) {
+                        uint32_t o[32], o1[32];
+                        tmem_ld32(t_out + 32 * c, o);
+                        tmem_ld32(t_out + 128 + 32 * c, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * a0 + __uint_as_float(o1[k]) * a1);
+                        tmem_st32(t_out + 32 * c, o);
+                    }
+                    tmem_wait_st();
+                    l = (M == -INFINITY ? l : l * a0) + (M1 == -INFINITY ? l1 : l1 * a1) * pp_exp2(eb - eb1);
+                    M = Mx;
+                }
+                tc_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tc_fence_after();
+            }
+            // ---- the rows leave: finished, or as a part
+            if (p.pair || g == 0) {
+                if (p.whole) {
+                    const float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
+                    if (nb == 0) {
+#pragma unroll
+                        for (int c = 0; c < W / 32; ++c) {
+                            uint32_t o[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = 0u;
+                            tmem_st32(t_out + 32 * c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    // rotated back, s . H (s2 . o): 64 dims at a time, then across
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) {
+                        float y[E];
+                        uint32_t o[32];
+#pragma unroll
+                        for (int c = 0; c < E / 32; ++c) {
+                            tmem_ld32(t_out + 64 * h + 32 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int j = 64 * h + 32 * c + k;
+                                y[32 * c + k] = __uint_as_float(P.two_sided ? o[k] ^ P.sgn2[j] : o[k]);
+                            }
+                        }
+                        fwht_reg2<E>(y);
+#pragma unroll
+                        for (int c = 0; c < E / 32; ++c) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[32 * c + k]);
+                            tmem_st32(t_out + 64 * h + 32 * c, o);
+                        }
+                    }
+                    tmem_wait_st();
+                    const bool write = rvalid && *abort_f == 0;
+#pragma unroll
+                    for (int c = 0; c < E / 16; ++c) {
+                        uint32_t y[PARTS][16];
+#pragma unroll
+                        for (int h = 0; h < PARTS; ++h) tmem_ld16(t_out + 64 * h + 16 * c, y[h]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int len = 1; len < PARTS; len *= 2)
+#pragma unroll
+                            for (int h = 0; h < PARTS; ++h)
+                                if (!(h & len)) {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        const float u = __uint_as_float(y[h][k]), v = __uint_as_float(y[h + len][k]);
+                                        y[h][k] = __float_as_uint(u + v);
+                                        y[h + len][k] = __float_as_uint(u - v);
+                                    }
+                                }
+                        if (write) {
+#pragma unroll
+                        for (int h = 0; h < PARTS; ++h) {
+                            const int j0 = 64 * h + 16 * c;
+                            float v[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                v[k] = __uint_as_float(__float_as_uint(__uint_as_float(y[h][k]) * inv) ^ P.sgn[j0 + k]);
+                            if (A.out_bf16) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const __nv_bfloat162 bb = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                                    w[k] = *reinterpret_cast<const uint32_t*>(&bb);
+                                }
+                                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + qrow * D + j0);
+                                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            } else {
+                                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(A.out) + qrow * D + j0);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            }
+                        }
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    const int which = p.head ? 1 : 0;
+                    float* w = A.part + ((int64_t)blockIdx.x * 2 + which) * PagedPrefillGeo<D>::kPartFloats;
+                    float4* o4 = reinterpret_cast<float4*>(w);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(t_out + 16 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o4[(4 * c + k) * Z::kRows + lrow] =
+                                make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                            __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                    }
+                    float* x = w + D * Z::kRows;
+                    x[lrow] = M;
+                    x[Z::kRows + lrow] = l;
+                    x[2 * Z::kRows + lrow] = eb;
+                }
+                tc_fence_before();
+            }
+            if (!p.whole) part_no |= p.head ? 2 : 1;
+            tc0 += nb;
+        }
+        // ---- which parts this share left, and the item it owns: the one that
+        // starts in this share and ends in a later one
+        if (tid == 0) {
+            int32_t* m = A.meta + (int64_t)blockIdx.x * kPpMeta;
+            m[kMetaHas0] = part_no & 1;
+            m[kMetaHas1] = part_no >> 1;
+            bool owner = cur.off > 0 && !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
+            if (owner) {
+                const int64_t w = seq.weight(cur.i), per = *share;
+                const int nblk = pp_blocks<D>(A, seq, cur.i);
+                int last = blockIdx.x;
+                // no join where one share has all of the item's blocks
+                owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
+                for (int64_t at = cur.off; at < w; at += per) {
+                    ++last;
+                    if (pp_cut(nblk, at, w) == 0 && pp_cut(nblk, min(w, at + per), w) == nblk) owner = false;
+                }
+                m[kMetaB] = cur.b;
+                m[kMetaI] = cur.i;
+                m[kMetaH] = cur.h;
+                m[kMetaLast] = last;
+            }
+            m[kMetaOwner] = owner;
+        }
+    }
+    griddep_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == SW + 8) {
+        tc_fence_after();
+        tmem_dealloc<512>(tmem);
+    }
+}
+
+// Block (share, y): rows 32 y .. + 31 of the item that the share owns, its
+// parts summed in the order of the shares, divided and rotated back.
+template <int D>
+__global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constant__ PpArgs A,
+                                                            const __grid_constant__ AttnParams P) {
+    using Z = PpGeo<D>;
+    constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
+    __shared__ float tile[32][D + 1];
+    griddep_wait();
+    const int sh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t* meta = A.meta + (int64_t)sh * kPpMeta;
+    if (!__ldcg(meta + kMetaOwner)) return;
+    const int b = __ldcg(meta + kMetaB), i = __ldcg(meta + kMetaI), h = __ldcg(meta + kMetaH),
+              last = __ldcg(meta + kMetaLast);
+    PpSeq<D> q;
+    q.load(A, b, nullptr);
+    const int row0 = i * Z::kRows, rows = min(Z::kRows, q.rows - row0);
+    const int lrow = 32 * blockIdx.y + lane;  // every warp: the same 32 rows
+    if (32 * (int)blockIdx.y >= rows) return;
+    constexpr int64_t PF = PagedPrefillGeo<D>::kPartFloats;
+    auto part = [&](int c) { return A.part + ((int64_t)c * 2 + (c == sh)) * PF; };
+    auto has = [&](int c) { return __ldcg(A.meta + (int64_t)c * kPpMeta + (c == sh ? kMetaHas1 : kMetaHas0)) != 0; };
+    float M = -INFINITY, eb = 0.f;
+    bool first = true;
+    for (int c = sh; c <= last; ++c) {
+        if (!has(c)) continue;
+        const float* x = part(c) + D * Z::kRows;
+        M = fmaxf(M, __ldcg(x + lrow));
+        if (first) eb = __ldcg(x + 2 * Z::kRows + lrow);
+        first = false;
+    }
+    float l = 0.f;
+    float4 o[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = sh; c <= last; ++c) {
+        if (!has(c)) continue;
+        const float* x = part(c) + D * Z::kRows;
+        const float m = __ldcg(x + lrow), lc = __ldcg(x + Z::kRows + lrow), ec = __ldcg(x + 2 * Z::kRows + lrow);
+        const float a = m == -INFINITY ? 0.f : pp_exp2(m - M);
+        l += (m == -INFINITY ? lc : lc * a) * pp_exp2(eb - ec);
+        const float4* o4 = reinterpret_cast<const float4*>(part(c));
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const float4 v = __ldcg(o4 + (warp + 8 * k) * Z::kRows + lrow);
+            o[k].x = fmaf(a, v.x, o[k].x);
+            o[k].y = fmaf(a, v.y, o[k].y);
+            o[k].z = fmaf(a, v.z, o[k].z);
+            o[k].w = fmaf(a, v.w, o[k].w);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        const float v[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = 4 * (warp + 8 * k) + u;
+            tile[lane][j] = __uint_as_float(__float_as_uint(v[u] * inv) ^ (P.two_sided ? P.sgn2[j] : 0u));
+        }
+    }
+    __syncthreads();
+    // rows rotated back, one per warp at a time: elements lane + 32 k, the
+    // transform's low five bits across lanes, the rest in registers
+    for (int r = warp; r < 32; r += 8) {
+        const int lr = 32 * blockIdx.y + r;
+        if (lr >= rows) break;
+        float e[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) e[k] = tile[r][lane + 32 * k];
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2)
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                const float u = __shfl_xor_sync(0xFFFFFFFFu, e[k], m);
+                e[k] = lane & m ? u - e[k] : e[k] + u;
+            }
+#pragma unroll
+        for (int len = 1; len < C; len *= 2)
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (!(k & len)) {
+                    const float u = e[k], v = e[k + len];
+                    e[k] = u + v;
+                    e[k + len] = u - v;
+                }
+        const int grow = row0 + lr, tok = grow / q.G, hd = grow - tok * q.G;
+        const int64_t at = (((int64_t)__ldg(A.cu + b) + tok) * A.Hq + (int64_t)h * q.G + hd) * D;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int j = lane + 32 * k;
+            const float v = __uint_as_float(__float_as_uint(e[k]) ^ sign_mask(P.sgnb, j));
+            if (A.out_bf16) static_cast<__nv_bfloat16*>(A.out)[at + j] = __float2bfloat16_rn(v);
+            else static_cast<float*>(A.out)[at + j] = v;
+        }
+    }
+}
+
+}  // namespace dev
+
+template <int D>
+cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P, cudaStream_t s) {
+    using namespace dev;
+    using Z = PpGeo<D>;
+    static_assert(Z::kSmem <= 232448, "shared memory per CTA");
+    PpArgs A = {};
+    A.q = static_cast<const __nv_bfloat16*>(c.q);
+    A.out = c.out;
+    A.cu = c.cu_q;
+    A.ctx = c.ctx_lens;
+    A.bt = c.block_table;
+    A.c = c.cache;
+    A.n_q = c.n_q;
+    A.B = c.B;
+    A.Hq = c.Hq;
+    A.Hkv = c.Hkv;
+    A.max_pages = c.max_pages;
+    A.shift = c.page_shift;
+    A.window = c.window;
+    A.k_bits = c.k_bits;
+    A.v_bits = c.v_bits;
+    A.out_bf16 = c.out_bf16;
+    for (int i = 0; i < 4; ++i) {
+        A.khi[i] = c.k_levels[i];
+        A.klo[i] = c.k_levels[4 + i];
+        A.vhi[i] = c.v_levels[i];
+        A.vlo[i] = c.v_levels[4 + i];
+    }
+    const int shares = num_sms();
+    A.part = static_cast<float*>(c.workspace);
+    A.meta = reinterpret_cast<int32_t*>(A.part + (size_t)shares * 2 * PagedPrefillGeo<D>::kPartFloats);
+    static int attr_done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        e = cudaFuncSetAttribute(k_prefill_paged<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Z::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev] = 1;
+    }
+    k_prefill_paged<D><<<shares, Z::kThreads, Z::kSmem, s>>>(A, P, status_word());
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_prefill_paged_join<D>, dim3(shares, Z::kRows / 32), dim3(256), 0, s, A, P);
+}
+
+template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, const AttnParams&, cudaStream_t);
+
+}  // namespace tq

@@ -154,3 +154,37 @@ def test_python_layer_refusals():
         abi.PagedLayers(abi.PagedCache(z(4, 2, 32, 64), z(4, 2, 32, dt=torch.float32), z(4, 2, 32, 48),
                                        z(4, 2, 32, dt=torch.float32), 4, 3))
     assert ctypes.sizeof(abi.PageTableView) == 24
+
+
+def test_prefill_paged_refusals(L):
+    """tq_attn_prefill_paged checks its arguments on the host before any launch."""
+    p128, p16 = abi.Plan(128, 42), abi.Plan(16, 42)
+    A, W = 1 << 20, 1 << 28
+    f = ctypes.c_float
+    need = L.tq_attn_prefill_paged_workspace_bytes(8, 2, 128)
+    assert need > 0
+    for bad in ((0, 2, 128), (8, 3, 128), (8, 0, 128), (8, 2, 16), (8, 2, 96)):
+        assert L.tq_attn_prefill_paged_workspace_bytes(*bad) == 0
+
+    def call(plan=p128.handle, q=A, n_q=10, B=2, Hq=8, Hkv=2, cache=_cache(), bt=A, mp=4, cu=A, ctx=A, window=0,
+             kb=4, vb=3, scale=1.0, out=A, dt=1, ws=W, size=need):
+        return L.tq_attn_prefill_paged(plan, q, n_q, B, Hq, Hkv, cache, bt, mp, cu, ctx, window, kb, vb, f(scale), out,
+                                       dt, ws, size, None)
+
+    assert call(plan=None) == 1
+    assert call(plan=p16.handle) == 2
+    assert call(B=-1) == 1 and call(n_q=-1) == 1 and call(Hq=7) == 1 and call(Hkv=0) == 1 and call(mp=0) == 1
+    assert call(window=-1) == 1 and call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
+    assert call(kb=1) == 2 and call(vb=5) == 2 and call(dt=2) == 2
+    assert call(Hq=258, Hkv=2) == 2                                  # 129 heads a group
+    assert call(cache=_cache(page_size=48)) == 2
+    assert call(cache=_cache(n_pages=0)) == 1
+    assert call(mp=1 << 25) == 2                                     # positions past 2^30
+    assert call(n_q=1 << 30) == 2                                    # rows past int32
+    assert call(B=0, q=None, out=None, ws=None) == 0 and call(n_q=0, q=None) == 0
+    for name in ("q", "out", "bt", "cu", "ctx"):
+        assert call(**{name: None}) == 1
+        assert call(**{name: A + 2}) == 3
+    assert call(q=A + 8) == 3 and call(out=A + 8) == 3
+    assert call(cache=abi.PagedCacheView(1 << 32, (1 << 33) + 4, 1 << 34, 1 << 35, 4, 64)) == 3  # norms: 16 bytes
+    assert call(ws=None) == 5 and call(size=need - 1) == 5 and call(ws=W + 8) == 3
