@@ -87,8 +87,9 @@ struct PpGeo {
     static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
     static constexpr uint32_t kRedBytes = 18 * 8 + 16;
     static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
-    static constexpr uint32_t kBar = kCur + 64;
-    static constexpr int kBars = 2 * kStages + 4 + 4 + 4 + 2 + 2 + 2 + 1 + 1;
+    static constexpr uint32_t kJobs = kCur + 64;                // [2] jobs
+    static constexpr uint32_t kBar = kJobs + 2 * 48;
+    static constexpr int kBars = 2 * kStages + 4 + 4 + 4 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr uint32_t kSmem = (kMisc + 8 + 127) / 128 * 128;
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // buffer b at kN b; output g at 128 g further
@@ -237,6 +238,20 @@ __device__ bool pp_next(const PpArgs& A, PpCursor& c, PpSeq<D>& q, PpPart& p) {
     return false;
 }
 
+// A part as the copy warp hands it to the others, through shared memory.
+struct PpJob {
+    int nb;        // blocks, -1: no more parts
+    int flags;     // kJob*
+    int q0;        // the sequence's first row of q
+    int h;         // KV head
+    int row0, rows;  // first row within (sequence, KV head); valid rows
+    int blk;       // first block
+    int kv_end;    // positions at or past it are not read
+    int pos0;      // position of the sequence's token 0
+    int pad[3];
+};
+enum { kJobPair = 1, kJobWhole = 2, kJobHead = 4 };
+
 __device__ __forceinline__ uint32_t pp_chunk(uint32_t half_bytes, int row, int k8) {
     return (uint32_t)(k8 >> 3) * half_bytes + (uint32_t)row * 128 + (((k8 & 7) ^ (row & 7)) << 4);
 }
@@ -247,6 +262,20 @@ __device__ __forceinline__ float pp_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+
+// The value of lane 0: known to the compiler to be the same in the whole warp.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+    return ((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v);
 }
 
 // Bounded wait; gives up at once when the CTA's abort flag is set.
@@ -311,88 +340,192 @@ __device__ __forceinline__ void pp_levels4(uint32_t sel, uint32_t x, const uint3
     p23 = __byte_perm(l, h, 0x7362);
 }
 
-// 32 indices (BITS words) -> 32 fp16 values times r, four 16-byte chunks at
-// k8 = 4 quarter .. + 3 of the tile row.
-template <int BITS>
-__device__ __forceinline__ void pp_expand32(const uint32_t* w, __half2 r, const uint32_t* hi, const uint32_t* lo,
-                                            unsigned char* tile, uint32_t half_bytes, int row, int quarter) {
-    unsigned char* base = tile + (uint32_t)(quarter >> 1) * half_bytes + (uint32_t)row * 128;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t sel, x = 0;
-        if constexpr (BITS == 4) {
-            // an index with its top bit set is positive level (index - 8), one
-            // without is the negative of level 7 - index
-            const uint32_t t = w[c] & 0x88888888u;
-            x = t >> 3;
-            sel = (w[c] ^ ~(t - x)) & 0x77777777u;
-        } else if constexpr (BITS == 3) {
-            const int bit = 24 * c;
-            const uint32_t f = bit % 32 == 0 ? w[bit / 32]
-                                             : __funnelshift_r(w[bit / 32], bit / 32 + 1 < 3 ? w[bit / 32 + 1] : 0u, bit % 32);
-            sel = (f & 0xFFFu) | ((f << 4) & 0x0FFF0000u);
-            sel = (sel & 0x003F003Fu) | ((sel << 2) & 0x3F003F00u);
-            sel = (sel & 0x07070707u) | ((sel << 1) & 0x70707070u);
-        } else {
-            const uint32_t f = w[c >> 1] >> (16 * (c & 1));
-            sel = (f & 0xFFu) | ((f << 8) & 0x00FF0000u);
-            sel = (sel & 0x000F000Fu) | ((sel << 4) & 0x0F000F00u);
-            sel = (sel & 0x03030303u) | ((sel << 2) & 0x30303030u);
-        }
-        uint32_t v[4];
-        pp_levels4<BITS>(sel, x, hi, lo, v[0], v[1]);
-        pp_levels4<BITS>(sel >> 16, x >> 16, hi, lo, v[2], v[3]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[k]), r);
-            v[k] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-        const int k8 = 4 * (quarter & 1) + c;
-        *reinterpret_cast<uint4*>(base + ((k8 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+// 8 indices (fp16 pairs of their levels times the row's norm) to 16 bytes at
+// dst.  The norm comes as fp16 high part r; with LOW also its rest rl, so that
+// only the product is rounded (a rounded norm would shift a key's scores for
+// every query alike).
+template <int BITS, bool LOW>
+__device__ __forceinline__ void pp_expand8(uint32_t f, __half2 r, __half2 rl, const uint32_t* hi, const uint32_t* lo,
+                                           unsigned char* dst) {
+    uint32_t sel, x = 0;
+    if constexpr (BITS == 4) {
+        // an index with its top bit set is positive level (index - 8), one
+        // without is the negative of level 7 - index
+        const uint32_t t = f & 0x88888888u;
+        x = t >> 3;
+        sel = (f ^ ~(t - x)) & 0x77777777u;
+    } else if constexpr (BITS == 3) {
+        sel = (f & 0xFFFu) | ((f << 4) & 0x0FFF0000u);
+        sel = (sel & 0x003F003Fu) | ((sel << 2) & 0x3F003F00u);
+        sel = (sel & 0x07070707u) | ((sel << 1) & 0x70707070u);
+    } else {
+        sel = (f & 0xFFu) | ((f << 8) & 0x00FF0000u);
+        sel = (sel & 0x000F000Fu) | ((sel << 4) & 0x0F000F00u);
+        sel = (sel & 0x03030303u) | ((sel << 2) & 0x30303030u);
     }
+    uint32_t v[4];
+    pp_levels4<BITS>(sel, x, hi, lo, v[0], v[1]);
+    pp_levels4<BITS>(sel >> 16, x >> 16, hi, lo, v[2], v[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2 c = *reinterpret_cast<const __half2*>(&v[k]);
+        const __half2 y = LOW ? __hfma2(c, r, __hmul2(c, rl)) : __hmul2(c, r);
+        v[k] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// This thread's quarters (32 indices each) of one staged row.  Which quarter
-// comes first is rotated by the row so that the staged words of a warp's rows
-// sit in different banks.
-template <int BITS, int D, int TPR>
+// Which pair of 16-byte chunks a row's thread starts with (an xor on the pair
+// number): a permutation per row under which a warp's reads of the staged
+// words fall into different banks, and each eight lanes' writes to the
+// swizzled tile too.
+template <int BITS, int D>
+__device__ __forceinline__ int pp_turn(int r) {
+    if constexpr (BITS == 4)
+        return D == 128 ? ((r >> 2) & 3) | ((r & 2) << 1)
+                        : D == 256 ? ((r >> 2) & 3) | ((r & 3) << 2) : D == 64 ? (r >> 2) & 3 : (r >> 3) & 1;
+    else if constexpr (BITS == 3)
+        return D == 128 ? ((r >> 3) & 3) << 1
+                        : D == 256 ? (((r >> 3) & 3) << 1) | ((r & 4) << 1) : D == 64 ? (r >> 4) & 1 : 0;
+    else
+        return D == 128 ? (r >> 2) & 7
+                        : D == 256 ? ((r >> 2) & 7) | ((r & 2) << 2) : D == 64 ? (r >> 3) & 3 : (r >> 4) & 1;
+}
+
+// This thread's share of one staged row, 16 indices per turn of a rolled loop.
+// (All of the kernel's inner loops are rolled to stay within the instruction
+// cache: unrolled, its warps waited for instructions most of the time.)
+template <int BITS, int D, int TPR, bool LOW>
 __device__ __forceinline__ void pp_expand_row(const unsigned char* rows, float rf, const uint32_t* hi,
                                               const uint32_t* lo, unsigned char* tile, uint32_t half_bytes, int row,
                                               int sub) {
-    constexpr int NQ = D / 32;                                       // quarters per row
-    constexpr int EACH = (NQ + TPR - 1) / TPR;
-    constexpr int SPREAD = BITS == 4 ? 8 : (BITS == 3 ? 32 : 16);    // lanes per conflict-free group
-    constexpr int SH = SPREAD / NQ == 32 ? 5 : SPREAD / NQ == 16 ? 4 : SPREAD / NQ == 8 ? 3 : SPREAD / NQ == 4 ? 2 : SPREAD / NQ == 2 ? 1 : 0;
-    const __half2 r = __float2half2_rn(rf);
+    constexpr int EACH = D / 16 / TPR;
+    const __half rh = __float2half_rn(rf);
+    const __half2 r = __half2half2(rh), rl = __float2half2_rn(rf - __half2float(rh));
     const unsigned char* src = rows + row * (D * BITS / 8);
-#pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        const int qi = sub * EACH + e;
-        if (NQ < TPR && qi >= NQ) return;
-        const int qq = NQ > 1 ? (qi + (row >> SH)) & (NQ - 1) : 0;
-        uint32_t w[4];
-        const unsigned char* s = src + qq * (4 * BITS);
+    unsigned char* dst = tile + (uint32_t)row * 128;
+    const int turn = pp_turn<BITS, D>(row);
+    const uint32_t sw = (row & 7) << 4;
+#pragma unroll 1
+    for (int e = sub * EACH; e < sub * EACH + EACH; ++e) {
+        const int c = e ^ turn;
+        uint32_t f0, f1;
         if constexpr (BITS == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(s);
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            const uint2 u = reinterpret_cast<const uint2*>(src)[c];
+            f0 = u.x;
+            f1 = u.y;
         } else if constexpr (BITS == 3) {
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(s);
-            w[0] = u[0], w[1] = u[1], w[2] = u[2];
+            // 48 bits from a 32-bit boundary or 16 bits past one
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(src) + ((3 * c) >> 1);
+            const uint32_t a = w[0], b = w[1];
+            f0 = c & 1 ? __funnelshift_r(a, b, 16) : a;
+            f1 = c & 1 ? b >> 8 : __funnelshift_r(a, b, 24);
         } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(s);
-            w[0] = u.x, w[1] = u.y;
+            f0 = reinterpret_cast<const uint32_t*>(src)[c];
+            f1 = f0 >> 16;
         }
-        pp_expand32<BITS>(w, r, hi, lo, tile, half_bytes, row, qq);
+        unsigned char* d0 = dst + (uint32_t)(c >> 2) * half_bytes;
+        const uint32_t at = ((uint32_t)(c & 3) << 5) ^ sw;
+        pp_expand8<BITS, LOW>(f0, r, rl, hi, lo, d0 + at);
+        pp_expand8<BITS, LOW>(f1, r, rl, hi, lo, d0 + (at ^ 16u));
     }
 }
 
-template <int D, int TPR>
+template <int D, int TPR, bool LOW>
 __device__ __forceinline__ void pp_expand(int bits, const unsigned char* rows, float rf, const uint32_t* hi,
                                           const uint32_t* lo, unsigned char* tile, uint32_t half_bytes, int row,
                                           int sub) {
-    if (bits == 4) pp_expand_row<4, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
-    else if (bits == 3) pp_expand_row<3, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
-    else pp_expand_row<2, D, TPR>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+    if (bits == 4) pp_expand_row<4, D, TPR, LOW>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+    else if (bits == 3) pp_expand_row<3, D, TPR, LOW>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+    else pp_expand_row<2, D, TPR, LOW>(rows, rf, hi, lo, tile, half_bytes, row, sub);
+}
+
+__device__ __forceinline__ float pp_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The largest of 32 values, NaN left out, in four chains.
+__device__ __forceinline__ float pp_max32(const uint32_t (&s)[32]) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[4 + k]));
+#pragma unroll
+    for (int j = 8; j < 32; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = pp_max3(m[k], __uint_as_float(s[j + k]), __uint_as_float(s[j + 4 + k]));
+    return fmaxf(pp_max3(m[0], m[1], m[2]), m[3]);
+}
+
+// 32 bytes of global memory in one load.
+__device__ __forceinline__ void pp_ld256(const void* p, uint32_t* u) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(p));
+}
+
+// Flip y[j] where bit j of the words is set.
+template <int E>
+__device__ __forceinline__ void pp_signs(float (&y)[E], const uint32_t* bits) {
+#pragma unroll
+    for (int w = 0; w < E / 32; ++w) {
+        const uint32_t b = bits[w];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            y[32 * w + k] = __uint_as_float(__float_as_uint(y[32 * w + k]) ^ ((b << (31 - k)) & 0x80000000u));
+    }
+}
+
+// A piece of a row to and from this lane's tensor-memory columns.
+template <int E>
+__device__ __forceinline__ void pp_store_row(uint32_t t, const float (&y)[E]) {
+#pragma unroll
+    for (int c = 0; c < E / 32; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[32 * c + k]);
+        tmem_st32(t + 32 * c, o);
+    }
+}
+template <int E>
+__device__ __forceinline__ void pp_load_row(uint32_t t, float (&y)[E]) {
+#pragma unroll
+    for (int c = 0; c < E / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(t + 32 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[32 * c + k] = __uint_as_float(o[k]);
+    }
+}
+
+// 16 columns of each of a row's pieces (64 columns apart), and the
+// transform's stages across the pieces.
+template <int PARTS>
+__device__ __forceinline__ void pp_across(uint32_t t, uint32_t (&y)[PARTS][16]) {
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) tmem_ld16(t + 64 * h, y[h]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int len = 1; len < PARTS; len *= 2)
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h)
+            if (!(h & len)) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float u = __uint_as_float(y[h][k]), v = __uint_as_float(y[h + len][k]);
+                    y[h][k] = __float_as_uint(u + v);
+                    y[h + len][k] = __float_as_uint(u - v);
+                }
+            }
+}
+
+// Scores outside columns [c0, c1) of 32 become -inf.
+__device__ __forceinline__ void pp_mask(uint32_t (&s)[32], int c0, int c1) {
+    const uint32_t on = (c1 >= 32 ? 0xFFFFFFFFu : c1 <= 0 ? 0u : (1u << c1) - 1u) &
+                        (c0 <= 0 ? 0xFFFFFFFFu : c0 >= 32 ? 0u : ~((1u << c0) - 1u));
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[k] = (on >> k) & 1u ? s[k] : 0xFF800000u;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -406,7 +539,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
     constexpr int E = D < 64 ? D : 64;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t sa = smem_addr(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in a warp
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Z::kBar);
     uint64_t* stage_full = bars;              // [NS] the block's packed rows have landed
     uint64_t* stage_free = stage_full + NS;   // [NS] the expansion has read them
@@ -416,8 +550,11 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
     uint64_t* s_full = meta_full + 4;         // [2] scores of the buffer's step are done
     uint64_t* p_full = s_full + 2;            // [2] the softmax warps wrote P over them
     uint64_t* pv_done = p_full + 2;           // [2] its PV product is done
-    uint64_t* q_full = pv_done + 2;           // the item's queries are in shared memory
-    uint64_t* drain = q_full + 1;             // products in flight, on the abort path
+    uint64_t* job_full = pv_done + 2;         // [2] a job is written
+    uint64_t* job_free = job_full + 2;        // [2] every warp has read it
+    uint64_t* q_full = job_free + 2;          // the item's queries are in shared memory
+    uint64_t* meet = q_full + 1;              // all softmax warps are here
+    uint64_t* drain = meet + 1;               // products in flight, on the abort path
     volatile int* abort_f = reinterpret_cast<volatile int*>(sm + Z::kMisc + 4);
     uint32_t* slot = reinterpret_cast<uint32_t*>(sm + Z::kMisc);
     PpCursor* start = reinterpret_cast<PpCursor*>(sm + Z::kCur);
@@ -443,7 +580,12 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&job_full[i], 1);
+            mbar_init(&job_free[i], SW + 9);
+        }
         mbar_init(q_full, SW);
+        mbar_init(meet, SW);
         mbar_init(drain, 1);
         *abort_f = 0;
         mbar_fence_init();
@@ -508,10 +650,27 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
-    PpCursor cur = *start;
-    PpSeq<D> seq;
-    if (cur.left > 0) seq.load(A, cur.b, nullptr);
-    PpPart p;
+    PpJob p;
+    int job = 0;
+    // The next job; false at the end.
+    auto next_job = [&]() {
+        const bool ok = pp_wait(&job_full[job & 1], (job >> 1) & 1, abort_f, status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        const volatile PpJob* m = reinterpret_cast<const volatile PpJob*>(sm + Z::kJobs) + (job & 1);
+        p.nb = m->nb;
+        p.flags = m->flags;
+        p.q0 = m->q0;
+        p.h = m->h;
+        p.row0 = m->row0;
+        p.rows = m->rows;
+        p.blk = m->blk;
+        p.kv_end = m->kv_end;
+        p.pos0 = m->pos0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&job_free[job & 1]);
+        ++job;
+        return p.nb >= 0;
+    };
 
     if (warp == SW + 9) {
         // ---- copies: lane 4 s + a brings array a of segment s (min(page, N)
@@ -523,31 +682,57 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             a == 0 ? (const void*)A.c.k_packed : a == 1 ? (const void*)A.c.v_packed : a == 2 ? (const void*)A.c.k_norm
                                                                                              : (const void*)A.c.v_norm);
         const uint32_t at = a == 0 ? 0u : a == 1 ? N * D / 2 : a == 2 ? N * D : N * D + 4 * N;
+        PpCursor cur = *start;
+        PpSeq<D> seq;
+        if (cur.left > 0) seq.load(A, cur.b, nullptr);
         uint32_t tc = 0;
+        int has = 0;  // parts left in the workspace
         bool ok = true;
-        while (ok && pp_next<D>(A, cur, seq, p)) {
-            for (int j = p.blk0; j < p.blk1; ++j, ++tc) {
+        for (; ok; ++job) {
+            PpPart u;
+            const bool more = pp_next<D>(A, cur, seq, u);
+            if (job >= 2) ok = pp_wait(&job_free[job & 1], ((job >> 1) - 1) & 1, abort_f, status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                volatile PpJob* m = reinterpret_cast<volatile PpJob*>(sm + Z::kJobs) + (job & 1);
+                m->nb = more ? u.blk1 - u.blk0 : -1;
+                if (more) {
+                    m->flags = (u.pair ? kJobPair : 0) | (u.whole ? kJobWhole : 0) | (u.head ? kJobHead : 0);
+                    m->q0 = __ldg(A.cu + u.b);
+                    m->h = u.h;
+                    m->row0 = u.row0;
+                    m->rows = u.rows;
+                    m->blk = u.lo_blk + u.blk0;
+                    m->kv_end = u.kv_end;
+                    m->pos0 = seq.ctx - seq.n;
+                }
+                mbar_arrive(&job_full[job & 1]);
+            }
+            __syncwarp();
+            if (!more) break;
+            if (!u.whole) has |= u.head ? 2 : 1;
+            for (int j = u.blk0; j < u.blk1; ++j, ++tc) {
                 const int st = tc % NS;
-                const int pos = (p.lo_blk + j) * N + s * seg;
-                bool have = s < nseg && pos < p.kv_end;
+                const int pos = (u.lo_blk + j) * N + s * seg;
+                bool have = s < nseg && pos < u.kv_end;
                 int64_t src = 0;
                 if (have) {
-                    const int page = __ldg(A.bt + (int64_t)p.b * A.max_pages + (pos >> A.shift));
+                    const int page = __ldg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift));
                     if (page < 0 || page >= A.c.n_pages) {
                         report_timeout(status, kPpStatusPage);
                         have = false;
                     }
-                    src = (((int64_t)page * A.Hkv + p.h) << A.shift) + (pos & ((1 << A.shift) - 1));
+                    src = (((int64_t)page * A.Hkv + u.h) << A.shift) + (pos & ((1 << A.shift) - 1));
                 }
                 if (tc >= (uint32_t)NS) ok = pp_wait(&stage_free[st], (tc / NS - 1) & 1, abort_f, status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t bytes = have ? row_bytes * seg : 0u;
-                uint32_t all = bytes;
-                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+                const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
                 const uint32_t mask = __ballot_sync(0xFFFFFFFFu, have && a == 0);
                 if (lane == 0) {
-                    reinterpret_cast<uint32_t*>(sm + Z::kSegs)[st] = mask;  // bit 4 s: segment s is there
+                    reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st] = mask;  // bit 4 s: segment s is there
                     mbar_arrive_expect_tx(&stage_full[st], all);
                 }
                 __syncwarp();
@@ -556,71 +741,111 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                               &stage_full[st]);
             }
         }
+        // which parts this share left, and the item it owns: the one that starts
+        // in this share and ends in a later one
+        if (lane == 0) {
+            int32_t* m = A.meta + (int64_t)blockIdx.x * kPpMeta;
+            m[kMetaHas0] = has & 1;
+            m[kMetaHas1] = has >> 1;
+            bool owner = ok && cur.off > 0 &&
+                         !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
+            if (owner) {
+                const int64_t w = seq.weight(cur.i), per = *share;
+                const int nblk = pp_blocks<D>(A, seq, cur.i);
+                int last = blockIdx.x;
+                // no join where one share has all of the item's blocks
+                owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
+                for (int64_t x = cur.off; x < w; x += per) {
+                    ++last;
+                    if (pp_cut(nblk, x, w) == 0 && pp_cut(nblk, min(w, x + per), w) == nblk) owner = false;
+                }
+                m[kMetaB] = cur.b;
+                m[kMetaI] = cur.i;
+                m[kMetaH] = cur.h;
+                m[kMetaLast] = last;
+            }
+            m[kMetaOwner] = owner;
+        }
         // the copies issued have landed before the CTA leaves (bounded)
         if (lane == 0 && tc > 0)
             for (uint32_t t = tc > (uint32_t)NS ? tc - NS : 0; t < tc; ++t) mbar_wait(&stage_full[t % NS], (t / NS) & 1);
     } else if (warp == SW + 8) {
-        // ---- MMAs
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_f16(128, N, false);
-            constexpr uint32_t idesc_o = umma_idesc_f16(128, W, false) | kIdescBTransposed;
-            uint32_t tc0 = 0, items = 0;
-            uint32_t np[2] = {0, 0}, npv[2] = {0, 0};  // P waits and PV products per buffer
-            bool ok = true;
-            while (ok && pp_next<D>(A, cur, seq, p)) {
-                const int nb = p.blk1 - p.blk0;
-                if (nb == 0) continue;
-                ok = pp_wait(q_full, items & 1, abort_f, status);
-                ++items;
-                const int T = p.pair ? 2 * nb : nb;
-                for (int t = 0; ok && t < T + 2; ++t) {
-                    const int g = t & 1;
-                    if (t >= 2) {
-                        const int u = t - 2, j = p.pair ? u >> 1 : u;
-                        const uint32_t tc = tc0 + j, sl = (2 * tc + 1) & 3;
-                        ok = pp_wait(&p_full[g], np[g] & 1, abort_f, status) &&
-                             pp_wait(&kv_full[sl], (tc >> 1) & 1, abort_f, status);
-                        if (!ok) break;
-                        ++np[g];
-                        tc_fence_after();
-                        const uint32_t vt = sa + Z::kRing + sl * Z::kTile;
-                        const uint32_t o = tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0);
-                        const bool first = Z::kStreams == 2 ? u < 2 : u == 0;  // the output's first product
+        // ---- MMAs.  The whole warp walks through the steps and one elected lane
+        // issues: with a warp-uniform flow the descriptors are computed in
+        // uniform registers and the products follow one another at the tensor
+        // cores' rate (64 cycles for M = N = 128, K = 16, shared-memory or
+        // tensor-memory A, either order of B); inside a one-thread branch each
+        // took 150 to 250 cycles to issue.
+        constexpr uint32_t idesc_s = umma_idesc_f16(128, N, false);
+        constexpr uint32_t idesc_o = umma_idesc_f16(128, W, false) | kIdescBTransposed;
+        const uint32_t elected = elect_one();
+        const uint64_t dq = umma_desc_sw128(sa + Z::kQ), dk = umma_desc_sw128(sa + Z::kRing),
+                       dv = umma_desc_sw128_mn(sa + Z::kRing, N * 128);
+        uint32_t tc0 = 0, items = 0;
+        uint32_t np[2] = {0, 0};  // steps of each buffer whose P was taken
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, pp_wait(bar, parity, abort_f, status));
+        };
+        while (ok && next_job()) {
+            const int nb = p.nb;
+            const bool pair = p.flags & kJobPair;
+            if (nb == 0) continue;
+            ok = wait(q_full, items & 1);
+            ++items;
+            const int T = pair ? 2 * nb : nb;
+            for (int t = 0; ok && t < T + 2; ++t) {
+                const int g = t & 1;
+                const bool frees = !pair || g == 1;  // the last step that reads the tile
+                if (t >= 2) {
+                    const int u = t - 2, j = pair ? u >> 1 : u;
+                    const uint32_t tc = tc0 + j, sl = (2 * tc + 1) & 3;
+                    const uint32_t n = g ? np[1]++ : np[0]++;
+                    ok = wait(&kv_full[sl], (tc >> 1) & 1) && wait(&p_full[g], n & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vt = uniform(dv + ((sl * Z::kTile) >> 4));
+                    const uint32_t o = uniform(tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0));
+                    const uint32_t pa = uniform(tmem + Z::kTmemS + N * g);
+                    // 0 for the output's first product
+                    const uint32_t more = uniform((Z::kStreams == 2 ? u < 2 : u == 0) ? 0u : 1u);
+                    if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < N / 16; ++kk)
-                            umma_f16_ts(o, tmem + Z::kTmemS + N * g + 8 * kk,
-                                        umma_desc_sw128_mn(vt + kk * 2048, N * 128), idesc_o,
-                                        (!first || kk > 0) ? 1u : 0u);
+                            umma_f16_ts(o, pa + 8 * kk, vt + ((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
                         umma_commit(&pv_done[g]);
-                        if (!p.pair || g == 1) umma_commit(&kv_free[sl]);
-                        ++npv[g];
-                        if (t < T) ok = pp_wait(&pv_done[g], (npv[g] - 1) & 1, abort_f, status);
-                        if (!ok) break;
+                        if (frees) umma_commit(&kv_free[sl]);
                     }
-                    if (t < T) {
-                        const int j = p.pair ? t >> 1 : t;
-                        const uint32_t tc = tc0 + j, sl = (2 * tc) & 3;
-                        ok = pp_wait(&kv_full[sl], (tc >> 1) & 1, abort_f, status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t kt = sa + Z::kRing + sl * Z::kTile;
-                        const uint32_t qt = sa + Z::kQ + (p.pair ? g * Z::kQTile : 0);
-                        const uint32_t d = tmem + Z::kTmemS + N * g;
+                    __syncwarp();
+                    if (t < T) ok = wait(&pv_done[g], n & 1);
+                    if (!ok) break;
+                }
+                if (t < T) {
+                    const int j = pair ? t >> 1 : t;
+                    const uint32_t tc = tc0 + j, sl = (2 * tc) & 3;
+                    ok = wait(&kv_full[sl], (tc >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t kt = uniform(dk + ((sl * Z::kTile) >> 4));
+                    const uint64_t qt = uniform(dq + ((pair && g ? Z::kQTile : 0u) >> 4));
+                    const uint32_t d = uniform(tmem + Z::kTmemS + N * g);
+                    if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < W / 16; ++kk)
-                            umma_f16(d, umma_desc_sw128(qt + (kk >> 2) * 16384 + (kk & 3) * 32),
-                                     umma_desc_sw128(kt + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc_s,
-                                     kk > 0 ? 1u : 0u);
+                            umma_f16(d, qt + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                     kt + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                         umma_commit(&s_full[g]);
-                        if (!p.pair || g == 1) umma_commit(&kv_free[sl]);
+                        if (frees) umma_commit(&kv_free[sl]);
                     }
+                    __syncwarp();
                 }
-                tc0 += nb;
             }
-            if (!ok) {  // products in flight finish before the tensor memory is freed (bounded)
-                umma_commit(drain);
-                mbar_wait(drain, 0);
-            }
+            tc0 += nb;
+        }
+        if (!ok) {  // products in flight finish before the tensor memory is freed (bounded)
+            if (elected) umma_commit(drain);
+            __syncwarp();
+            mbar_wait(drain, 0);
         }
     } else if (warp >= SW) {
         // ---- expansion: thread = (row, sub) of the block
@@ -634,9 +859,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         }
         uint32_t tc = 0;
         bool ok = true;
-        while (ok && pp_next<D>(A, cur, seq, p)) {
+        while (ok && next_job()) {
             int eprev = 0, emax = -1000;
-            for (int j = p.blk0; j < p.blk1; ++j, ++tc) {
+            for (int j = 0; j < p.nb; ++j, ++tc) {
                 const int st = tc % NS;
                 const unsigned char* stg = sm + Z::kStg + st * Z::kStage;
                 const float* knp = reinterpret_cast<const float*>(stg + N * D);
@@ -647,7 +872,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                     break;
                 }
                 const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
-                const int t0 = (p.lo_blk + j) * N;
+                const int t0 = (p.blk + j) * N;
                 const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
                 auto there = [&](int k) { return t0 + k < p.kv_end && ((segs >> (4 * (k >> seg_sh))) & 1u); };
                 // the block's largest finite norms (each warp for itself)
@@ -689,7 +914,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                     reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 3] = make_float2(pp_pow2(ek), (float)ev);
                     mbar_arrive(&meta_full[tc & 3]);
                 }
-                pp_expand<D, TPR>(A.k_bits, stg, rk, A.khi, A.klo, sm + Z::kRing + slk * Z::kTile, N * 128, row, sub);
+                pp_expand<D, TPR, true>(A.k_bits, stg, rk, A.khi, A.klo, sm + Z::kRing + slk * Z::kTile, N * 128, row, sub);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kv_full[slk]);
@@ -698,7 +923,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                     ok = false;
                     break;
                 }
-                pp_expand<D, TPR>(A.v_bits, stg + N * D / 2, rv, A.vhi, A.vlo, sm + Z::kRing + slv * Z::kTile, N * 128,
+                pp_expand<D, TPR, false>(A.v_bits, stg + N * D / 2, rv, A.vhi, A.vlo, sm + Z::kRing + slv * Z::kTile, N * 128,
                                   row, sub);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -716,49 +941,56 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         const int G = A.Hq / A.Hkv;
         const float q_sign = P.q_mul > 0.f ? 1.f : (P.q_mul < 0.f ? -1.f : 0.f);
         const float q_abs = P.q_mul == 0.f ? 1.f : fabsf(P.q_mul);
-        uint32_t ns[2] = {0, 0}, npv[2] = {0, 0}, tc0 = 0;
-        int part_no = 0;
-        while (pp_next<D>(A, cur, seq, p)) {
-            const int nb = p.blk1 - p.blk0;
+        uint32_t ns[2] = {0, 0}, npv[2] = {0, 0}, tc0 = 0, met = 0;
+        // All softmax warps arrive and wait for one another (bounded).
+        auto meet_all = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(meet);
+            pp_wait(meet, met & 1, abort_f, status);
+            ++met;
+            __syncwarp();
+            tc_fence_after();
+        };
+        while (next_job()) {
+            const int nb = p.nb;
+            const bool pair = p.flags & kJobPair, split = Z::kStreams == 2 && !pair;
             // the row of this thread: in split mode both streams have row r
-            const int lrow = p.pair ? 128 * g + r : r;
+            const int lrow = pair ? 128 * g + r : r;
             const bool rvalid = lrow < p.rows;
-            const int grow = p.row0 + lrow;
-            const int tok = rvalid ? grow / G : 0, hd = rvalid ? grow - tok * G : 0;
-            const int64_t qrow = ((int64_t)__ldg(A.cu + p.b) + tok) * A.Hq + (int64_t)p.h * G + hd;
-            const int pos = rvalid ? seq.ctx - seq.n + tok : -1;
+            const int tok = rvalid ? (p.row0 + lrow) / G : 0, hd = rvalid ? p.row0 + lrow - tok * G : 0;
+            const int64_t qrow = ((int64_t)p.q0 + tok) * A.Hq + (int64_t)p.h * G + hd;
+            const int pos = rvalid ? p.pos0 + tok : -1;
             const int lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
             // ---- queries: rotated in registers and tensor memory (the output
             // columns, free until the item's first product), 64 dims at a time,
             // and rounded to fp16 under a power of two per row
             float cq = q_abs;
-            if (nb > 0 && (p.pair || g == 0)) {
+            if (nb > 0 && (pair || g == 0)) {
                 float amax = 0.f;
-                const uint4* src = reinterpret_cast<const uint4*>(A.q + qrow * D);
-#pragma unroll
+                const __nv_bfloat16* src = A.q + qrow * D;
+#pragma unroll 1
                 for (int h = 0; h < PARTS; ++h) {
                     float y[E];
+                    {
+                        uint32_t u[E / 2];
 #pragma unroll
-                    for (int k = 0; k < E / 8; ++k) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (rvalid) u = __ldg(src + (64 * h) / 8 + k);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+                        for (int k = 0; k < E / 16; ++k) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            y[8 * k + 2 * c] = __uint_as_float((uu[c] << 16) ^ P.sgn[64 * h + 8 * k + 2 * c]);
-                            y[8 * k + 2 * c + 1] =
-                                __uint_as_float((uu[c] & 0xFFFF0000u) ^ P.sgn[64 * h + 8 * k + 2 * c + 1]);
-                            amax = fmaxf(amax, fmaxf(fabsf(y[8 * k + 2 * c]), fabsf(y[8 * k + 2 * c + 1])));
+                            for (int c = 0; c < 8; ++c) u[8 * k + c] = 0u;
+                            if (rvalid) pp_ld256(src + 64 * h + 16 * k, u + 8 * k);
+                        }
+#pragma unroll
+                        for (int k = 0; k < E / 2; ++k) {
+                            y[2 * k] = __uint_as_float(u[k] << 16);
+                            y[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
                         }
                     }
+#pragma unroll
+                    for (int k = 0; k < E; k += 2) amax = pp_max3(amax, fabsf(y[k]), fabsf(y[k + 1]));
+                    pp_signs<E>(y, P.sgnb + 2 * h);
                     fwht_reg2<E>(y);
-                    uint32_t o[32];
-#pragma unroll
-                    for (int c = 0; c < E / 32; ++c) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[32 * c + k]);
-                        tmem_st32(t_out + 64 * h + 32 * c, o);
-                    }
+                    pp_store_row<E>(t_out + 64 * h, y);
                 }
                 tmem_wait_st();
                 // |rotated| <= D amax: below 2^14 after the scaling by 2^-e
@@ -769,58 +1001,41 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 }
                 cq = q_abs * pp_pow2(e);
                 const float inv = q_sign * pp_pow2(-e);
-                unsigned char* qt = sm + Z::kQ + (p.pair ? g * Z::kQTile : 0);
-#pragma unroll
+                unsigned char* qt = sm + Z::kQ + (pair ? g * Z::kQTile : 0) + r * 128;
+#pragma unroll 1
                 for (int c = 0; c < E / 16; ++c) {
                     uint32_t y[PARTS][16];
-#pragma unroll
-                    for (int h = 0; h < PARTS; ++h) tmem_ld16(t_out + 64 * h + 16 * c, y[h]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int len = 1; len < PARTS; len *= 2)
-#pragma unroll
-                        for (int h = 0; h < PARTS; ++h)
-                            if (!(h & len)) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const float u = __uint_as_float(y[h][k]), v = __uint_as_float(y[h + len][k]);
-                                    y[h][k] = __float_as_uint(u + v);
-                                    y[h + len][k] = __float_as_uint(u - v);
-                                }
-                            }
+                    pp_across<PARTS>(t_out + 16 * c, y);
 #pragma unroll
                     for (int h = 0; h < PARTS; ++h) {
+                        const uint32_t flip = P.two_sided ? (P.sgn2b[2 * h + (c >> 1)] >> (16 * (c & 1))) & 0xFFFFu : 0u;
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const int j = 64 * h + 16 * c + 2 * k;
-                            float v0 = __uint_as_float(y[h][2 * k]) * inv, v1 = __uint_as_float(y[h][2 * k + 1]) * inv;
-                            if (P.two_sided) {
-                                v0 = __uint_as_float(__float_as_uint(v0) ^ P.sgn2[j]);
-                                v1 = __uint_as_float(__float_as_uint(v1) ^ P.sgn2[j + 1]);
-                            }
-                            const __half2 hh = __floats2half2_rn(v0, v1);
-                            w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                            const __half2 hh = __floats2half2_rn(__uint_as_float(y[h][2 * k]) * inv,
+                                                                 __uint_as_float(y[h][2 * k + 1]) * inv);
+                            // signs of dims 2 k and 2 k + 1 onto bits 15 and 31
+                            const uint32_t sg = ((flip << (15 - 2 * k)) & 0x8000u) | ((flip << (30 - 2 * k)) & 0x80000000u);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&hh) ^ sg;
                         }
-                        const int k8 = 8 * h + 2 * c;
-                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        unsigned char* qh = qt + h * 16384;
+                        *reinterpret_cast<uint4*>(qh + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(qh + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
                 if constexpr (D < 64) {
 #pragma unroll
                     for (int k8 = D / 8; k8 < 8; ++k8)
-                        *reinterpret_cast<uint4*>(qt + pp_chunk(16384, r, k8)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(qt + ((k8 ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
-            if (Z::kStreams == 2 && !p.pair && nb > 0) {
+            float* xs = reinterpret_cast<float*>(sm + Z::kQ + Z::kQTile);  // split mode: row tile 1 is free
+            if (split && nb > 0) {
                 // stream 1 has the same rows: it takes their factor from stream 0
-                float* xs = reinterpret_cast<float*>(sm + Z::kQ + Z::kQTile);
-                if (g == 0) xs[r] = cq;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (g == 1) cq = xs[r];
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (g == 0) xs[384 + r] = cq;
+                meet_all();
+                if (g == 1) cq = xs[384 + r];
             }
             tc_fence_before();
             __syncwarp();
@@ -829,7 +1044,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             // ---- the steps
             float M = -INFINITY, l = 0.f, eb = 0.f;
             int lastb = -1;  // buffer of this stream's last step
-            for (int j = (Z::kStreams == 2 && !p.pair) ? g : 0; j < nb; j += (Z::kStreams == 2 && !p.pair) ? 2 : 1) {
+            for (int j = split ? g : 0; j < nb; j += split ? 2 : 1) {
                 const int buf = Z::kStreams == 2 ? g : (j & 1);
                 const uint32_t tc = tc0 + j;
                 pp_wait(&meta_full[tc & 3], (tc >> 2) & 1, abort_f, status);
@@ -841,26 +1056,18 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
-                const int t0 = (p.lo_blk + p.blk0 + j) * N;
+                const int t0 = (p.blk + j) * N;
                 // columns [c0, c1) of the block are this row's
                 const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
                 const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
                 float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < N / 32; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < N; c += 32) {
                     uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_ld32(t_s + c, s);
                     tmem_wait_ld();
-                    if (full) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int col = 32 * c + k;
-                            if (col >= c0 && col < c1) mx = fmaxf(mx, __uint_as_float(s[k]));
-                        }
-                    }
+                    if (!full) pp_mask(s, c0 - c, c1 - c);
+                    mx = fmaxf(mx, pp_max32(s));
                 }
                 const float cs = cq * meta.x;
                 const float cand = mx * cs + meta.y;  // -inf where nothing is attended
@@ -872,33 +1079,27 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                         pp_wait(&pv_done[buf ^ 1], (npv[buf ^ 1] - 1) & 1, abort_f, status);
                     __syncwarp();
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < W / 32; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < W; c += 32) {
                         uint32_t o[32];
-                        tmem_ld32(t_out + 32 * c, o);
+                        tmem_ld32(t_out + c, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st32(t_out + 32 * c, o);
+                        tmem_st32(t_out + c, o);
                     }
                     l *= alpha;
                 }
                 if (move) M = cand;
                 const float off = M == -INFINITY ? 0.f : meta.y - M;
                 const F2 CS = f2(cs, cs), OFF = f2(off, off);
-                F2 sum = f2(0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < N / 32; ++c) {
+                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+                for (int c = 0; c < N; c += 32) {
                     uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_ld32(t_s + c, s);
                     tmem_wait_ld();
-                    if (!full) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int col = 32 * c + k;
-                            if (!(col >= c0 && col < c1)) s[k] = 0xFF800000u;  // -inf
-                        }
-                    }
+                    if (!full) pp_mask(s, c0 - c, c1 - c);
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -906,11 +1107,11 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                         f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), CS, OFF), a0, a1);
                         a0 = pp_exp2(a0);
                         a1 = pp_exp2(a1);
-                        sum = f2_add(sum, f2(a0, a1));
+                        sum[k & 1] = f2_add(sum[k & 1], f2(a0, a1));
                         const __half2 hh = __floats2half2_rn(a0, a1);
                         w[k] = *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    tmem_st16(t_s + 16 * c, w);
+                    tmem_st16(t_s + c / 2, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -918,7 +1119,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 if (lane == 0) mbar_arrive(&p_full[buf]);
                 ++npv[buf];
                 float s0, s1;
-                f2_split(sum, s0, s1);
+                f2_split(f2_add(sum[0], sum[1]), s0, s1);
                 l = fmaf(s0 + s1, pp_exp2(eb - meta.y), l);
                 lastb = buf;
             }
@@ -929,136 +1130,99 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             __syncwarp();
             tc_fence_after();
             // ---- split mode: stream 0 adds stream 1's output and sums to its own
-            if (Z::kStreams == 2 && !p.pair && nb > 0) {
-                float* xs = reinterpret_cast<float*>(sm + Z::kQ + Z::kQTile);
+            if (split && nb > 0) {
                 if (g == 1) {
                     xs[r] = M;
                     xs[128 + r] = l;
                     xs[256 + r] = eb;
                 }
-                tc_fence_before();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                tc_fence_after();
+                meet_all();
                 if (g == 0 && nb > 1) {
                     const float M1 = xs[r], l1 = xs[128 + r], eb1 = xs[256 + r];
                     const float Mx = fmaxf(M, M1);
                     const float a0 = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = M1 == -INFINITY ? 0.f : pp_exp2(M1 - Mx);
-#pragma unroll
-                    for (int c = 0; c < W / 32; ++c) {
-                        uint32_t o[32], o1[32];
-                        tmem_ld32(t_out + 32 * c, o);
-                        tmem_ld32(t_out + 128 + 32 * c, o1);
+#pragma unroll 1
+                    for (int c = 0; c < W; c += 16) {
+                        uint32_t o[16], o1[16];
+                        tmem_ld16(t_out + c, o);
+                        tmem_ld16(t_out + 128 + c, o1);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
+                        for (int k = 0; k < 16; ++k)
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * a0 + __uint_as_float(o1[k]) * a1);
-                        tmem_st32(t_out + 32 * c, o);
+                        tmem_st16(t_out + c, o);
                     }
                     tmem_wait_st();
                     l = (M == -INFINITY ? l : l * a0) + (M1 == -INFINITY ? l1 : l1 * a1) * pp_exp2(eb - eb1);
                     M = Mx;
                 }
-                tc_fence_before();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                tc_fence_after();
+                meet_all();
             }
             // ---- the rows leave: finished, or as a part
-            if (p.pair || g == 0) {
-                if (p.whole) {
-                    const float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
-                    if (nb == 0) {
-#pragma unroll
-                        for (int c = 0; c < W / 32; ++c) {
-                            uint32_t o[32];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = 0u;
-                            tmem_st32(t_out + 32 * c, o);
-                        }
-                        tmem_wait_st();
-                    }
+            if (pair || g == 0) {
+                if (p.flags & kJobWhole) {
+                    float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
                     // rotated back, s . H (s2 . o): 64 dims at a time, then across
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < PARTS; ++h) {
                         float y[E];
-                        uint32_t o[32];
+                        pp_load_row<E>(t_out + 64 * h, y);
+                        if (nb == 0) {  // no position to attend to: the columns hold nothing of this item
 #pragma unroll
-                        for (int c = 0; c < E / 32; ++c) {
-                            tmem_ld32(t_out + 64 * h + 32 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int j = 64 * h + 32 * c + k;
-                                y[32 * c + k] = __uint_as_float(P.two_sided ? o[k] ^ P.sgn2[j] : o[k]);
-                            }
+                            for (int k = 0; k < E; ++k) y[k] = 0.f;
                         }
+                        if (P.two_sided) pp_signs<E>(y, P.sgn2b + 2 * h);
                         fwht_reg2<E>(y);
-#pragma unroll
-                        for (int c = 0; c < E / 32; ++c) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(y[32 * c + k]);
-                            tmem_st32(t_out + 64 * h + 32 * c, o);
-                        }
+                        pp_store_row<E>(t_out + 64 * h, y);
                     }
                     tmem_wait_st();
                     const bool write = rvalid && *abort_f == 0;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < E / 16; ++c) {
                         uint32_t y[PARTS][16];
-#pragma unroll
-                        for (int h = 0; h < PARTS; ++h) tmem_ld16(t_out + 64 * h + 16 * c, y[h]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int len = 1; len < PARTS; len *= 2)
-#pragma unroll
-                            for (int h = 0; h < PARTS; ++h)
-                                if (!(h & len)) {
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const float u = __uint_as_float(y[h][k]), v = __uint_as_float(y[h + len][k]);
-                                        y[h][k] = __float_as_uint(u + v);
-                                        y[h + len][k] = __float_as_uint(u - v);
-                                    }
-                                }
+                        pp_across<PARTS>(t_out + 16 * c, y);
                         if (write) {
 #pragma unroll
-                        for (int h = 0; h < PARTS; ++h) {
-                            const int j0 = 64 * h + 16 * c;
-                            float v[16];
+                            for (int h = 0; h < PARTS; ++h) {
+                                const uint32_t flip = P.sgnb[2 * h + (c >> 1)] >> (16 * (c & 1));
+                                uint32_t v[16];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                v[k] = __uint_as_float(__float_as_uint(__uint_as_float(y[h][k]) * inv) ^ P.sgn[j0 + k]);
-                            if (A.out_bf16) {
-                                uint32_t w[8];
+                                for (int k = 0; k < 16; ++k)
+                                    v[k] = __float_as_uint(__uint_as_float(y[h][k]) * inv) ^ ((flip << (31 - k)) & 0x80000000u);
+                                const int64_t at = qrow * D + 64 * h + 16 * c;
+                                if (A.out_bf16) {
+                                    uint32_t w[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const __nv_bfloat162 bb = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                                    w[k] = *reinterpret_cast<const uint32_t*>(&bb);
+                                    for (int k = 0; k < 8; ++k) {
+                                        const __nv_bfloat162 bb =
+                                            __floats2bfloat162_rn(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                                        w[k] = *reinterpret_cast<const uint32_t*>(&bb);
+                                    }
+                                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + at);
+                                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                } else {
+                                    uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.out) + at);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                                 }
-                                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + qrow * D + j0);
-                                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                            } else {
-                                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(A.out) + qrow * D + j0);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                             }
-                        }
                         }
                         __syncwarp();
                     }
                 } else {
-                    const int which = p.head ? 1 : 0;
+                    const int which = p.flags & kJobHead ? 1 : 0;
                     float* w = A.part + ((int64_t)blockIdx.x * 2 + which) * PagedPrefillGeo<D>::kPartFloats;
-                    float4* o4 = reinterpret_cast<float4*>(w);
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
+                    float4* o4 = reinterpret_cast<float4*>(w) + lrow;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
-                        tmem_ld16(t_out + 16 * c, o);
+                        tmem_ld16(t_out + c, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            o4[(4 * c + k) * Z::kRows + lrow] =
+                            o4[(c / 4 + k) * Z::kRows] =
                                 make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                             __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                     }
@@ -1069,32 +1233,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 }
                 tc_fence_before();
             }
-            if (!p.whole) part_no |= p.head ? 2 : 1;
             tc0 += nb;
-        }
-        // ---- which parts this share left, and the item it owns: the one that
-        // starts in this share and ends in a later one
-        if (tid == 0) {
-            int32_t* m = A.meta + (int64_t)blockIdx.x * kPpMeta;
-            m[kMetaHas0] = part_no & 1;
-            m[kMetaHas1] = part_no >> 1;
-            bool owner = cur.off > 0 && !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
-            if (owner) {
-                const int64_t w = seq.weight(cur.i), per = *share;
-                const int nblk = pp_blocks<D>(A, seq, cur.i);
-                int last = blockIdx.x;
-                // no join where one share has all of the item's blocks
-                owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
-                for (int64_t at = cur.off; at < w; at += per) {
-                    ++last;
-                    if (pp_cut(nblk, at, w) == 0 && pp_cut(nblk, min(w, at + per), w) == nblk) owner = false;
-                }
-                m[kMetaB] = cur.b;
-                m[kMetaI] = cur.i;
-                m[kMetaH] = cur.h;
-                m[kMetaLast] = last;
-            }
-            m[kMetaOwner] = owner;
         }
     }
     griddep_launch();
