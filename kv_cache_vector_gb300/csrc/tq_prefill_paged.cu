@@ -15,8 +15,10 @@
 //
 //   warps 0-7    softmax, one thread per query row (4 warps at d = 256)
 //   8 warps      expansion: bytes -> fp16 levels times the row's norm
-//   1 warp       MMAs (one thread)
-//   1 warp       copies of packed rows and norms from the pages (bulk copies)
+//   1 warp       MMAs
+//   1 warp       copies of packed rows and norms from the pages (bulk copies);
+//                it also walks along the CTA's parts and hands them out
+//   1 warp       the blocks' powers of two and the rows' factors
 //
 // The work is cut into equal shares, one per SM, along a line of all (query
 // tile, KV head, block of positions) units: a share may end inside an item.
@@ -73,7 +75,7 @@ struct PpGeo {
     static constexpr int kRows = PagedPrefillGeo<D>::kRows;
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kSoftWarps = 4 * kStreams;
-    static constexpr int kWarps = kSoftWarps + 10;
+    static constexpr int kWarps = kSoftWarps + 11;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = D <= 64 ? 4 : 2;   // staged packed blocks
     static constexpr uint32_t kTile = kN * kD * 2;    // an expanded K or V tile
@@ -82,14 +84,14 @@ struct PpGeo {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kQ + kStreams * kQTile;  // 4 tiles: K, V of two blocks
     static constexpr uint32_t kStg = kRing + 4 * kTile;
-    static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [4] float2: 2^Ek, Ev
-    static constexpr uint32_t kSegs = kMeta + 32;               // [kStages] segments staged
+    static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [8] float2: 2^Ek, Ev
+    static constexpr uint32_t kSegs = kMeta + 64;               // [kStages] segments staged
     static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
-    static constexpr uint32_t kRedBytes = 18 * 8 + 16;
+    static constexpr uint32_t kRedBytes = 20 * 8;
     static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
     static constexpr uint32_t kJobs = kCur + 64;                // [2] jobs
     static constexpr uint32_t kBar = kJobs + 2 * 48;
-    static constexpr int kBars = 2 * kStages + 4 + 4 + 4 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1;
+    static constexpr int kBars = 2 * kStages + 4 + 4 + 8 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr uint32_t kSmem = (kMisc + 8 + 127) / 128 * 128;
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // buffer b at kN b; output g at 128 g further
@@ -177,8 +179,10 @@ struct PpPart {
     bool head, whole;    // part starts the item; covers it
 };
 
+// The block at which a cut `off` units into an item of w units falls: any
+// rounding will do that never decreases and is the same for every CTA.
 __device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w) {
-    return off >= w ? nblk : (int)((int64_t)nblk * off / w);
+    return off >= w ? nblk : min(nblk, (int)((float)nblk * __fdividef((float)off, (float)w)));
 }
 
 // Blocks of row tile i, the first of them, and the end of its positions.
@@ -278,11 +282,25 @@ __device__ __forceinline__ uint64_t uniform(uint64_t v) {
     return ((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v);
 }
 
+// A try_wait that may suspend the warp for up to 100 us: the default limit is
+// short, and warps that spin take issue slots from the working ones.
+__device__ __forceinline__ bool pp_try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait; gives up at once when the CTA's abort flag is set.
 __device__ __forceinline__ bool pp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_f, int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (pp_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!pp_try_wait(bar, parity)) {
         if (*abort_f) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
             *abort_f = 1;
@@ -309,6 +327,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// The largest of 32 columns as fp32, NaN left out: the load's own reduction.
+__device__ __forceinline__ float tmem_max32(uint32_t taddr) {
+    uint32_t r[32];
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=f"(m)
+        : "r"(taddr));
+    // completes the load; naming its registers keeps them the load's until then
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+f"(m)::"memory");
+    return m;
+}
+
 // Shared-memory descriptor of the V tile as an N-major B operand (N = dims):
 // 128-byte swizzle, 64-dim columns `lbo` bytes apart (leading offset), groups
 // of 8 positions 1024 bytes apart (stride offset).
@@ -325,6 +361,16 @@ constexpr uint32_t kIdescBTransposed = 1u << 16;
 
 // ------------------------------------------------------------------ expansion
 
+// Byte permute whose selector nibbles are below 8 already (__byte_perm masks
+// them first).
+__device__ __forceinline__ uint32_t pp_prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+// Bits of b where m is set, of a elsewhere.
+__device__ __forceinline__ uint32_t pp_select(uint32_t a, uint32_t b, uint32_t m) { return (a & ~m) | (b & m); }
+
 // Four fp16 levels from four 4-bit selectors (nibbles of sel's low half) and
 // the level bytes: two byte permutes pick the high and the low bytes, two
 // interleave them.  4-bit indices: hi/lo hold the 8 positive levels; x has a 1
@@ -333,11 +379,11 @@ constexpr uint32_t kIdescBTransposed = 1u << 16;
 template <int BITS>
 __device__ __forceinline__ void pp_levels4(uint32_t sel, uint32_t x, const uint32_t* hi, const uint32_t* lo,
                                            uint32_t& p01, uint32_t& p23) {
-    uint32_t h = __byte_perm(hi[0], hi[1], sel);
-    const uint32_t l = __byte_perm(lo[0], lo[1], sel);
-    if constexpr (BITS == 4) h ^= __byte_perm(0x00000080u, 0u, x);
-    p01 = __byte_perm(l, h, 0x5140);
-    p23 = __byte_perm(l, h, 0x7362);
+    uint32_t h = pp_prmt(hi[0], hi[1], sel);
+    const uint32_t l = pp_prmt(lo[0], lo[1], sel);
+    if constexpr (BITS == 4) h ^= pp_prmt(0x00000080u, 0u, x);
+    p01 = pp_prmt(l, h, 0x5140);
+    p23 = pp_prmt(l, h, 0x7362);
 }
 
 // 8 indices (fp16 pairs of their levels times the row's norm) to 16 bytes at
@@ -355,13 +401,14 @@ __device__ __forceinline__ void pp_expand8(uint32_t f, __half2 r, __half2 rl, co
         x = t >> 3;
         sel = (f ^ ~(t - x)) & 0x77777777u;
     } else if constexpr (BITS == 3) {
-        sel = (f & 0xFFFu) | ((f << 4) & 0x0FFF0000u);
-        sel = (sel & 0x003F003Fu) | ((sel << 2) & 0x3F003F00u);
-        sel = (sel & 0x07070707u) | ((sel << 1) & 0x70707070u);
+        // 3-bit fields spread to nibbles; the bits between them are cleared last
+        sel = pp_select(f, f << 4, 0xFFFF0000u);
+        sel = pp_select(sel, sel << 2, 0xFF00FF00u);
+        sel = pp_select(sel, sel << 1, 0xF0F0F0F0u) & 0x77777777u;
     } else {
-        sel = (f & 0xFFu) | ((f << 8) & 0x00FF0000u);
-        sel = (sel & 0x000F000Fu) | ((sel << 4) & 0x0F000F00u);
-        sel = (sel & 0x03030303u) | ((sel << 2) & 0x30303030u);
+        sel = pp_select(f, f << 8, 0xFFFF0000u);
+        sel = pp_select(sel, sel << 4, 0xFF00FF00u);
+        sel = pp_select(sel, sel << 2, 0xF0F0F0F0u) & 0x33333333u;
     }
     uint32_t v[4];
     pp_levels4<BITS>(sel, x, hi, lo, v[0], v[1]);
@@ -546,8 +593,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
     uint64_t* stage_free = stage_full + NS;   // [NS] the expansion has read them
     uint64_t* kv_full = stage_free + NS;      // [4] a tile is expanded
     uint64_t* kv_free = kv_full + 4;          // [4] its products are done
-    uint64_t* meta_full = kv_free + 4;        // [4] the block's powers of two are written
-    uint64_t* s_full = meta_full + 4;         // [2] scores of the buffer's step are done
+    uint64_t* meta_full = kv_free + 4;        // [8] the block's row factors and powers of two are written
+    uint64_t* s_full = meta_full + 8;         // [2] scores of the buffer's step are done
     uint64_t* p_full = s_full + 2;            // [2] the softmax warps wrote P over them
     uint64_t* pv_done = p_full + 2;           // [2] its PV product is done
     uint64_t* job_full = pv_done + 2;         // [2] a job is written
@@ -573,8 +620,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         for (int i = 0; i < 4; ++i) {
             mbar_init(&kv_full[i], 8);
             mbar_init(&kv_free[i], 1);
-            mbar_init(&meta_full[i], 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&meta_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
@@ -582,7 +629,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&job_full[i], 1);
-            mbar_init(&job_free[i], SW + 9);
+            mbar_init(&job_free[i], SW + 10);
         }
         mbar_init(q_full, SW);
         mbar_init(meet, SW);
@@ -593,6 +640,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
     }
     if (warp == SW + 8) tmem_alloc<512>(slot);
 
+    griddep_wait();  // from here on: what earlier kernels wrote
     // ---- this CTA's share: the sequences' weights, scanned over the block
     {
         const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
@@ -618,7 +666,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             total += red[w];
         }
         before += incl - mine;
-        const long long per = (total + gridDim.x - 1) / gridDim.x;
+        // a little over total / grid: the last CTA's share may be smaller
+        const long long per = (long long)((float)total * (1.000001f / (float)gridDim.x)) + 1;
         const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
         if (tid == 0) *share = per;
         if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
@@ -641,15 +690,18 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             const long long w = q.weight(lo);
             start->b = b;
             start->i = lo;
-            start->h = (int)(v / w);
-            start->off = v % w;
+            int h = (int)((float)v / (float)w);  // v / w, to within one
+            h -= (long long)h * w > v;
+            h += (long long)(h + 1) * w <= v;
+            start->h = h;
+            start->off = v - (long long)h * w;
             start->left = u1 - u0;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = uniform(*slot);
     PpJob p;
     int job = 0;
     // The next job; false at the end.
@@ -782,60 +834,64 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         const uint64_t dq = umma_desc_sw128(sa + Z::kQ), dk = umma_desc_sw128(sa + Z::kRing),
                        dv = umma_desc_sw128_mn(sa + Z::kRing, N * 128);
         uint32_t tc0 = 0, items = 0;
-        uint32_t np[2] = {0, 0};  // steps of each buffer whose P was taken
+        uint32_t n0 = 0, n1 = 0;  // products of each buffer so far
         bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xFFFFFFFFu, pp_wait(bar, parity, abort_f, status));
-        };
+        // each lane for itself: the lanes agree once a step
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return pp_wait(bar, parity, abort_f, status); };
         while (ok && next_job()) {
-            const int nb = p.nb;
-            const bool pair = p.flags & kJobPair;
+            const int nb = (int)uniform((uint32_t)p.nb);
+            const bool pair = uniform((uint32_t)p.flags) & kJobPair;
             if (nb == 0) continue;
-            ok = wait(q_full, items & 1);
+            ok = __all_sync(0xFFFFFFFFu, wait(q_full, items & 1));
             ++items;
             const int T = pair ? 2 * nb : nb;
             for (int t = 0; ok && t < T + 2; ++t) {
                 const int g = t & 1;
-                const bool frees = !pair || g == 1;  // the last step that reads the tile
+                // a pair's second step reads the tiles that the first one waited
+                // for, and frees them
+                const bool first_use = !(pair && g), last_use = !pair || g;
+                const uint32_t tk = tc0 + (pair ? t >> 1 : t), tv = tk - (pair ? 1 : 2);  // blocks of S and PV
+                const uint32_t slk = (2 * tk) & 3, slv = (2 * tv + 1) & 3;
                 if (t >= 2) {
-                    const int u = t - 2, j = pair ? u >> 1 : u;
-                    const uint32_t tc = tc0 + j, sl = (2 * tc + 1) & 3;
-                    const uint32_t n = g ? np[1]++ : np[0]++;
-                    ok = wait(&kv_full[sl], (tc >> 1) & 1) && wait(&p_full[g], n & 1);
-                    if (!ok) break;
+                    const uint32_t n = g ? n1++ : n0++;
+                    if (first_use) ok = wait(&kv_full[slv], (tv >> 1) & 1) && ok;
+                    ok = wait(&p_full[g], n & 1) && ok;
                     tc_fence_after();
-                    const uint64_t vt = uniform(dv + ((sl * Z::kTile) >> 4));
-                    const uint32_t o = uniform(tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0));
-                    const uint32_t pa = uniform(tmem + Z::kTmemS + N * g);
+                    const uint64_t vt = dv + ((slv * Z::kTile) >> 4);
+                    const uint32_t o = tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0);
+                    const uint32_t pa = tmem + Z::kTmemS + N * g;
                     // 0 for the output's first product
-                    const uint32_t more = uniform((Z::kStreams == 2 ? u < 2 : u == 0) ? 0u : 1u);
+                    const uint32_t more = (Z::kStreams == 2 ? t < 4 : t == 2) ? 0u : 1u;
                     if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < N / 16; ++kk)
                             umma_f16_ts(o, pa + 8 * kk, vt + ((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
                         umma_commit(&pv_done[g]);
-                        if (frees) umma_commit(&kv_free[sl]);
+                        if (last_use) umma_commit(&kv_free[slv]);
                     }
                     __syncwarp();
-                    if (t < T) ok = wait(&pv_done[g], n & 1);
-                    if (!ok) break;
+                    if (t < T) {
+                        // the buffer takes the next scores once P has been read
+                        if (first_use) ok = wait(&kv_full[slk], (tk >> 1) & 1) && ok;
+                        ok = wait(&pv_done[g], n & 1) && ok;
+                    }
+                } else if (t < T && first_use) {
+                    ok = wait(&kv_full[slk], (tk >> 1) & 1);
                 }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 if (t < T) {
-                    const int j = pair ? t >> 1 : t;
-                    const uint32_t tc = tc0 + j, sl = (2 * tc) & 3;
-                    ok = wait(&kv_full[sl], (tc >> 1) & 1);
-                    if (!ok) break;
                     tc_fence_after();
-                    const uint64_t kt = uniform(dk + ((sl * Z::kTile) >> 4));
-                    const uint64_t qt = uniform(dq + ((pair && g ? Z::kQTile : 0u) >> 4));
-                    const uint32_t d = uniform(tmem + Z::kTmemS + N * g);
+                    const uint64_t kt = dk + ((slk * Z::kTile) >> 4);
+                    const uint64_t qt = dq + ((pair && g ? Z::kQTile : 0u) >> 4);
+                    const uint32_t d = tmem + Z::kTmemS + N * g;
                     if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < W / 16; ++kk)
                             umma_f16(d, qt + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                                      kt + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                         umma_commit(&s_full[g]);
-                        if (frees) umma_commit(&kv_free[sl]);
+                        if (last_use) umma_commit(&kv_free[slk]);
                     }
                     __syncwarp();
                 }
@@ -846,6 +902,60 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             if (elected) umma_commit(drain);
             __syncwarp();
             mbar_wait(drain, 0);
+        }
+    } else if (warp == SW + 10) {
+        // ---- norms: a block's powers of two, and its rows' factors in the
+        // norms' place
+        uint32_t tc = 0;
+        bool ok = true;
+        while (ok && next_job()) {
+            int eprev = 0, emax = -1000;
+            for (int j = 0; j < p.nb; ++j, ++tc) {
+                const int st = tc % NS;
+                float* knp = reinterpret_cast<float*>(sm + Z::kStg + st * Z::kStage + N * D);
+                float* vnp = knp + N;
+                ok = __all_sync(0xFFFFFFFFu, pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status));
+                if (!ok) break;
+                const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
+                const int lim = p.kv_end - (p.blk + j) * N;  // the block's positions below it count
+                const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
+                float kn[N / 32], vn[N / 32];
+                uint32_t mk = 0, mv = 0;  // the largest finite norms, as bits
+#pragma unroll
+                for (int k = 0; k < N / 32; ++k) {
+                    const int r = 32 * k + lane;
+                    const bool in = r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+                    kn[k] = in ? knp[r] : 0.f;
+                    vn[k] = in ? vnp[r] : 0.f;
+                    const uint32_t x = __float_as_uint(kn[k]) & 0x7FFFFFFFu, y = __float_as_uint(vn[k]) & 0x7FFFFFFFu;
+                    mk = max(mk, x < 0x7F800000u ? x : 0u);
+                    mv = max(mv, y < 0x7F800000u ? y : 0u);
+                }
+                mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+                mv = __reduce_max_sync(0xFFFFFFFFu, mv);
+                // below 2^e; the range keeps every factor of the kernel a normal fp32
+                auto exponent = [](uint32_t m) { return min(100, max(-100, (int)(m >> 23) - 126)); };
+                const int ek = mk ? exponent(mk) : 0;
+                int ev = mv ? exponent(mv) : eprev;
+                if (mv) {
+                    // a block of far smaller values rides on the largest so far
+                    ev = max(ev, emax - 60);
+                    emax = max(emax, ev);
+                    eprev = ev;
+                }
+                const float sk = pp_pow2(-ek), sv = pp_pow2(-ev);
+#pragma unroll
+                for (int k = 0; k < N / 32; ++k) {
+                    const int r = 32 * k + lane;
+                    knp[r] = fmaf(vn[k], 0.f, kn[k] * sk);  // NaN if either norm is not finite
+                    vnp[r] = fabsf(vn[k]) <= FLT_MAX ? vn[k] * sv : 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 7] = make_float2(pp_pow2(ek), (float)ev);
+                    mbar_arrive(&meta_full[tc & 7]);
+                }
+            }
         }
     } else if (warp >= SW) {
         // ---- expansion: thread = (row, sub) of the block
@@ -860,61 +970,20 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         uint32_t tc = 0;
         bool ok = true;
         while (ok && next_job()) {
-            int eprev = 0, emax = -1000;
             for (int j = 0; j < p.nb; ++j, ++tc) {
                 const int st = tc % NS;
                 const unsigned char* stg = sm + Z::kStg + st * Z::kStage;
-                const float* knp = reinterpret_cast<const float*>(stg + N * D);
-                const float* vnp = knp + N;
-                ok = pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
-                const int t0 = (p.blk + j) * N;
-                const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
-                auto there = [&](int k) { return t0 + k < p.kv_end && ((segs >> (4 * (k >> seg_sh))) & 1u); };
-                // the block's largest finite norms (each warp for itself)
-                float mk = 0.f, mv = 0.f;
-#pragma unroll
-                for (int k = 0; k < N / 32; ++k) {
-                    const int kk = 32 * k + lane;
-                    if (there(kk)) {
-                        const float x = fabsf(knp[kk]), y = fabsf(vnp[kk]);
-                        if (x <= FLT_MAX) mk = fmaxf(mk, x);
-                        if (y <= FLT_MAX) mv = fmaxf(mv, y);
-                    }
-                }
-                mk = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mk)));
-                mv = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mv)));
-                // below 2^e; the range keeps every factor of the kernel a normal fp32
-                auto exponent = [](float m) { return min(100, max(-100, (int)(__float_as_uint(m) >> 23) - 126)); };
-                const int ek = mk > 0.f ? exponent(mk) : 0;
-                int ev = mv > 0.f ? exponent(mv) : eprev;
-                if (mv > 0.f) {
-                    // a block of far smaller values rides on the largest so far
-                    ev = max(ev, emax - 60);
-                    emax = max(emax, ev);
-                    eprev = ev;
-                }
-                float rk = 0.f, rv = 0.f;
-                if (there(row)) {
-                    const float kn = knp[row], vn = vnp[row];
-                    rk = fmaf(vn, 0.f, kn * pp_pow2(-ek));  // NaN if either norm is not finite
-                    rv = fabsf(vn) <= FLT_MAX ? vn * pp_pow2(-ev) : 0.f;
-                }
+                const float* fac = reinterpret_cast<const float*>(stg + N * D);
                 const uint32_t slk = (2 * tc) & 3, slv = (2 * tc + 1) & 3;
-                if (tc >= 2) ok = pp_wait(&kv_free[slk], ((tc >> 1) - 1) & 1, abort_f, status);
+                ok = pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status) &&
+                     pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status) &&
+                     (tc < 2 || pp_wait(&kv_free[slk], ((tc >> 1) - 1) & 1, abort_f, status));
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
-                if (dt == 0) {
-                    reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 3] = make_float2(pp_pow2(ek), (float)ev);
-                    mbar_arrive(&meta_full[tc & 3]);
-                }
-                pp_expand<D, TPR, true>(A.k_bits, stg, rk, A.khi, A.klo, sm + Z::kRing + slk * Z::kTile, N * 128, row, sub);
+                pp_expand<D, TPR, true>(A.k_bits, stg, fac[row], A.khi, A.klo, sm + Z::kRing + slk * Z::kTile, N * 128,
+                                        row, sub);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kv_full[slk]);
@@ -923,8 +992,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                     ok = false;
                     break;
                 }
-                pp_expand<D, TPR, false>(A.v_bits, stg + N * D / 2, rv, A.vhi, A.vlo, sm + Z::kRing + slv * Z::kTile, N * 128,
-                                  row, sub);
+                pp_expand<D, TPR, false>(A.v_bits, stg + N * D / 2, fac[N + row], A.vhi, A.vlo,
+                                         sm + Z::kRing + slv * Z::kTile, N * 128, row, sub);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -961,6 +1030,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             const int tok = rvalid ? (p.row0 + lrow) / G : 0, hd = rvalid ? p.row0 + lrow - tok * G : 0;
             const int64_t qrow = ((int64_t)p.q0 + tok) * A.Hq + (int64_t)p.h * G + hd;
             const int pos = rvalid ? p.pos0 + tok : -1;
+            // a warp without rows only keeps the barriers' count
+            const bool rows_here = __any_sync(0xFFFFFFFFu, rvalid);
             const int lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
             // ---- queries: rotated in registers and tensor memory (the output
             // columns, free until the item's first product), 64 dims at a time,
@@ -1047,13 +1118,21 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
             for (int j = split ? g : 0; j < nb; j += split ? 2 : 1) {
                 const int buf = Z::kStreams == 2 ? g : (j & 1);
                 const uint32_t tc = tc0 + j;
-                pp_wait(&meta_full[tc & 3], (tc >> 2) & 1, abort_f, status);
-                const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 3);
+                pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status);
+                const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 7);
                 const float2 meta = make_float2(mp[0], mp[1]);
                 if (lastb < 0) eb = meta.y;
                 pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
                 ++ns[buf];
                 __syncwarp();
+                lastb = buf;
+                if (!rows_here) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[buf]);
+                    ++npv[buf];
+                    continue;
+                }
                 tc_fence_after();
                 const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
                 const int t0 = (p.blk + j) * N;
@@ -1061,13 +1140,18 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
                 const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
                 float mx = -INFINITY;
+                if (full) {
 #pragma unroll 1
-                for (int c = 0; c < N; c += 32) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + c, s);
-                    tmem_wait_ld();
-                    if (!full) pp_mask(s, c0 - c, c1 - c);
-                    mx = fmaxf(mx, pp_max32(s));
+                    for (int c = 0; c < N; c += 32) mx = fmaxf(mx, tmem_max32(t_s + c));
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < N; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(t_s + c, s);
+                        tmem_wait_ld();
+                        pp_mask(s, c0 - c, c1 - c);
+                        mx = fmaxf(mx, pp_max32(s));
+                    }
                 }
                 const float cs = cq * meta.x;
                 const float cand = mx * cs + meta.y;  // -inf where nothing is attended
@@ -1121,7 +1205,6 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 float s0, s1;
                 f2_split(f2_add(sum[0], sum[1]), s0, s1);
                 l = fmaf(s0 + s1, pp_exp2(eb - meta.y), l);
-                lastb = buf;
             }
             if (lastb >= 0) {
                 if (Z::kStreams == 1 && nb > 1) pp_wait(&pv_done[lastb ^ 1], (npv[lastb ^ 1] - 1) & 1, abort_f, status);
@@ -1137,7 +1220,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                     xs[256 + r] = eb;
                 }
                 meet_all();
-                if (g == 0 && nb > 1) {
+                if (g == 0 && nb > 1 && rows_here) {
                     const float M1 = xs[r], l1 = xs[128 + r], eb1 = xs[256 + r];
                     const float Mx = fmaxf(M, M1);
                     const float a0 = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = M1 == -INFINITY ? 0.f : pp_exp2(M1 - Mx);
@@ -1159,7 +1242,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                 meet_all();
             }
             // ---- the rows leave: finished, or as a part
-            if (pair || g == 0) {
+            if ((pair || g == 0) && rows_here) {
                 if (p.flags & kJobWhole) {
                     float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
                     // rotated back, s . H (s2 . o): 64 dims at a time, then across
@@ -1222,9 +1305,10 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            o4[(c / 4 + k) * Z::kRows] =
-                                make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                            __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                            if (rvalid)
+                                o4[(c / 4 + k) * Z::kRows] =
+                                    make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                     }
                     float* x = w + D * Z::kRows;
                     x[lrow] = M;
@@ -1265,35 +1349,43 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
     const int lrow = 32 * blockIdx.y + lane;  // every warp: the same 32 rows
     if (32 * (int)blockIdx.y >= rows) return;
     constexpr int64_t PF = PagedPrefillGeo<D>::kPartFloats;
-    auto part = [&](int c) { return A.part + ((int64_t)c * 2 + (c == sh)) * PF; };
-    auto has = [&](int c) { return __ldcg(A.meta + (int64_t)c * kPpMeta + (c == sh ? kMetaHas1 : kMetaHas0)) != 0; };
-    float M = -INFINITY, eb = 0.f;
+    const bool in = lrow < rows;
+    float M = -INFINITY, l = 0.f, eb = 0.f;
     bool first = true;
-    for (int c = sh; c <= last; ++c) {
-        if (!has(c)) continue;
-        const float* x = part(c) + D * Z::kRows;
-        M = fmaxf(M, __ldcg(x + lrow));
-        if (first) eb = __ldcg(x + 2 * Z::kRows + lrow);
-        first = false;
-    }
-    float l = 0.f;
     float4 o[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = sh; c <= last; ++c) {
-        if (!has(c)) continue;
-        const float* x = part(c) + D * Z::kRows;
-        const float m = __ldcg(x + lrow), lc = __ldcg(x + Z::kRows + lrow), ec = __ldcg(x + 2 * Z::kRows + lrow);
-        const float a = m == -INFINITY ? 0.f : pp_exp2(m - M);
-        l += (m == -INFINITY ? lc : lc * a) * pp_exp2(eb - ec);
-        const float4* o4 = reinterpret_cast<const float4*>(part(c));
+    for (int c0 = sh; c0 <= last; c0 += 32) {
+        // which of the shares left a part: looked up at once
+        const int cl = c0 + lane;
+        unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && __ldcg(A.meta + (int64_t)min(cl, last) * kPpMeta +
+                                                                       (cl == sh ? kMetaHas1 : kMetaHas0)) != 0);
+        while (has) {
+            const int c = c0 + __ffs(has) - 1;
+            has &= has - 1;
+            const float* pt = A.part + ((int64_t)c * 2 + (c == sh)) * PF;
+            const float4* o4 = reinterpret_cast<const float4*>(pt) + lrow;
+            const float* x = pt + D * Z::kRows + lrow;
+            if (!in) continue;
+            float4 v[C];
+            const float m = __ldcg(x), lc = __ldcg(x + Z::kRows), ec = __ldcg(x + 2 * Z::kRows);
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const float4 v = __ldcg(o4 + (warp + 8 * k) * Z::kRows + lrow);
-            o[k].x = fmaf(a, v.x, o[k].x);
-            o[k].y = fmaf(a, v.y, o[k].y);
-            o[k].z = fmaf(a, v.z, o[k].z);
-            o[k].w = fmaf(a, v.w, o[k].w);
+            for (int k = 0; k < C; ++k) v[k] = __ldcg(o4 + (warp + 8 * k) * Z::kRows);
+            if (first) eb = ec;
+            first = false;
+            // both sides to the larger maximum; a side that attended to nothing has
+            // -inf, no output and the sum 0 (or NaN)
+            const float Mx = fmaxf(M, m);
+            const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = m == -INFINITY ? 0.f : pp_exp2(m - Mx);
+            l = (M == -INFINITY ? l : l * a) + (m == -INFINITY ? lc : lc * a1) * pp_exp2(eb - ec);
+            M = Mx;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                o[k].x = o[k].x * a + v[k].x * a1;
+                o[k].y = o[k].y * a + v[k].y * a1;
+                o[k].z = o[k].z * a + v[k].z * a1;
+                o[k].w = o[k].w * a + v[k].w * a1;
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
@@ -1385,8 +1477,7 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P,
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
-    k_prefill_paged<D><<<shares, Z::kThreads, Z::kSmem, s>>>(A, P, status_word());
-    e = cudaGetLastError();
+    e = launch_pdl(k_prefill_paged<D>, dim3(shares), dim3(Z::kThreads), Z::kSmem, s, A, P, status_word());
     if (e != cudaSuccess) return e;
     return launch_pdl(k_prefill_paged_join<D>, dim3(shares, Z::kRows / 32), dim3(256), 0, s, A, P);
 }
