@@ -509,22 +509,21 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
     _cuda(q)
-    _i32(cu_q, "cu_q")
-    _i32(block_table, "block_table")
-    _i32(ctx_lens, "ctx_lens")
-    _same_device(q.device, cu_q, block_table, ctx_lens, cache.k_norm)
-    with _on(q.device):
+    dev = q.device
+    _ints(dev, cu_q, block_table, ctx_lens)
+    _same_device(dev, cache.k_norm)
+    with _on(dev):
         if out is None:
-            out = torch.zeros(n_q, Hq, d, dtype=out_dtype, device=q.device)
+            out = torch.zeros(n_q, Hq, d, dtype=out_dtype, device=dev)
         _cuda(out)
-        _same_device(q.device, out)
+        _same_device(dev, out)
         if out.shape != q.shape:
             raise ValueError("out must be [n_q, Hq, d]")
-        ws = _scratch(workspace, tq_attn_prefill_paged_workspace_bytes(Hq, cache.Hkv, d), q.device)
+        ws = _scratch(workspace, tq_attn_prefill_paged_workspace_bytes(Hq, cache.Hkv, d), dev)
         _check("tq_attn_prefill_paged", lib().tq_attn_prefill_paged(
             plan.handle, q.data_ptr(), n_q, B, Hq, cache.Hkv, cache.view(), block_table.data_ptr(),
             block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), window, cache.k_bits, cache.v_bits,
-            scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(q)))
+            scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev)))
     return out
 
 
@@ -574,14 +573,28 @@ class PageTable:
                          torch.zeros(n_seqs, dtype=torch.int32, device=device),
                          torch.zeros(n_pages, dtype=torch.int32, device=device))
 
-    def _view(self, layers: PagedLayers) -> PageTableView:
-        for name, t in (("block_table", self.block_table), ("lens", self.lens), ("refs", self.refs)):
-            _i32(t, name)
-        if self.block_table.dim() != 2 or self.lens.numel() != self.block_table.shape[0] or \
-                self.refs.numel() != layers.n_pages:
+    def _view(self, layers: PagedLayers, shape) -> PageTableView:
+        b, n, r = self.block_table, self.lens, self.refs
+        _ints(layers.device, b, n, r)
+        if b.shape != shape or n.numel() != shape[0] or r.numel() != layers.n_pages:
             raise ValueError("block_table [n_seqs, max_pages], lens [n_seqs], refs [n_pages] expected")
-        _same_device(layers.device, self.block_table, self.lens, self.refs)
-        return PageTableView(self.block_table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr())
+        return PageTableView(b.data_ptr(), n.data_ptr(), r.data_ptr())
+
+
+def _ints(device, *ts):
+    """Contiguous int32 CUDA tensors on `device`."""
+    for t in ts:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("expected contiguous CUDA tensors")
+        if t.dtype != torch.int32:
+            raise TypeError("expected int32 tensors")
+        if t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _raw_stream(device):
+    """torch's current stream of the device, without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _same_device(device, *ts):
@@ -620,41 +633,40 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
     src, dst = _layers(src), _layers(dst)
     if len(src.views) != len(dst.views) or src.args != dst.args or src.page_size != dst.page_size:
         raise ValueError("src and dst must have the same number of layers and geometry")
-    _i32(src_ids, "src_ids")
-    _i32(dst_ids, "dst_ids")
+    _ints(dst.device, src_ids, dst_ids)
     if src_ids.numel() != dst_ids.numel():
         raise ValueError("src_ids and dst_ids must have one length")
-    _same_device(dst.device, src.layers[0].k_norm, src_ids, dst_ids)
+    if src.device != dst.device:
+        raise ValueError("src and dst must be on one device")
     with _on(dst.device):
         ws = _scratch(workspace, tq_pages_workspace_bytes(0, 0, dst.n_pages), dst.device)
         _check("tq_pages_copy", lib().tq_pages_copy(
             src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(),
-            src_ids.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dst_ids)))
+            src_ids.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dst.device)))
 
 
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
     layers = _layers(layers)
-    n_seqs, max_pages = table.block_table.shape
+    shape = table.block_table.shape
+    if len(shape) != 2:
+        raise ValueError("block_table must be [n_seqs, max_pages]")
+    n_seqs, max_pages = shape
     dev = layers.device
     with _on(dev):
         if out is None:
             out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
         if info is None:
             info = torch.empty(2, dtype=torch.int32, device=dev)
-        _i32(info, "info")
-        if info.numel() != 2 or out.block_table.shape != table.block_table.shape:
-            raise ValueError("info must have 2 entries and out the table's shape")
-        _same_device(dev, info)
-        if arg is not None:
-            _i32(arg, "parents / new_lens")
-            _same_device(dev, arg)
-            if arg.numel() != n_seqs:
-                raise ValueError("one entry per row expected")
-        views = (table._view(layers), out._view(layers))
+        other = moved if arg is None else arg
+        _ints(dev, info, other)
+        if info.numel() != 2 or other.numel() != (layers.n_pages if arg is None else n_seqs):
+            raise ValueError("info has 2 entries, parents and new_lens one per row, moved_to one per page")
+        a, b = table._view(layers, shape), out._view(layers, shape)
         ws = _scratch(workspace, tq_pages_workspace_bytes(n_seqs, max_pages, layers.n_pages), dev)
-        middle = (views[0], arg.data_ptr(), views[1]) if arg is not None else (*views, moved.data_ptr())
+        middle = (a, b, other.data_ptr()) if arg is None else (a, other.data_ptr(), b)
         _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,
-                                      info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(info)))
+                                      info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      _raw_stream(dev)))
     return out, info
 
 
@@ -683,10 +695,6 @@ def tq_pages_compact(table: PageTable, layers, out: PageTable | None = None, mov
     layers = _layers(layers)
     if moved_to is None:
         moved_to = torch.empty(layers.n_pages, dtype=torch.int32, device=layers.device)
-    _i32(moved_to, "moved_to")
-    _same_device(layers.device, moved_to)
-    if moved_to.numel() != layers.n_pages:
-        raise ValueError("moved_to must have n_pages entries")
     out, info = _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
     return out, moved_to, info
 

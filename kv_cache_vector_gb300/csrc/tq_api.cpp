@@ -1055,10 +1055,13 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d) {
 }
 
 namespace {
-// The levels c * s as fp16 bytes for the byte-permute lookups; s is the
-// plan's scale where it has one (then every c * s is close to an fp16 value).
+// The scale s under which the levels are kept in fp16: the plan's where it has
+// one (then every c * s is close to an fp16 value).
+double level_scale(const tq::Plan& P, int bits) { return P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0; }
+
+// The levels c * s as fp16 bytes for the byte-permute lookups.
 void level_bytes(const tq::Plan& P, int bits, uint32_t* w) {
-    const double s = P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0;
+    const double s = level_scale(P, bits);
     const int first = bits == 4 ? 8 : 0, n = bits == 2 ? 4 : 8;
     for (int i = 0; i < 8; ++i) w[i] = 0u;
     for (int i = 0; i < n; ++i) {
@@ -1097,9 +1100,16 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
         !device_accessible(cu_q) || !device_accessible(ctx_lens) || !device_accessible(workspace) ||
         !paged_accessible(cache))
         return TQ_ERR_INVALID_ARG;
-    tq::AttnParams A;
-    tq::fill_attn_params(*P, k_bits, v_bits, scale, 0.0f, A);
     tq::PagedPrefillCall c = {};
+    for (int i = 0; i < P->d; ++i) {
+        c.consts.sgnb[i >> 5] |= (P->signs[i] < 0 ? 1u : 0u) << (i & 31);
+        c.consts.sgn2b[i >> 5] |= (P->signs2[i] < 0 ? 1u : 0u) << (i & 31);
+    }
+    const double sd = std::sqrt((double)P->d);
+    c.consts.two_sided = (P->flags & TQ_PLAN_TWO_SIDED_SIGNS) ? 1 : 0;
+    c.consts.q_mul = (float)((double)scale * 1.4426950408889634 / (sd * level_scale(*P, k_bits)));
+    c.consts.out_mul = (float)(1.0 / level_scale(*P, v_bits));
+    c.consts.inv_sqrt_d = (float)(1.0 / sd);
     c.q = q;
     c.out = out;
     c.cu_q = cu_q;
@@ -1120,7 +1130,7 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
     level_bytes(*P, k_bits, c.k_levels);
     level_bytes(*P, v_bits, c.v_levels);
     const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
-        return tq::launch_prefill_paged<decltype(D)::value>(c, A, reinterpret_cast<cudaStream_t>(stream));
+        return tq::launch_prefill_paged<decltype(D)::value>(c, reinterpret_cast<cudaStream_t>(stream));
     });
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }

@@ -354,7 +354,16 @@ struct PagedPrefillGeo {
 inline size_t prefill_paged_ws_bytes(int d, int sms) {
     return (size_t)sms * (2 * (size_t)(d + 3) * (d == 256 ? 128 : 256) * 4 + 32);
 }
+struct PagedPrefillConsts {
+    uint32_t sgnb[kMaxD / 32];   // as AttnParams
+    uint32_t sgn2b[kMaxD / 32];
+    int two_sided;
+    float q_mul;       // scale log2(e) / (sqrt(d) s_k)
+    float out_mul;     // 1 / s_v
+    float inv_sqrt_d;
+};
 struct PagedPrefillCall {
+    PagedPrefillConsts consts;
     const void* q;
     void* out;
     const int32_t* cu_q;
@@ -369,7 +378,7 @@ struct PagedPrefillCall {
     uint32_t k_levels[8], v_levels[8];
 };
 template <int D>
-cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P, cudaStream_t s);
+cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s);
 
 // Paged append of one token per sequence, d >= 32 (tq_codec.cu).
 template <int D>

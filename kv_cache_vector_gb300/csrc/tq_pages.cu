@@ -512,11 +512,13 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
 constexpr int kPcThreads = 256;
 constexpr int kPcUnroll = 2;
 constexpr int kPcChunk = kPcThreads * kPcUnroll;  // 16-byte words per step
-constexpr int kPcLayers = 64;                     // layers per launch (4 KB of parameters)
+constexpr int kPcLayers = 64;                     // most layers per launch (4 KB of parameters)
 
+// A launch with few layers has few parameters: they are copied at every call.
+template <int MAX>
 struct CopyLayers {
-    const uint4* src[kPcLayers][4];
-    uint4* dst[kPcLayers][4];
+    const uint4* src[MAX][4];
+    uint4* dst[MAX][4];
 };
 
 // 16-byte words of a page's four arrays: n[0] packed K, n[1] K norms, ...
@@ -527,8 +529,9 @@ struct CopySizes {
 // Step u of the copy: words [u % steps * kPcChunk, ..) of page pair u / steps
 // / L in layer u / steps % L, the page's four arrays taken as one run of
 // words.
+template <int MAX>
 __global__ void __launch_bounds__(kPcThreads, 8)
-k_pages_copy(const __grid_constant__ CopyLayers P, const CopySizes Z, int L, const int32_t* head,
+k_pages_copy(const __grid_constant__ CopyLayers<MAX> P, const CopySizes Z, int L, const int32_t* head,
              const int32_t* src, const int32_t* dst) {
     griddep_wait();
     // read at the L2, where the plan's writes are: this kernel's CTAs were
@@ -573,6 +576,25 @@ k_pages_copy(const __grid_constant__ CopyLayers P, const CopySizes Z, int L, con
     }
 }
 
+template <int MAX>
+static cudaError_t launch_copy(const PagesCall& c, int l0, int L, const CopySizes& Z, const PagesWs& W, int64_t grid,
+                               cudaStream_t s) {
+    CopyLayers<MAX> P;
+    for (int l = 0; l < L; ++l) {
+        const tq_paged_cache &f = c.src[l0 + l], &t = c.dst[l0 + l];
+        P.src[l][0] = reinterpret_cast<const uint4*>(f.k_packed);
+        P.src[l][1] = reinterpret_cast<const uint4*>(f.k_norm);
+        P.src[l][2] = reinterpret_cast<const uint4*>(f.v_packed);
+        P.src[l][3] = reinterpret_cast<const uint4*>(f.v_norm);
+        P.dst[l][0] = reinterpret_cast<uint4*>(t.k_packed);
+        P.dst[l][1] = reinterpret_cast<uint4*>(t.k_norm);
+        P.dst[l][2] = reinterpret_cast<uint4*>(t.v_packed);
+        P.dst[l][3] = reinterpret_cast<uint4*>(t.v_norm);
+    }
+    return launch_pdl(k_pages_copy<MAX>, dim3((unsigned)grid), dim3(kPcThreads), 0, s, P, Z, L,
+                      (const int32_t*)W.head, (const int32_t*)W.src, (const int32_t*)W.dst);
+}
+
 // One cluster suits every size: 8 CTAs once the books are long enough for the
 // barriers between more CTAs to cost less than they save.
 static int plan_ctas(const PagesPlan& A) {
@@ -593,7 +615,7 @@ static cudaError_t launch_plan(const PagesPlan& A, cudaStream_t s) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = nb > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pages_plan<OP>, A, status_word());
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -645,23 +667,10 @@ cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s) {
     const int64_t steps = (words + kPcChunk - 1) / kPcChunk;
     for (int l0 = 0; l0 < c.n_layers; l0 += kPcLayers) {
         const int L = c.n_layers - l0 < kPcLayers ? c.n_layers - l0 : kPcLayers;
-        CopyLayers P;
-        for (int l = 0; l < L; ++l) {
-            const tq_paged_cache &f = c.src[l0 + l], &t = c.dst[l0 + l];
-            P.src[l][0] = reinterpret_cast<const uint4*>(f.k_packed);
-            P.src[l][1] = reinterpret_cast<const uint4*>(f.k_norm);
-            P.src[l][2] = reinterpret_cast<const uint4*>(f.v_packed);
-            P.src[l][3] = reinterpret_cast<const uint4*>(f.v_norm);
-            P.dst[l][0] = reinterpret_cast<uint4*>(t.k_packed);
-            P.dst[l][1] = reinterpret_cast<uint4*>(t.k_norm);
-            P.dst[l][2] = reinterpret_cast<uint4*>(t.v_packed);
-            P.dst[l][3] = reinterpret_cast<uint4*>(t.v_norm);
-        }
         const int64_t cap = (int64_t)num_sms() * 8;
         int64_t grid = most * L * steps;
         grid = grid < 1 ? 1 : (grid > cap ? cap : grid);
-        e = launch_pdl(k_pages_copy, dim3((unsigned)grid), dim3(kPcThreads), 0, s, P, Z, L,
-                       (const int32_t*)W.head, (const int32_t*)W.src, (const int32_t*)W.dst);
+        e = L <= 4 ? launch_copy<4>(c, l0, L, Z, W, grid, s) : launch_copy<kPcLayers>(c, l0, L, Z, W, grid, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -110,7 +110,10 @@ struct PpArgs {
     int B, Hq, Hkv, max_pages, shift, window, k_bits, v_bits, out_bf16;
     uint32_t khi[4], klo[4], vhi[4], vlo[4];  // level bytes (see expand)
 };
-enum { kMetaOwner = 0, kMetaB, kMetaI, kMetaH, kMetaLast, kMetaHas0, kMetaHas1, kPpMeta = 8 };
+// what a share left: bit 0 a part of the item it starts in, bit 1 one of the
+// item it owns (which starts in this share and ends in the share kMetaLast;
+// -1: none), that item's first row of q, KV head, rows
+enum { kMetaHas = 0, kMetaLast, kMetaQ0, kMetaH, kMetaRow0, kMetaRows, kPpMeta = 8 };
 
 // Where a share starts or goes on: sequence, row tile, KV head, and the units
 // of the item that belong to earlier shares.
@@ -579,7 +582,7 @@ __device__ __forceinline__ void pp_mask(uint32_t (&s)[32], int c0, int c1) {
 
 template <int D>
 __global__ void __launch_bounds__(PpGeo<D>::kThreads, 1)
-k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnParams P, int* status) {
+k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefillConsts P, int* status) {
     using Z = PpGeo<D>;
     constexpr int N = Z::kN, W = Z::kD, SW = Z::kSoftWarps, NS = Z::kStages;
     constexpr int PARTS = D < 64 ? 1 : D / 64;  // register-sized pieces of a row
@@ -796,27 +799,23 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
         // which parts this share left, and the item it owns: the one that starts
         // in this share and ends in a later one
         if (lane == 0) {
-            int32_t* m = A.meta + (int64_t)blockIdx.x * kPpMeta;
-            m[kMetaHas0] = has & 1;
-            m[kMetaHas1] = has >> 1;
+            int last = blockIdx.x;
             bool owner = ok && cur.off > 0 &&
                          !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
             if (owner) {
                 const int64_t w = seq.weight(cur.i), per = *share;
                 const int nblk = pp_blocks<D>(A, seq, cur.i);
-                int last = blockIdx.x;
                 // no join where one share has all of the item's blocks
                 owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
                 for (int64_t x = cur.off; x < w; x += per) {
                     ++last;
                     if (pp_cut(nblk, x, w) == 0 && pp_cut(nblk, min(w, x + per), w) == nblk) owner = false;
                 }
-                m[kMetaB] = cur.b;
-                m[kMetaI] = cur.i;
-                m[kMetaH] = cur.h;
-                m[kMetaLast] = last;
             }
-            m[kMetaOwner] = owner;
+            const int row0 = cur.i * Z::kRows;
+            int4* m = reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta);
+            m[0] = make_int4(has, owner ? last : -1, owner ? __ldg(A.cu + cur.b) : 0, cur.h);
+            m[1] = make_int4(row0, owner ? min(Z::kRows, seq.rows - row0) : 0, 0, 0);
         }
         // the copies issued have landed before the CTA leaves (bounded)
         if (lane == 0 && tc > 0)
@@ -1333,21 +1332,20 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ AttnPa
 // parts summed in the order of the shares, divided and rotated back.
 template <int D>
 __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constant__ PpArgs A,
-                                                            const __grid_constant__ AttnParams P) {
+                                                            const __grid_constant__ PagedPrefillConsts P) {
     using Z = PpGeo<D>;
     constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
     __shared__ float tile[32][D + 1];
     griddep_wait();
     const int sh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t* meta = A.meta + (int64_t)sh * kPpMeta;
-    if (!__ldcg(meta + kMetaOwner)) return;
-    const int b = __ldcg(meta + kMetaB), i = __ldcg(meta + kMetaI), h = __ldcg(meta + kMetaH),
-              last = __ldcg(meta + kMetaLast);
-    PpSeq<D> q;
-    q.load(A, b, nullptr);
-    const int row0 = i * Z::kRows, rows = min(Z::kRows, q.rows - row0);
+    const int4* meta = reinterpret_cast<const int4*>(A.meta);
+    const int4 m0 = __ldcg(meta + 2 * sh), m1 = __ldcg(meta + 2 * sh + 1);
+    int near = 0;  // what the shares up to 31 further on left, looked up together with the item
+    if (sh + lane < (int)gridDim.x) near = __ldcg(A.meta + (sh + lane) * kPpMeta + kMetaHas);
+    const int last = m0.y, rows = m1.y;
+    if (last < 0 || 32 * (int)blockIdx.y >= rows) return;
+    const int G = A.Hq / A.Hkv;
     const int lrow = 32 * blockIdx.y + lane;  // every warp: the same 32 rows
-    if (32 * (int)blockIdx.y >= rows) return;
     constexpr int64_t PF = PagedPrefillGeo<D>::kPartFloats;
     const bool in = lrow < rows;
     float M = -INFINITY, l = 0.f, eb = 0.f;
@@ -1356,35 +1354,48 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
 #pragma unroll
     for (int k = 0; k < C; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = sh; c0 <= last; c0 += 32) {
-        // which of the shares left a part: looked up at once
         const int cl = c0 + lane;
-        unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && __ldcg(A.meta + (int64_t)min(cl, last) * kPpMeta +
-                                                                       (cl == sh ? kMetaHas1 : kMetaHas0)) != 0);
-        while (has) {
-            const int c = c0 + __ffs(has) - 1;
-            has &= has - 1;
-            const float* pt = A.part + ((int64_t)c * 2 + (c == sh)) * PF;
-            const float4* o4 = reinterpret_cast<const float4*>(pt) + lrow;
-            const float* x = pt + D * Z::kRows + lrow;
-            if (!in) continue;
-            float4 v[C];
-            const float m = __ldcg(x), lc = __ldcg(x + Z::kRows), ec = __ldcg(x + 2 * Z::kRows);
+        if (c0 > sh && cl <= last) near = __ldcg(A.meta + cl * kPpMeta + kMetaHas);
+        unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && (near & (cl == sh ? 2 : 1)));
+        while (has && in) {
+            // a few parts' loads in flight at once
+            constexpr int AT = D >= 256 ? 2 : 4;
+            float4 v[AT][C];
+            float m[AT], lc[AT], ec[AT];
+            unsigned left = has;
 #pragma unroll
-            for (int k = 0; k < C; ++k) v[k] = __ldcg(o4 + (warp + 8 * k) * Z::kRows);
-            if (first) eb = ec;
-            first = false;
-            // both sides to the larger maximum; a side that attended to nothing has
-            // -inf, no output and the sum 0 (or NaN)
-            const float Mx = fmaxf(M, m);
-            const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = m == -INFINITY ? 0.f : pp_exp2(m - Mx);
-            l = (M == -INFINITY ? l : l * a) + (m == -INFINITY ? lc : lc * a1) * pp_exp2(eb - ec);
-            M = Mx;
+            for (int t = 0; t < AT; ++t) {
+                m[t] = -INFINITY, lc[t] = 0.f, ec[t] = 0.f;
+                if (left) {
+                    const int c = c0 + __ffs(left) - 1;
+                    left &= left - 1;
+                    const float* pt = A.part + ((int64_t)c * 2 + (c == sh)) * PF;
+                    const float* x = pt + D * Z::kRows + lrow;
+                    m[t] = __ldcg(x), lc[t] = __ldcg(x + Z::kRows), ec[t] = __ldcg(x + 2 * Z::kRows);
 #pragma unroll
-            for (int k = 0; k < C; ++k) {
-                o[k].x = o[k].x * a + v[k].x * a1;
-                o[k].y = o[k].y * a + v[k].y * a1;
-                o[k].z = o[k].z * a + v[k].z * a1;
-                o[k].w = o[k].w * a + v[k].w * a1;
+                    for (int k = 0; k < C; ++k)
+                        v[t][k] = __ldcg(reinterpret_cast<const float4*>(pt) + lrow + (warp + 8 * k) * Z::kRows);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < AT; ++t) {
+                if (!has) break;
+                has &= has - 1;
+                if (first) eb = ec[t];
+                first = false;
+                // both sides to the larger maximum; a side that attended to nothing
+                // has -inf, no output and the sum 0 (or NaN)
+                const float Mx = fmaxf(M, m[t]);
+                const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = m[t] == -INFINITY ? 0.f : pp_exp2(m[t] - Mx);
+                l = (M == -INFINITY ? l : l * a) + (m[t] == -INFINITY ? lc[t] : lc[t] * a1) * pp_exp2(eb - ec[t]);
+                M = Mx;
+#pragma unroll
+                for (int k = 0; k < C; ++k) {
+                    o[k].x = o[k].x * a + v[t][k].x * a1;
+                    o[k].y = o[k].y * a + v[t][k].y * a1;
+                    o[k].z = o[k].z * a + v[t][k].z * a1;
+                    o[k].w = o[k].w * a + v[t][k].w * a1;
+                }
             }
         }
     }
@@ -1395,7 +1406,7 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int j = 4 * (warp + 8 * k) + u;
-            tile[lane][j] = __uint_as_float(__float_as_uint(v[u] * inv) ^ (P.two_sided ? P.sgn2[j] : 0u));
+            tile[lane][j] = __uint_as_float(__float_as_uint(v[u] * inv) ^ (P.two_sided ? sign_mask(P.sgn2b, j) : 0u));
         }
     }
     __syncthreads();
@@ -1423,8 +1434,8 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
                     e[k] = u + v;
                     e[k + len] = u - v;
                 }
-        const int grow = row0 + lr, tok = grow / q.G, hd = grow - tok * q.G;
-        const int64_t at = (((int64_t)__ldg(A.cu + b) + tok) * A.Hq + (int64_t)h * q.G + hd) * D;
+        const int grow = m1.x + lr, tok = grow / G, hd = grow - tok * G;
+        const int64_t at = (((int64_t)m0.z + tok) * A.Hq + (int64_t)m0.w * G + hd) * D;
 #pragma unroll
         for (int k = 0; k < C; ++k) {
             const int j = lane + 32 * k;
@@ -1438,7 +1449,8 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
 }  // namespace dev
 
 template <int D>
-cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P, cudaStream_t s) {
+cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
+    const PagedPrefillConsts& P = c.consts;
     using namespace dev;
     using Z = PpGeo<D>;
     static_assert(Z::kSmem <= 232448, "shared memory per CTA");
@@ -1482,6 +1494,6 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, const AttnParams& P,
     return launch_pdl(k_prefill_paged_join<D>, dim3(shares, Z::kRows / 32), dim3(256), 0, s, A, P);
 }
 
-template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, const AttnParams&, cudaStream_t);
+template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, cudaStream_t);
 
 }  // namespace tq
