@@ -1104,6 +1104,7 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
     for (int i = 0; i < P->d; ++i) {
         c.consts.sgnb[i >> 5] |= (P->signs[i] < 0 ? 1u : 0u) << (i & 31);
         c.consts.sgn2b[i >> 5] |= (P->signs2[i] < 0 ? 1u : 0u) << (i & 31);
+        c.consts.sgnh[i >> 1] |= (P->signs[i] < 0 ? 0x8000u : 0u) << (16 * (i & 1));
     }
     const double sd = std::sqrt((double)P->d);
     c.consts.two_sided = (P->flags & TQ_PLAN_TWO_SIDED_SIGNS) ? 1 : 0;

@@ -357,6 +357,7 @@ inline size_t prefill_paged_ws_bytes(int d, int sms) {
 struct PagedPrefillConsts {
     uint32_t sgnb[kMaxD / 32];   // as AttnParams
     uint32_t sgn2b[kMaxD / 32];
+    uint32_t sgnh[kMaxD / 2];    // as RowParams: one word per pair of 16-bit values
     int two_sided;
     float q_mul;       // scale log2(e) / (sqrt(d) s_k)
     float out_mul;     // 1 / s_v

@@ -14,7 +14,7 @@
 // serves two MMA row tiles.
 //
 //   warps 0-7    softmax, one thread per query row (4 warps at d = 256)
-//   8 warps      expansion: bytes -> fp16 levels times the row's norm
+//   8 warps     expansion: bytes -> fp16 levels times the row's norm
 //   1 warp       MMAs
 //   1 warp       copies of packed rows and norms from the pages (bulk copies);
 //                it also walks along the CTA's parts and hands them out
@@ -49,6 +49,7 @@
 // on through their (then failing) waits so that their barriers stay paired;
 // no output is written after the flag.
 #include <cfloat>
+#include <climits>
 
 #include "tq_async.cuh"
 #include "tq_device.cuh"
@@ -75,7 +76,8 @@ struct PpGeo {
     static constexpr int kRows = PagedPrefillGeo<D>::kRows;
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kSoftWarps = 4 * kStreams;
-    static constexpr int kWarps = kSoftWarps + 11;
+    static constexpr int kDeqWarps = 8;
+    static constexpr int kWarps = kSoftWarps + kDeqWarps + 3;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = D <= 64 ? 4 : 2;   // staged packed blocks
     static constexpr uint32_t kTile = kN * kD * 2;    // an expanded K or V tile
@@ -87,7 +89,7 @@ struct PpGeo {
     static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [8] float2: 2^Ek, Ev
     static constexpr uint32_t kSegs = kMeta + 64;               // [kStages] segments staged
     static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
-    static constexpr uint32_t kRedBytes = 20 * 8;
+    static constexpr uint32_t kRedBytes = 28 * 8;
     static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
     static constexpr uint32_t kJobs = kCur + 64;                // [2] jobs
     static constexpr uint32_t kBar = kJobs + 2 * 48;
@@ -449,7 +451,8 @@ template <int BITS, int D, int TPR, bool LOW>
 __device__ __forceinline__ void pp_expand_row(const unsigned char* rows, float rf, const uint32_t* hi,
                                               const uint32_t* lo, unsigned char* tile, uint32_t half_bytes, int row,
                                               int sub) {
-    constexpr int EACH = D / 16 / TPR;
+    constexpr int EACH = D / 16 >= TPR ? D / 16 / TPR : 1;
+    if (D / 16 < TPR && sub >= D / 16) return;
     const __half rh = __float2half_rn(rf);
     const __half2 r = __half2half2(rh), rl = __float2half2_rn(rf - __half2float(rh));
     const unsigned char* src = rows + row * (D * BITS / 8);
@@ -507,13 +510,6 @@ __device__ __forceinline__ float pp_max32(const uint32_t (&s)[32]) {
     return fmaxf(pp_max3(m[0], m[1], m[2]), m[3]);
 }
 
-// 32 bytes of global memory in one load.
-__device__ __forceinline__ void pp_ld256(const void* p, uint32_t* u) {
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                 : "l"(p));
-}
-
 // Flip y[j] where bit j of the words is set.
 template <int E>
 __device__ __forceinline__ void pp_signs(float (&y)[E], const uint32_t* bits) {
@@ -539,14 +535,12 @@ __device__ __forceinline__ void pp_store_row(uint32_t t, const float (&y)[E]) {
 }
 template <int E>
 __device__ __forceinline__ void pp_load_row(uint32_t t, float (&y)[E]) {
+    uint32_t o[E / 32][32];
 #pragma unroll
-    for (int c = 0; c < E / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(t + 32 * c, o);
-        tmem_wait_ld();
+    for (int c = 0; c < E / 32; ++c) tmem_ld32(t + 32 * c, o[c]);
+    tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) y[32 * c + k] = __uint_as_float(o[k]);
-    }
+    for (int k = 0; k < E; ++k) y[k] = __uint_as_float(o[k / 32][k % 32]);
 }
 
 // 16 columns of each of a row's pieces (64 columns apart), and the
@@ -584,7 +578,7 @@ template <int D>
 __global__ void __launch_bounds__(PpGeo<D>::kThreads, 1)
 k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefillConsts P, int* status) {
     using Z = PpGeo<D>;
-    constexpr int N = Z::kN, W = Z::kD, SW = Z::kSoftWarps, NS = Z::kStages;
+    constexpr int N = Z::kN, W = Z::kD, SW = Z::kSoftWarps, DW = Z::kDeqWarps, NS = Z::kStages;
     constexpr int PARTS = D < 64 ? 1 : D / 64;  // register-sized pieces of a row
     constexpr int E = D < 64 ? D : 64;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -618,10 +612,10 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&stage_full[i], 1);
-            mbar_init(&stage_free[i], 8);
+            mbar_init(&stage_free[i], DW);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&kv_full[i], 8);
+            mbar_init(&kv_full[i], DW);
             mbar_init(&kv_free[i], 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(&meta_full[i], 1);
@@ -632,7 +626,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&job_full[i], 1);
-            mbar_init(&job_free[i], SW + 10);
+            mbar_init(&job_free[i], SW + DW + 2);
         }
         mbar_init(q_full, SW);
         mbar_init(meet, SW);
@@ -641,7 +635,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         mbar_fence_init();
         start->left = 0;
     }
-    if (warp == SW + 8) tmem_alloc<512>(slot);
+    if (warp == SW + DW) tmem_alloc<512>(slot);
 
     griddep_wait();  // from here on: what earlier kernels wrote
     // ---- this CTA's share: the sequences' weights, scanned over the block
@@ -727,7 +721,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         return p.nb >= 0;
     };
 
-    if (warp == SW + 9) {
+    if (warp == SW + DW + 1) {
         // ---- copies: lane 4 s + a brings array a of segment s (min(page, N)
         // positions) of a block
         const int seg = min(1 << A.shift, N), nseg = N / seg;
@@ -767,19 +761,25 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             __syncwarp();
             if (!more) break;
             if (!u.whole) has |= u.head ? 2 : 1;
+            // this lane's segment of block j: its page, or -1; looked up a block ahead
+            auto page_of = [&](int j) {
+                const int pos = (u.lo_blk + j) * N + s * seg;
+                return s < nseg && j < u.blk1 && pos < u.kv_end
+                           ? __ldg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift))
+                           : INT_MIN;
+            };
+            int next_page = page_of(u.blk0);
             for (int j = u.blk0; j < u.blk1; ++j, ++tc) {
                 const int st = tc % NS;
                 const int pos = (u.lo_blk + j) * N + s * seg;
-                bool have = s < nseg && pos < u.kv_end;
-                int64_t src = 0;
-                if (have) {
-                    const int page = __ldg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift));
-                    if (page < 0 || page >= A.c.n_pages) {
-                        report_timeout(status, kPpStatusPage);
-                        have = false;
-                    }
-                    src = (((int64_t)page * A.Hkv + u.h) << A.shift) + (pos & ((1 << A.shift) - 1));
+                const int page = next_page;
+                next_page = page_of(j + 1);
+                bool have = page != INT_MIN;
+                if (have && (page < 0 || page >= A.c.n_pages)) {
+                    report_timeout(status, kPpStatusPage);
+                    have = false;
                 }
+                const int64_t src = (((int64_t)page * A.Hkv + u.h) << A.shift) + (pos & ((1 << A.shift) - 1));
                 if (tc >= (uint32_t)NS) ok = pp_wait(&stage_free[st], (tc / NS - 1) & 1, abort_f, status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -820,7 +820,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         // the copies issued have landed before the CTA leaves (bounded)
         if (lane == 0 && tc > 0)
             for (uint32_t t = tc > (uint32_t)NS ? tc - NS : 0; t < tc; ++t) mbar_wait(&stage_full[t % NS], (t / NS) & 1);
-    } else if (warp == SW + 8) {
+    } else if (warp == SW + DW) {
         // ---- MMAs.  The whole warp walks through the steps and one elected lane
         // issues: with a warp-uniform flow the descriptors are computed in
         // uniform registers and the products follow one another at the tensor
@@ -844,55 +844,60 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             ok = __all_sync(0xFFFFFFFFu, wait(q_full, items & 1));
             ++items;
             const int T = pair ? 2 * nb : nb;
-            for (int t = 0; ok && t < T + 2; ++t) {
+            for (int t = 0; t < T + 2; ++t) {
                 const int g = t & 1;
                 // a pair's second step reads the tiles that the first one waited
                 // for, and frees them
                 const bool first_use = !(pair && g), last_use = !pair || g;
                 const uint32_t tk = tc0 + (pair ? t >> 1 : t), tv = tk - (pair ? 1 : 2);  // blocks of S and PV
                 const uint32_t slk = (2 * tk) & 3, slv = (2 * tv + 1) & 3;
+                // operands and barriers first: nothing is left between a wait and its products
+                const uint64_t vt = dv + ((slv * Z::kTile) >> 4), kt = dk + ((slk * Z::kTile) >> 4);
+                const uint64_t qt = dq + ((pair && g ? Z::kQTile : 0u) >> 4);
+                const uint32_t o = tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0);
+                const uint32_t d = tmem + Z::kTmemS + N * g;
+                const uint32_t more = (Z::kStreams == 2 ? t < 4 : t == 2) ? 0u : 1u;  // 0: the output's first product
+                uint64_t *bp = &p_full[g], *bpv = &pv_done[g], *bs = &s_full[g], *bvf = &kv_free[slv], *bkf = &kv_free[slk];
+                if (t < T && first_use && t < 2) ok = wait(&kv_full[slk], (tk >> 1) & 1) && ok;
                 if (t >= 2) {
                     const uint32_t n = g ? n1++ : n0++;
-                    if (first_use) ok = wait(&kv_full[slv], (tv >> 1) & 1) && ok;
-                    ok = wait(&p_full[g], n & 1) && ok;
+                    ok = wait(bp, n & 1) && ok;
                     tc_fence_after();
-                    const uint64_t vt = dv + ((slv * Z::kTile) >> 4);
-                    const uint32_t o = tmem + Z::kTmemO + (Z::kStreams == 2 ? 128 * g : 0);
-                    const uint32_t pa = tmem + Z::kTmemS + N * g;
-                    // 0 for the output's first product
-                    const uint32_t more = (Z::kStreams == 2 ? t < 4 : t == 2) ? 0u : 1u;
                     if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < N / 16; ++kk)
-                            umma_f16_ts(o, pa + 8 * kk, vt + ((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
-                        umma_commit(&pv_done[g]);
-                        if (last_use) umma_commit(&kv_free[slv]);
+                            umma_f16_ts(o, d + 8 * kk, vt + ((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
+                        umma_commit(bpv);
+                        if (last_use) umma_commit(bvf);
                     }
                     __syncwarp();
+                    // under the products: the next step's V tile, this step's K tile;
+                    // the buffer takes the next scores once P has been read
                     if (t < T) {
-                        // the buffer takes the next scores once P has been read
                         if (first_use) ok = wait(&kv_full[slk], (tk >> 1) & 1) && ok;
-                        ok = wait(&pv_done[g], n & 1) && ok;
+                        ok = wait(bpv, n & 1) && ok;
                     }
-                } else if (t < T && first_use) {
-                    ok = wait(&kv_full[slk], (tk >> 1) & 1);
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
                 if (t < T) {
                     tc_fence_after();
-                    const uint64_t kt = dk + ((slk * Z::kTile) >> 4);
-                    const uint64_t qt = dq + ((pair && g ? Z::kQTile : 0u) >> 4);
-                    const uint32_t d = tmem + Z::kTmemS + N * g;
                     if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < W / 16; ++kk)
                             umma_f16(d, qt + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                                      kt + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-                        umma_commit(&s_full[g]);
-                        if (last_use) umma_commit(&kv_free[slk]);
+                        umma_commit(bs);
+                        if (last_use) umma_commit(bkf);
                     }
                     __syncwarp();
+                }
+                // under the scores' product: the V tile of the next step's product
+                if (t >= 1 && t + 1 < T + 2 && !(pair && !g)) {
+                    const uint32_t tn = tc0 + (pair ? (t + 1) >> 1 : t + 1) - (pair ? 1 : 2);
+                    ok = wait(&kv_full[(2 * tn + 1) & 3], (tn >> 1) & 1) && ok;
                 }
             }
             tc0 += nb;
@@ -902,7 +907,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             __syncwarp();
             mbar_wait(drain, 0);
         }
-    } else if (warp == SW + 10) {
+    } else if (warp == SW + DW + 2) {
         // ---- norms: a block's powers of two, and its rows' factors in the
         // norms' place
         uint32_t tc = 0;
@@ -958,13 +963,13 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         }
     } else if (warp >= SW) {
         // ---- expansion: thread = (row, sub) of the block
-        constexpr int TPR = 256 / N;
+        constexpr int TPR = 32 * DW / N;  // threads per row
         const int dt = tid - 32 * SW;
         const int row = dt % N, sub = dt / N;
         if (D < 64) {  // the padded half of the tiles stays zero
-            for (uint32_t i = dt; i < 4 * Z::kTile / 16; i += 256)
+            for (uint32_t i = dt; i < 4 * Z::kTile / 16; i += 32 * DW)
                 reinterpret_cast<uint4*>(sm + Z::kRing)[i] = make_uint4(0, 0, 0, 0);
-            asm volatile("bar.sync 2, 256;" ::: "memory");
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * DW) : "memory");
         }
         uint32_t tc = 0;
         bool ok = true;
@@ -1039,26 +1044,31 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             if (nb > 0 && (pair || g == 0)) {
                 float amax = 0.f;
                 const __nv_bfloat16* src = A.q + qrow * D;
+                if (rvalid) {  // the later pieces' lines are on their way during the first one's work
+#pragma unroll
+                    for (int h = 1; h < PARTS; ++h)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * h));
+                }
 #pragma unroll 1
                 for (int h = 0; h < PARTS; ++h) {
                     float y[E];
                     {
                         uint32_t u[E / 2];
 #pragma unroll
-                        for (int k = 0; k < E / 16; ++k) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) u[8 * k + c] = 0u;
-                            if (rvalid) pp_ld256(src + 64 * h + 16 * k, u + 8 * k);
+                        for (int k = 0; k < E / 8; ++k) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (rvalid) v = __ldg(reinterpret_cast<const uint4*>(src + 64 * h) + k);
+                            u[4 * k] = v.x, u[4 * k + 1] = v.y, u[4 * k + 2] = v.z, u[4 * k + 3] = v.w;
                         }
 #pragma unroll
                         for (int k = 0; k < E / 2; ++k) {
-                            y[2 * k] = __uint_as_float(u[k] << 16);
-                            y[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+                            const uint32_t v = u[k] ^ P.sgnh[32 * h + k];
+                            y[2 * k] = __uint_as_float(v << 16);
+                            y[2 * k + 1] = __uint_as_float(v & 0xFFFF0000u);
                         }
                     }
 #pragma unroll
                     for (int k = 0; k < E; k += 2) amax = pp_max3(amax, fabsf(y[k]), fabsf(y[k + 1]));
-                    pp_signs<E>(y, P.sgnb + 2 * h);
                     fwht_reg2<E>(y);
                     pp_store_row<E>(t_out + 64 * h, y);
                 }
@@ -1078,15 +1088,18 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     pp_across<PARTS>(t_out + 16 * c, y);
 #pragma unroll
                     for (int h = 0; h < PARTS; ++h) {
-                        const uint32_t flip = P.two_sided ? (P.sgn2b[2 * h + (c >> 1)] >> (16 * (c & 1))) & 0xFFFFu : 0u;
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const __half2 hh = __floats2half2_rn(__uint_as_float(y[h][2 * k]) * inv,
                                                                  __uint_as_float(y[h][2 * k + 1]) * inv);
-                            // signs of dims 2 k and 2 k + 1 onto bits 15 and 31
-                            const uint32_t sg = ((flip << (15 - 2 * k)) & 0x8000u) | ((flip << (30 - 2 * k)) & 0x80000000u);
-                            w[k] = *reinterpret_cast<const uint32_t*>(&hh) ^ sg;
+                            w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                        }
+                        if (P.two_sided) {  // signs of dims 2 k and 2 k + 1 onto bits 15 and 31
+                            const uint32_t flip = (P.sgn2b[2 * h + (c >> 1)] >> (16 * (c & 1))) & 0xFFFFu;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                w[k] ^= ((flip << (15 - 2 * k)) & 0x8000u) | ((flip << (30 - 2 * k)) & 0x80000000u);
                         }
                         unsigned char* qh = qt + h * 16384;
                         *reinterpret_cast<uint4*>(qh + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1266,24 +1279,25 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                         if (write) {
 #pragma unroll
                             for (int h = 0; h < PARTS; ++h) {
-                                const uint32_t flip = P.sgnb[2 * h + (c >> 1)] >> (16 * (c & 1));
-                                uint32_t v[16];
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    v[k] = __float_as_uint(__uint_as_float(y[h][k]) * inv) ^ ((flip << (31 - k)) & 0x80000000u);
                                 const int64_t at = qrow * D + 64 * h + 16 * c;
                                 if (A.out_bf16) {
                                     uint32_t w[8];
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) {
-                                        const __nv_bfloat162 bb =
-                                            __floats2bfloat162_rn(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-                                        w[k] = *reinterpret_cast<const uint32_t*>(&bb);
+                                        const __nv_bfloat162 bb = __floats2bfloat162_rn(
+                                            __uint_as_float(y[h][2 * k]) * inv, __uint_as_float(y[h][2 * k + 1]) * inv);
+                                        w[k] = *reinterpret_cast<const uint32_t*>(&bb) ^ P.sgnh[32 * h + 8 * c + k];
                                     }
                                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + at);
                                     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                                     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                                 } else {
+                                    const uint32_t flip = P.sgnb[2 * h + (c >> 1)] >> (16 * (c & 1));
+                                    uint32_t v[16];
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        v[k] = __float_as_uint(__uint_as_float(y[h][k]) * inv) ^
+                                               ((flip << (31 - k)) & 0x80000000u);
                                     uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.out) + at);
 #pragma unroll
                                     for (int k = 0; k < 4; ++k)
@@ -1322,7 +1336,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     griddep_launch();
     tc_fence_before();
     __syncthreads();
-    if (warp == SW + 8) {
+    if (warp == SW + DW) {
         tc_fence_after();
         tmem_dealloc<512>(tmem);
     }
