@@ -75,6 +75,13 @@ struct PpGeo {
     static constexpr int kN = D == 256 ? 64 : 128;    // positions per block
     static constexpr int kRows = PagedPrefillGeo<D>::kRows;
     static constexpr int kStreams = D == 256 ? 1 : 2;
+    // The cost of a block for two row tiles and for one, and of an item's query
+    // rotation and output, by which the line of work is cut into shares.  One row
+    // tile costs nearly what two do (the expansion is the same): 32 sequences of
+    // 1-496 tokens over 0.2-8k positions took 339 us with 2 : 1 and 2 blocks an
+    // item, 233 us with these.
+    static constexpr int kCostPair = kStreams == 2 ? 6 : 1, kCostSplit = kStreams == 2 ? 5 : 1;
+    static constexpr int kCostItem = 5 * kCostPair;
     static constexpr int kSoftWarps = 4 * kStreams;
     static constexpr int kDeqWarps = 8;
     static constexpr int kWarps = kSoftWarps + kDeqWarps + 3;
@@ -152,10 +159,10 @@ struct PpSeq {
         // tiles before the window's cap binds: base + (k + 1) kRows < cap
         kstar = cap == INT64_MAX ? INT32_MAX : (cap - base - 1) / Z::kRows;
         if (cap - base - 1 < 0) kstar = 0;
-        over = 2 * (int64_t)Z::kN * G;
+        over = (int64_t)Z::kCostItem * Z::kN * G;
     }
     __device__ int factor(int i) const {
-        return Z::kStreams == 2 && rows - (int64_t)i * Z::kRows > 128 ? 2 : 1;
+        return rows - (int64_t)i * Z::kRows > 128 ? Z::kCostPair : Z::kCostSplit;
     }
     __device__ int64_t weight(int i) const {
         int64_t e = base + min((int64_t)(i + 1) * Z::kRows, (int64_t)rows);
@@ -168,7 +175,7 @@ struct PpSeq {
         const int64_t m = min((int64_t)i, kstar);
         int64_t s = m * base + (int64_t)Z::kRows * (m * (m + 1) / 2);
         if (i > m) s += (i - m) * cap;
-        return Z::kStreams * s + i * over;
+        return Z::kCostPair * s + i * over;
     }
 };
 
