@@ -519,7 +519,7 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
         _same_device(dev, out)
         if out.shape != q.shape:
             raise ValueError("out must be [n_q, Hq, d]")
-        ws = _scratch(workspace, tq_attn_prefill_paged_workspace_bytes(Hq, cache.Hkv, d), dev)
+        ws = _scratch(workspace, dev, tq_attn_prefill_paged_workspace_bytes, Hq, cache.Hkv, d)
         _check("tq_attn_prefill_paged", lib().tq_attn_prefill_paged(
             plan.handle, q.data_ptr(), n_q, B, Hq, cache.Hkv, cache.view(), block_table.data_ptr(),
             block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), window, cache.k_bits, cache.v_bits,
@@ -584,12 +584,10 @@ class PageTable:
 def _ints(device, *ts):
     """Contiguous int32 CUDA tensors on `device`."""
     for t in ts:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("expected contiguous CUDA tensors")
         if t.dtype != torch.int32:
             raise TypeError("expected int32 tensors")
-        if t.device != device:
-            raise ValueError("all tensors must be on one device")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError("expected contiguous CUDA tensors on one device")
 
 
 def _raw_stream(device):
@@ -612,11 +610,12 @@ def _layers(x) -> PagedLayers:
     return x if isinstance(x, PagedLayers) else PagedLayers(x)
 
 
-def _scratch(workspace, need: int, device):
+def _scratch(workspace, device, bytes_fn, *sizes):
+    """The workspace, or a new one of bytes_fn(*sizes) bytes."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _cuda(workspace)
-    _same_device(device, workspace)
+        return torch.empty(max(bytes_fn(*sizes), 16), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous CUDA tensor on the call's device")
     return workspace
 
 
@@ -639,7 +638,7 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
     if src.device != dst.device:
         raise ValueError("src and dst must be on one device")
     with _on(dst.device):
-        ws = _scratch(workspace, tq_pages_workspace_bytes(0, 0, dst.n_pages), dst.device)
+        ws = _scratch(workspace, dst.device, tq_pages_workspace_bytes, 0, 0, dst.n_pages)
         _check("tq_pages_copy", lib().tq_pages_copy(
             src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(),
             src_ids.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dst.device)))
@@ -656,13 +655,13 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         if out is None:
             out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
         if info is None:
-            info = torch.empty(2, dtype=torch.int32, device=dev)
+            info = table.lens.new_empty(2)
         other = moved if arg is None else arg
         _ints(dev, info, other)
         if info.numel() != 2 or other.numel() != (layers.n_pages if arg is None else n_seqs):
             raise ValueError("info has 2 entries, parents and new_lens one per row, moved_to one per page")
         a, b = table._view(layers, shape), out._view(layers, shape)
-        ws = _scratch(workspace, tq_pages_workspace_bytes(n_seqs, max_pages, layers.n_pages), dev)
+        ws = _scratch(workspace, dev, tq_pages_workspace_bytes, n_seqs, max_pages, layers.n_pages)
         middle = (a, b, other.data_ptr()) if arg is None else (a, other.data_ptr(), b)
         _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,
                                       info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),

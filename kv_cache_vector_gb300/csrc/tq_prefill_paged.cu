@@ -14,7 +14,7 @@
 // serves two MMA row tiles.
 //
 //   warps 0-7    softmax, one thread per query row (4 warps at d = 256)
-//   8 warps     expansion: bytes -> fp16 levels times the row's norm
+//   8 warps      expansion: bytes -> fp16 levels times the row's norm
 //   1 warp       MMAs
 //   1 warp       copies of packed rows and norms from the pages (bulk copies);
 //                it also walks along the CTA's parts and hands them out
@@ -39,10 +39,23 @@
 // so that O = sum P' V' keeps its precision however the norms vary from block
 // to block, and the denominator sums P' 2^(Eb - Ev) in fp32 (Eb: Ev of the
 // first block).  M moves only when it grows by more than 8, so P' < 2^8.
-// Each operand is rounded to fp16 once after its fp32 (query, P) or fp16
-// (level times norm) value: 2^-11 relative steps, an eighth of the bf16
-// output's.  A non-finite norm makes the scores of its row NaN (only rows
+// The query, P and the products of level and norm are rounded to fp16 once,
+// 2^-11 relative, an eighth of the bf16 output's step (V's norms once more,
+// before the product).  A non-finite norm makes the scores of its row NaN (only rows
 // that attend to it see them) and its V row zero.
+//
+// What bounds it.  Two chunks of 4096 tokens over 12-16k positions (32 / 8
+// heads, d = 128, K4/V3): 1.39 ms, 1.13 PFLOP/s of useful products, 59% of the
+// measured burst rate; about 4400 cycles per block and 256 rows, of which the
+// products need 2048.  A stream's step is a chain (scores 512 cycles and more,
+// as both operands come from shared memory that the expansion writes at the
+// same time; softmax about 2300; product with V 512; a barrier's wake-up of
+// about 110 between each), and two streams do not fill all of it.  With one
+// row tile the expansion's byte permutes set the pace, about 3800 cycles per
+// block: 24 sequences of 1-4 tokens over 6-9k positions read 1.1 TB/s of
+// packed rows.  Measured and not taken: score buffers of 64 columns, two per
+// stream (1886 us); two softmax threads per row (1532 us); separate warps for
+// the two kinds of products (1633 us); 4 or 16 expansion warps (1486 and 1570 us).
 //
 // Every wait on an mbarrier is bounded (2 s); one that gives up sets the
 // device status word and a flag that ends the others.  The softmax warps go
@@ -294,8 +307,7 @@ __device__ __forceinline__ uint64_t uniform(uint64_t v) {
     return ((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v);
 }
 
-// A try_wait that may suspend the warp for up to 100 us: the default limit is
-// short, and warps that spin take issue slots from the working ones.
+// A try_wait that may suspend the warp for up to 100 us.
 __device__ __forceinline__ bool pp_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
