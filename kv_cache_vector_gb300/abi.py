@@ -506,6 +506,8 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
         raise ValueError("q and cache must have the plan's head dimension")
     if cu_q.numel() != B + 1 or block_table.shape[0] != B:
         raise ValueError("cu_q [B + 1], ctx_lens [B] and block_table [B, max_pages] expected")
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be in [0, 2^31)")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
     _cuda(q)

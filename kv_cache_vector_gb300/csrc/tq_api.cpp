@@ -1124,7 +1124,8 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
     c.Hkv = Hkv;
     c.max_pages = max_pages;
     c.page_shift = shift;
-    c.window = window;
+    // a window past every length is none: below 2^30 a position minus it stays in 32 bits
+    c.window = window >= ((int64_t)max_pages << shift) ? 0 : window;
     c.k_bits = k_bits;
     c.v_bits = v_bits;
     c.out_bf16 = out_dtype == TQ_BF16;

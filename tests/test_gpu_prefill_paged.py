@@ -243,6 +243,14 @@ def test_non_finite_norms_reach_only_rows_that_attend(which, value, d):
     run_both(bt, 1 / math.sqrt(d), window=64)
 
 
+@pytest.mark.parametrize("window", [400, 4000, 2 ** 30 + 5, 2 ** 31 - 1])
+def test_a_window_past_every_length_is_none(window):
+    """Also for tokens before the first position (a position minus the window stays in 32 bits)."""
+    bt = Batch(15, [(300, 40), (5, 200), (140, 300)], 4, 2, 128, 64, 4, 3)
+    out = run_both(bt, 0.1, window)
+    assert torch.equal(out, abi.tq_attn_prefill_paged(*bt.gpu(), 0.1))
+
+
 def test_rows_outside_every_sequence_keep_their_values():
     bt = Batch(9, [(3, 90), (0, 0), (5, 5)], 4, 2, 128, 32, 4, 3, tail=4)
     bt.cu = bt.cu + 2  # two rows before the first sequence, two behind the last
