@@ -156,8 +156,8 @@ struct PpSeq {
 
     __device__ void load(const PpArgs& A, int b, int* status) {
         G = A.Hq / A.Hkv;
-        const int64_t c0 = __ldg(A.cu + b), c1 = __ldg(A.cu + b + 1);
-        ctx = __ldg(A.ctx + b);
+        const int64_t c0 = __ldcg(A.cu + b), c1 = __ldcg(A.cu + b + 1);
+        ctx = __ldcg(A.ctx + b);
         if (c0 < 0 || c1 < c0 || c1 > A.n_q || ctx < 0 || ctx > ((int64_t)A.max_pages << A.shift) ||
             (c1 - c0) * G > INT32_MAX) {
             if (status) report_timeout(status, kPpStatusRange);
@@ -624,8 +624,12 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     long long* share = reinterpret_cast<long long*>(sm + Z::kCur + 48);  // units of a share
     long long* red = reinterpret_cast<long long*>(sm + Z::kRed);
 
-    if (sa & 1023u) {  // the tiles' swizzle needs it; the whole grid leaves
-        if (tid == 0) report_timeout(status, kPpStatusAlign);
+    if (sa & 1023u) {  // the tiles' swizzle needs it; the whole grid leaves, with nothing to join
+        if (tid == 0) {
+            report_timeout(status, kPpStatusAlign);
+            griddep_wait();
+            *reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta) = make_int4(0, -1, 0, 0);
+        }
         return;
     }
     if (tid == 0) {
@@ -656,7 +660,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     }
     if (warp == SW + DW) tmem_alloc<512>(slot);
 
-    griddep_wait();  // from here on: what earlier kernels wrote
+    // From here on: what earlier kernels wrote.  No read-only loads (__ldg): they
+    // may be taken ahead of the wait, as these values change within the grid's life.
+    griddep_wait();
     // ---- this CTA's share: the sequences' weights, scanned over the block
     {
         const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
@@ -767,7 +773,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 m->nb = more ? u.blk1 - u.blk0 : -1;
                 if (more) {
                     m->flags = (u.pair ? kJobPair : 0) | (u.whole ? kJobWhole : 0) | (u.head ? kJobHead : 0);
-                    m->q0 = __ldg(A.cu + u.b);
+                    m->q0 = __ldcg(A.cu + u.b);
                     m->h = u.h;
                     m->row0 = u.row0;
                     m->rows = u.rows;
@@ -784,7 +790,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             auto page_of = [&](int j) {
                 const int pos = (u.lo_blk + j) * N + s * seg;
                 return s < nseg && j < u.blk1 && pos < u.kv_end
-                           ? __ldg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift))
+                           ? __ldcg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift))
                            : INT_MIN;
             };
             int next_page = page_of(u.blk0);
@@ -833,7 +839,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             }
             const int row0 = cur.i * Z::kRows;
             int4* m = reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta);
-            m[0] = make_int4(has, owner ? last : -1, owner ? __ldg(A.cu + cur.b) : 0, cur.h);
+            m[0] = make_int4(has, owner ? last : -1, owner ? __ldcg(A.cu + cur.b) : 0, cur.h);
             m[1] = make_int4(row0, owner ? min(Z::kRows, seq.rows - row0) : 0, 0, 0);
         }
         // the copies issued have landed before the CTA leaves (bounded)
@@ -1076,7 +1082,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
 #pragma unroll
                         for (int k = 0; k < E / 8; ++k) {
                             uint4 v = make_uint4(0, 0, 0, 0);
-                            if (rvalid) v = __ldg(reinterpret_cast<const uint4*>(src + 64 * h) + k);
+                            if (rvalid) v = reinterpret_cast<const uint4*>(src + 64 * h)[k];
                             u[4 * k] = v.x, u[4 * k + 1] = v.y, u[4 * k + 2] = v.z, u[4 * k + 3] = v.w;
                         }
 #pragma unroll

@@ -243,6 +243,22 @@ def test_non_finite_norms_reach_only_rows_that_attend(which, value, d):
     run_both(bt, 1 / math.sqrt(d), window=64)
 
 
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("d", [32, 128, 256])
+def test_non_finite_queries_stay_in_their_row(value, d):
+    bt = Batch(14, [(60, 200), (3, 500), (200, 260)], 4, 2, d, 64, 4, 3)
+    args = bt.gpu()
+    clean = abi.tq_attn_prefill_paged(*args, 0.1)
+    bad = torch.zeros(clean.shape[:2], dtype=torch.bool)
+    for row, h in ((0, 0), (7, 1), (61, 2), (100, 3), (262, 0)):
+        args[1][row, h, d // 2 + 1] = value
+        bad[row, h] = True
+    out = abi.tq_attn_prefill_paged(*args, 0.1)
+    assert abi.tq_device_status(reset=True) == 0
+    assert out[bad.cuda()].isnan().all()
+    assert torch.equal(out[~bad.cuda()], clean[~bad.cuda()])
+
+
 @pytest.mark.parametrize("window", [400, 4000, 2 ** 30 + 5, 2 ** 31 - 1])
 def test_a_window_past_every_length_is_none(window):
     """Also for tokens before the first position (a position minus the window stays in 32 bits)."""
