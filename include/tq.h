@@ -385,8 +385,11 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
  * a counted page without holder) changes nothing either; info is {0, -1} and
  * the device status word 61.
  * workspace: tq_pages_workspace_bytes(n_seqs, max_pages, n_pages) bytes.
+ * Where refs counts fewer holders than the rows have, the results are not
+ * specified (no access leaves its array).
  * Alignment: 16 bytes for every cache array (norms too) and the workspace, 4
- * for the books.  d is a power of two in [32, 256]; n_pages < 2^31.
+ * for the books.  d is a power of two in [32, 256]; n_pages < 2^31; n_seqs in
+ * [1, 2^18].
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, bits, page_size),
  * TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
 typedef struct {

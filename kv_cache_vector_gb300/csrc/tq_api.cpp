@@ -882,8 +882,10 @@ tq_status tq_attn_decode_append_paged(const tq_plan* plan, const void* q, const 
 
 // ------------------------------------------------------------ upkeep of the pages
 
+static constexpr int kMaxRows = 1 << 18;  // of a page table
+
 size_t tq_pages_workspace_bytes(int n_seqs, int max_pages, int64_t n_pages) {
-    if (n_seqs < 0 || max_pages < 0 || n_pages < 1 || n_pages > INT32_MAX) return 0;
+    if (n_seqs < 0 || n_seqs > kMaxRows || max_pages < 0 || n_pages < 1 || n_pages > INT32_MAX) return 0;
     return tq::pages_workspace_bytes(n_seqs, n_pages);
 }
 
@@ -934,7 +936,9 @@ tq_status pages_call(int op, tq_page_table in, tq_page_table out, const int32_t*
         !aligned4(out.lens) || !aligned4(out.refs) || !aligned4(info) || !aligned4(arg) || !aligned4(moved))
         return TQ_ERR_ALIGNMENT;
     const int shift = page_shift_of(layers[0].page_size);
-    if (((int64_t)max_pages << shift) > INT32_MAX) return TQ_ERR_UNSUPPORTED;  // lengths are int32
+    // lengths are int32; a row's place among the copied pages has 23 bits, and rows that
+    // go on in one shared page are counted one after the other
+    if (((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows) return TQ_ERR_UNSUPPORTED;
     const int64_t n_pages = layers[0].n_pages;
     if (!workspace || workspace_bytes < tq::pages_workspace_bytes(n_seqs, n_pages)) return TQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;

@@ -124,6 +124,18 @@ def test_refusals_of_the_books(L):
     assert L.tq_pages_compact(a, b, A + 8192, 4, 8, ly, 1, 2, 128, 4, 3, info, W, need, None) == 1  # moved_to on refs
 
 
+def test_most_rows_of_a_table(L):
+    a, b = abi.PageTableView(1 << 32, 1 << 33, 1 << 34), abi.PageTableView(1 << 35, 1 << 36, 1 << 37)
+    ly, n = _layers(_cache(1 << 40)), (1 << 18) + 1
+    assert L.tq_pages_workspace_bytes(n, 8, 4) == 0
+    need, W = 1 << 30, 1 << 38
+    assert L.tq_pages_fork(a, 1 << 39, b, n, 8, ly, 1, 2, 128, 4, 3, 1 << 20, W, need, None) == 2
+    assert L.tq_pages_resize(a, 1 << 39, b, n, 8, ly, 1, 2, 128, 4, 3, 1 << 20, W, need, None) == 2
+    assert L.tq_pages_compact(a, b, 1 << 39, n, 8, ly, 1, 2, 128, 4, 3, 1 << 20, W, need, None) == 2
+    # the most rows: refused for the workspace only
+    assert L.tq_pages_fork(a, 1 << 39, b, n - 1, 8, ly, 1, 2, 128, 4, 3, 1 << 20, None, 0, None) == 5
+
+
 def test_refusals_of_the_copy(L):
     ids, W = 1 << 20, 1 << 28
     one, two = _layers(_cache()), _layers(_cache(1 << 36))
