@@ -914,11 +914,28 @@ tq_status check_layers(const tq_paged_cache* layers, int n_layers, int Hkv, int 
     return TQ_OK;
 }
 
+bool layers_accessible(const tq_paged_cache* layers, int n_layers) {
+    for (int l = 0; l < n_layers; ++l)
+        if (!paged_accessible(layers[l])) return false;
+    return true;
+}
+
 // Bytes of array a (0 packed K, 1 K norms, 2 packed V, 3 V norms) of a layer.
 Span layer_span(const tq_paged_cache& c, int a, int Hkv, int d, int k_bits, int v_bits) {
     const uint64_t rows = (uint64_t)c.n_pages * Hkv * c.page_size;
     const void* p = a == 0 ? (const void*)c.k_packed : a == 1 ? (const void*)c.k_norm : a == 2 ? (const void*)c.v_packed : (const void*)c.v_norm;
     return {reinterpret_cast<uintptr_t>(p), rows * (a == 0 ? d * k_bits / 8 : a == 2 ? d * v_bits / 8 : 4)};
+}
+
+// From the first byte of a layer's arrays to the last.
+Span layer_run(const tq_paged_cache& c, int Hkv, int d, int k_bits, int v_bits) {
+    uintptr_t lo = UINTPTR_MAX, hi = 0;
+    for (int a = 0; a < 4; ++a) {
+        const Span s = layer_span(c, a, Hkv, d, k_bits, v_bits);
+        lo = s.at < lo ? s.at : lo;
+        hi = s.at + s.bytes > hi ? s.at + s.bytes : hi;
+    }
+    return {lo, hi - lo};
 }
 
 // Fork, resize and compaction: the checks they share, then the launch.
@@ -962,7 +979,7 @@ tq_status pages_call(int op, tq_page_table in, tq_page_table out, const int32_t*
     if (!device_accessible(in.block_table) || !device_accessible(in.lens) || !device_accessible(in.refs) ||
         !device_accessible(out.block_table) || !device_accessible(out.lens) || !device_accessible(out.refs) ||
         !device_accessible(info) || !device_accessible(workspace) || (arg && !device_accessible(arg)) ||
-        (moved && !device_accessible(moved)) || !paged_accessible(layers[0]))
+        (moved && !device_accessible(moved)) || !layers_accessible(layers, n_layers))
         return TQ_ERR_INVALID_ARG;
     tq::PagesCall c = {};
     c.in = in;
@@ -995,24 +1012,37 @@ tq_status tq_pages_copy(const tq_paged_cache* src, const tq_paged_cache* dst, in
     if (src[0].page_size != dst[0].page_size || n > dst[0].n_pages) return TQ_ERR_INVALID_ARG;
     // one pool, layer by layer, or two that share nothing
     const bool same = src[0].k_packed == dst[0].k_packed;
-    for (int l = 0; l < n_layers; ++l) {
+    for (int l = 0; same && l < n_layers; ++l) {
         const tq_paged_cache &a = src[l], &b = dst[l];
-        if (same && (a.k_packed != b.k_packed || a.k_norm != b.k_norm || a.v_packed != b.v_packed ||
-                     a.v_norm != b.v_norm || a.n_pages != b.n_pages))
+        if (a.k_packed != b.k_packed || a.k_norm != b.k_norm || a.v_packed != b.v_packed || a.v_norm != b.v_norm ||
+            a.n_pages != b.n_pages)
             return TQ_ERR_INVALID_ARG;
-        if (!same)
-            for (int m = 0; m < n_layers; ++m)
-                for (int k = 0; k < 4; ++k)
-                    if (overlap(layer_span(a, k, Hkv, d, k_bits, v_bits), layer_span(dst[m], k, Hkv, d, k_bits, v_bits)))
+    }
+    // (an array against an array only where the runs of memory that the layers' arrays lie in meet)
+    for (int m0 = 0; !same && m0 < n_layers; m0 += 64) {
+        Span run[64];
+        const int mn = n_layers - m0 < 64 ? n_layers - m0 : 64;
+        for (int m = 0; m < mn; ++m) run[m] = layer_run(dst[m0 + m], Hkv, d, k_bits, v_bits);
+        for (int l = 0; l < n_layers; ++l) {
+            const Span r = layer_run(src[l], Hkv, d, k_bits, v_bits);
+            for (int m = 0; m < mn; ++m)
+                for (int k = 0; overlap(r, run[m]) && k < 16; ++k)
+                    if (overlap(layer_span(src[l], k & 3, Hkv, d, k_bits, v_bits),
+                                layer_span(dst[m0 + m], k >> 2, Hkv, d, k_bits, v_bits)))
                         return TQ_ERR_INVALID_ARG;
+        }
     }
     if (n == 0) return TQ_OK;
     if (!src_ids || !dst_ids) return TQ_ERR_INVALID_ARG;
     if (!aligned4(src_ids) || !aligned4(dst_ids)) return TQ_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < tq::pages_workspace_bytes(0, dst[0].n_pages)) return TQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+    const Span ws{reinterpret_cast<uintptr_t>(workspace), tq::pages_workspace_bytes(0, dst[0].n_pages)};
+    if (overlap(ws, {reinterpret_cast<uintptr_t>(src_ids), 4 * (uint64_t)n}) ||
+        overlap(ws, {reinterpret_cast<uintptr_t>(dst_ids), 4 * (uint64_t)n}))
+        return TQ_ERR_INVALID_ARG;
     if (!device_accessible(src_ids) || !device_accessible(dst_ids) || !device_accessible(workspace) ||
-        !paged_accessible(src[0]) || !paged_accessible(dst[0]))
+        !layers_accessible(src, n_layers) || !layers_accessible(dst, n_layers))
         return TQ_ERR_INVALID_ARG;
     tq::PagesCall c = {};
     c.arg = src_ids;

@@ -152,6 +152,12 @@ def test_refusals_of_the_copy(L):
     assert copy(t=_layers(_cache((1 << 32) + 4096))) == 1                  # overlapping pools
     assert copy(s=_layers(_cache(), _cache(1 << 36)), t=_layers(_cache(1 << 36), _cache(1 << 40)), nl=2) == 1
     assert copy(s=_layers(_cache(), _cache(1 << 36)), t=_layers(_cache(), _cache(1 << 40)), nl=2) == 1
+    # a K array of one pool over a V array of the other, a few layers on
+    far = [_cache((40 + i) << 32) for i in range(70)]
+    assert copy(s=_layers(*far[:69], abi.PagedCacheView(1 << 32, 1 << 33, 1 << 34, (109 << 32) + (1 << 24), 4, 64)),
+                t=_layers(*[_cache((200 + i) << 32) for i in range(69)], far[69]), nl=70) == 1
+    assert copy(s=_layers(*far), t=_layers(*[_cache((200 + i) << 32) for i in range(70)]), nl=70, ws=None) == 5
+    assert copy(si=W + 64) == 1 and copy(ti=W + need - 4) == 1             # ids inside the workspace
     assert copy(d=48) == 2 and copy(kb=1) == 2
     assert copy(si=None) == 1 and copy(ti=ids + 2) == 3
     assert copy(ws=None) == 5 and copy(size=need - 1) == 5 and copy(ws=W + 8) == 3
