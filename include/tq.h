@@ -343,16 +343,19 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  *   ctx_lens: [B] int32, device, at most max_pages * page_size
  *   block_table: [B][max_pages] int32, device
  * d in {32, 64, 128, 256}, Hq / Hkv up to 128.  Both products run on the
- * tensor cores with fp16 operands and fp32 sums; norms up to 2^100.  Positions
- * past a row's range do not reach it, whatever their rows hold.
+ * tensor cores with fp16 operands and fp32 sums; norms up to 2^100, the largest
+ * V norms of a sequence's 128-position blocks within 2^120 of one another.
+ * Positions past a row's range do not reach it, whatever their rows hold.
  * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
  * rows are not written) and sets the device status word to 71.  A page id
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and
  * the device status word is set to 72.  73: a bounded wait gave up.
  * workspace: tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte
- * aligned like q, out and every array of the cache.
- * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (also max_pages * page_size
- * above 2^30), TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
+ * aligned like q, out and every array of the cache; calls that overlap on the
+ * GPU need one each.
+ * Errors: TQ_ERR_INVALID_ARG (also q, out and workspace not apart),
+ * TQ_ERR_UNSUPPORTED (also max_pages * page_size above 2^30, B above 2^20),
+ * TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
 tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
                                 tq_paged_cache cache, const int32_t *block_table, int max_pages,
                                 const int32_t *cu_q, const int32_t *ctx_lens, int window, int k_bits,
@@ -384,7 +387,8 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
  * outside [0, n_pages), a parent outside [-1, n_seqs), for the compaction also
  * a counted page without holder) changes nothing either; info is {0, -1} and
  * the device status word 61.
- * workspace: tq_pages_workspace_bytes(n_seqs, max_pages, n_pages) bytes.
+ * workspace: tq_pages_workspace_bytes(n_seqs, max_pages, n_pages) bytes; calls
+ * that overlap on the GPU need one each.
  * Where refs counts fewer holders than the rows have, the results are not
  * specified (no access leaves its array).
  * Alignment: 16 bytes for every cache array (norms too) and the workspace, 4

@@ -502,18 +502,24 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
     passed)."""
     n_q, Hq, d = q.shape
     B = ctx_lens.numel()
-    if d != plan.d or cache.k_packed.shape[-1] * 8 != d * cache.k_bits:
-        raise ValueError("q and cache must have the plan's head dimension")
+    rows = cache.k_norm.shape
+    if d != plan.d or len(rows) != 3 or cache.v_norm.shape != rows or \
+            cache.k_packed.shape != (*rows, d * cache.k_bits // 8) or \
+            cache.v_packed.shape != (*rows, d * cache.v_bits // 8):
+        raise ValueError("q and the cache's arrays must have the plan's head dimension and one geometry")
     if cu_q.numel() != B + 1 or block_table.shape[0] != B:
         raise ValueError("cu_q [B + 1], ctx_lens [B] and block_table [B, max_pages] expected")
     if not 0 <= window < 2 ** 31:
         raise ValueError("window must be in [0, 2^31)")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
+    if (cache.k_packed.dtype, cache.v_packed.dtype, cache.k_norm.dtype, cache.v_norm.dtype) != \
+            (torch.uint8, torch.uint8, torch.float32, torch.float32):
+        raise TypeError("packed rows must be uint8 and norms fp32")
     _cuda(q)
     dev = q.device
     _ints(dev, cu_q, block_table, ctx_lens)
-    _same_device(dev, cache.k_norm)
+    _same_device(dev, cache.k_packed, cache.k_norm, cache.v_packed, cache.v_norm)
     with _on(dev):
         if out is None:
             out = torch.zeros(n_q, Hq, d, dtype=out_dtype, device=dev)

@@ -1130,6 +1130,11 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
         return TQ_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < tq::prefill_paged_ws_bytes(P->d, tq::num_sms())) return TQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+    const uint64_t n_el = (uint64_t)n_q * Hq * P->d;
+    const Span rd = {reinterpret_cast<uintptr_t>(q), 2 * n_el};
+    const Span wr = {reinterpret_cast<uintptr_t>(out), n_el * (out_dtype == TQ_BF16 ? 2 : 4)};
+    const Span ws = {reinterpret_cast<uintptr_t>(workspace), tq::prefill_paged_ws_bytes(P->d, tq::num_sms())};
+    if (overlap(rd, wr) || overlap(rd, ws) || overlap(wr, ws)) return TQ_ERR_INVALID_ARG;
     if (!device_accessible(q) || !device_accessible(out) || !device_accessible(block_table) ||
         !device_accessible(cu_q) || !device_accessible(ctx_lens) || !device_accessible(workspace) ||
         !paged_accessible(cache))

@@ -206,3 +206,36 @@ def test_prefill_paged_refusals(L):
     assert call(q=A + 8) == 3 and call(out=A + 8) == 3
     assert call(cache=abi.PagedCacheView(1 << 32, (1 << 33) + 4, 1 << 34, 1 << 35, 4, 64)) == 3  # norms: 16 bytes
     assert call(ws=None) == 5 and call(size=need - 1) == 5 and call(ws=W + 8) == 3
+    # q, out and the workspace lie apart
+    assert call(out=A) == 1 and call(out=A + 10 * 8 * 128 * 2 - 16) == 1 and call(q=W + need - 16) == 1
+    assert call(out=W - 16, q=1 << 40) == 1 and call(out=W + 16, q=1 << 40) == 1
+
+
+def test_prefill_paged_python_refusals():
+    """Shapes and ranges that would not fit into the call are refused before it."""
+    import torch
+    plan = abi.Plan(128, 42)
+    q, i32 = torch.zeros(3, 4, 128, dtype=torch.bfloat16), lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    norm = lambda *s: torch.zeros(*s, dtype=torch.float32)  # noqa: E731
+    byte = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    good = abi.PagedCache(byte(4, 2, 32, 64), norm(4, 2, 32), byte(4, 2, 32, 48), norm(4, 2, 32), 4, 3)
+
+    def call(cache=good, window=0, q=q, cu=i32(3), table=i32(2, 4), ctx=i32(2)):
+        return abi.tq_attn_prefill_paged(plan, q, cu, cache, table, ctx, 0.1, window=window)
+
+    for bad in (abi.PagedCache(byte(4, 2, 32, 64), norm(4, 2, 32), byte(4, 2, 32, 64), norm(4, 2, 32), 4, 3),
+                abi.PagedCache(byte(4, 2, 32, 64), norm(4, 2, 32), byte(3, 2, 32, 48), norm(3, 2, 32), 4, 3),
+                abi.PagedCache(byte(4, 2, 32, 48), norm(4, 2, 32), byte(4, 2, 32, 48), norm(4, 2, 32), 4, 3),
+                abi.PagedCache(byte(4, 2, 32, 64), norm(4, 2, 32), byte(4, 2, 32, 48), norm(4, 2, 31), 4, 3)):
+        with pytest.raises(ValueError):
+            call(bad)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            call(window=window)
+    for kw in (dict(cu=i32(2)), dict(table=i32(3, 4)), dict(q=q[..., :64])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(TypeError):
+        call(q=q.float())
+    with pytest.raises(TypeError):
+        call(abi.PagedCache(good.k_packed, good.k_norm.half(), good.v_packed, good.v_norm, 4, 3))
