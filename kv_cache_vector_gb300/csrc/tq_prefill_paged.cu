@@ -109,9 +109,9 @@ struct PpGeo {
     static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [8] float2: 2^Ek, Ev
     static constexpr uint32_t kSegs = kMeta + 64;               // [kStages] segments staged
     static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
-    static constexpr uint32_t kRedBytes = 28 * 8;
+    static constexpr uint32_t kRedBytes = 2 * 8 * kWarps;
     static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
-    static constexpr uint32_t kJobs = kCur + 64;                // [2] jobs
+    static constexpr uint32_t kJobs = kCur + 80;                // [2] jobs
     static constexpr uint32_t kBar = kJobs + 2 * 48;
     static constexpr int kBars = 2 * kStages + 4 + 4 + 8 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars;  // tensor-memory base, abort flag
@@ -138,11 +138,14 @@ struct PpArgs {
 enum { kMetaHas = 0, kMetaLast, kMetaQ0, kMetaH, kMetaRow0, kMetaRows, kPpMeta = 8 };
 
 // Where a share starts or goes on: sequence, row tile, KV head, and the units
-// of the item that belong to earlier shares.
+// (or, where the share is one part of an item, the parts) of the item that
+// belong to earlier shares.
 struct PpCursor {
     int b, i, h;
     int64_t off;
     int64_t left;  // units of this share from here on
+    int n, ctx, q0;  // the sequence's lengths and first row of q
+    int parts;       // > 0: the share is part `off` of so many of one item
 };
 
 // Weights and ranges of sequence b's items.  A unit line position is only an
@@ -150,21 +153,26 @@ struct PpCursor {
 template <int D>
 struct PpSeq {
     using Z = PpGeo<D>;
-    int n, ctx, tiles, rows;
+    int n, ctx, q0, tiles = 0, rows;
     int64_t base, cap, kstar, over;
     int G;
 
     __device__ void load(const PpArgs& A, int b, int* status) {
-        G = A.Hq / A.Hkv;
-        const int64_t c0 = __ldcg(A.cu + b), c1 = __ldcg(A.cu + b + 1);
-        ctx = __ldcg(A.ctx + b);
-        if (c0 < 0 || c1 < c0 || c1 > A.n_q || ctx < 0 || ctx > ((int64_t)A.max_pages << A.shift) ||
-            (c1 - c0) * G > INT32_MAX) {
+        const int64_t c0 = A.cu[b], c1 = A.cu[b + 1];
+        const int len = A.ctx[b];
+        if (c0 < 0 || c1 < c0 || c1 > A.n_q || len < 0 || len > ((int64_t)A.max_pages << A.shift) ||
+            (c1 - c0) * (A.Hq / A.Hkv) > INT32_MAX) {
             if (status) report_timeout(status, kPpStatusRange);
-            n = ctx = 0;
+            set(A, 0, 0, 0);
         } else {
-            n = (int)(c1 - c0);
+            set(A, (int)(c1 - c0), len, (int)c0);
         }
+    }
+    __device__ void set(const PpArgs& A, int tokens, int len, int first) {
+        n = tokens;
+        ctx = len;
+        q0 = first;
+        G = A.Hq / A.Hkv;
         rows = n * G;
         tiles = (rows + Z::kRows - 1) / Z::kRows;
         base = ctx > n ? (int64_t)(ctx - n) * G : 0;
@@ -177,9 +185,10 @@ struct PpSeq {
     __device__ int factor(int i) const {
         return rows - (int64_t)i * Z::kRows > 128 ? Z::kCostPair : Z::kCostSplit;
     }
-    __device__ int64_t weight(int i) const {
-        int64_t e = base + min((int64_t)(i + 1) * Z::kRows, (int64_t)rows);
-        return factor(i) * min(e, cap) + over;
+    __device__ int64_t weight(int i) const { return work(i) + over; }
+    __device__ int64_t work(int i) const {  // without the item's own cost
+        const int64_t e = base + min((int64_t)(i + 1) * Z::kRows, (int64_t)rows);
+        return factor(i) * min(e, cap);
     }
     // sum of the weights of tiles 0 .. i - 1
     __device__ int64_t before(int i) const {
@@ -224,6 +233,16 @@ __device__ __forceinline__ int pp_blocks(const PpArgs& A, const PpSeq<D>& q, int
     return max(0, (end + Z::kN - 1) / Z::kN - lo);
 }
 
+// Rows and blocks of item p.b, p.i, p.h.
+template <int D>
+__device__ __forceinline__ void pp_rows(const PpArgs& A, const PpSeq<D>& q, PpPart& p) {
+    using Z = PpGeo<D>;
+    p.row0 = p.i * Z::kRows;
+    p.rows = min(Z::kRows, q.rows - p.row0);
+    p.pair = Z::kStreams == 2 && p.rows > 128;
+    p.nblk = pp_blocks<D>(A, q, p.i, &p.lo_blk, &p.kv_end);
+}
+
 // The share's next part with work in it; advances the cursor.  False at the
 // end of the share.  Items without blocks (no position to attend to) come as
 // a whole part with blk0 == blk1, to the share that holds their start.
@@ -245,10 +264,7 @@ __device__ bool pp_next(const PpArgs& A, PpCursor& c, PpSeq<D>& q, PpPart& p) {
         p.b = c.b;
         p.i = c.i;
         p.h = c.h;
-        p.row0 = c.i * Z::kRows;
-        p.rows = min(Z::kRows, q.rows - p.row0);
-        p.pair = Z::kStreams == 2 && p.rows > 128;
-        p.nblk = pp_blocks<D>(A, q, c.i, &p.lo_blk, &p.kv_end);
+        pp_rows<D>(A, q, p);
         p.blk0 = pp_cut(p.nblk, c.off, w);
         p.blk1 = pp_cut(p.nblk, end, w);
         p.head = c.off == 0;
@@ -277,12 +293,14 @@ struct PpJob {
     int blk;       // first block
     int kv_end;    // positions at or past it are not read
     int pos0;      // position of the sequence's token 0
-    int pad[3];
+    int tok0, rest;  // row0 / G and row0 % G
+    int pad;
 };
 enum { kJobPair = 1, kJobWhole = 2, kJobHead = 4 };
 
-__device__ __forceinline__ uint32_t pp_chunk(uint32_t half_bytes, int row, int k8) {
-    return (uint32_t)(k8 >> 3) * half_bytes + (uint32_t)row * 128 + (((k8 & 7) ^ (row & 7)) << 4);
+// Chunk c (8 dims, 16 bytes) of row r of a query tile.
+__device__ __forceinline__ unsigned char* pp_place(unsigned char* tile, int r, int c) {
+    return tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 __device__ __forceinline__ float pp_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -621,7 +639,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     volatile int* abort_f = reinterpret_cast<volatile int*>(sm + Z::kMisc + 4);
     uint32_t* slot = reinterpret_cast<uint32_t*>(sm + Z::kMisc);
     PpCursor* start = reinterpret_cast<PpCursor*>(sm + Z::kCur);
-    long long* share = reinterpret_cast<long long*>(sm + Z::kCur + 48);  // units of a share
+    long long* share = reinterpret_cast<long long*>(sm + Z::kCur + 64);  // units of a share
     long long* red = reinterpret_cast<long long*>(sm + Z::kRed);
 
     if (sa & 1023u) {  // the tiles' swizzle needs it; the whole grid leaves, with nothing to join
@@ -657,6 +675,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         *abort_f = 0;
         mbar_fence_init();
         start->left = 0;
+        start->parts = 0;
     }
     if (warp == SW + DW) tmem_alloc<512>(slot);
 
@@ -667,11 +686,15 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     {
         const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
         const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
+        PpSeq<D> q;
         long long mine = 0;
+        int items = 0;
+        float most = 0.f;  // the largest item's work
         for (int b = b0; b < b1; ++b) {
-            PpSeq<D> q;
             q.load(A, b, blockIdx.x == 0 ? status : nullptr);
             mine += (long long)A.Hkv * q.before(q.tiles);
+            if (q.tiles) most = fmaxf(most, fmaxf((float)q.work(q.tiles - 1), (float)q.work(max(0, q.tiles - 2))));
+            items += (int)min((int64_t)1 << 10, (int64_t)A.Hkv * q.tiles);  // exact where it counts: below the CTAs
         }
         long long incl = mine;
 #pragma unroll
@@ -680,28 +703,80 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             if (lane >= o) incl += u;
         }
         if (lane == 31) red[warp] = incl;
+        uint32_t* red2 = reinterpret_cast<uint32_t*>(red + Z::kWarps);
+        const uint32_t wi = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)items);
+        const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+        if (lane == 0) red2[2 * warp] = wi, red2[2 * warp + 1] = wm;
         __syncthreads();
         long long total = 0, before = 0;
+        uint32_t all = 0, top = 0;
 #pragma unroll
         for (int w = 0; w < Z::kWarps; ++w) {
             if (w < warp) before += red[w];
             total += red[w];
+            all += red2[2 * w];
+            top = max(top, red2[2 * w + 1]);
         }
         before += incl - mine;
+        const float sum = (float)total, grid = (float)gridDim.x;
         // a little over total / grid: the last CTA's share may be smaller
-        const long long per = (long long)((float)total * (1.000001f / (float)gridDim.x)) + 1;
-        const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+        const long long per = (long long)(sum * (1.000001f / grid)) + 1;
         if (tid == 0) *share = per;
+        // Shares along the line of all items cross from one item into the next, and
+        // then pay for two items' rotations and outputs.  With few items a share is
+        // a part of one item instead: an item gets (work / cut) + 1 shares, no more
+        // than there are CTAs in all.  Taken where the largest of them is no more
+        // than a share of the line: the drafts of 4 sequences over 400-2000
+        // positions took 24.7 us along the line, 20.8 us so.
+        float cut = 0.f;
+        if (each == 1 && all > 0 && all < gridDim.x) {
+            const float over = (float)Z::kCostItem * Z::kN * (A.Hq / A.Hkv);
+            const float c = fmaxf(1.f, __fdividef((sum - (float)all * over) * 1.000002f, grid - (float)all));
+            if (fminf(c, __uint_as_float(top)) * grid <= sum) cut = c;
+        }
+        if (cut > 0.f) {
+            auto parts = [&](int i) { return (int)__fdividef((float)q.work(i), cut) + 1; };
+            int sums = 0;
+            for (int i = 0; i < q.tiles; ++i) sums += A.Hkv * parts(i);
+            int ins = sums;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, ins, o);
+                if (lane >= o) ins += u;
+            }
+            __syncthreads();  // red2 is free
+            if (lane == 31) red2[warp] = ins;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) ins += red2[w];
+            int v = (int)blockIdx.x - (ins - sums);
+            if (v >= 0 && v < sums) {  // this thread's sequence holds this CTA's share
+                int i = 0, n;
+                for (;; ++i) {
+                    n = parts(i);
+                    if (v < A.Hkv * n) break;
+                    v -= A.Hkv * n;
+                }
+                start->b = b0;
+                start->i = i;
+                start->h = v / n;
+                start->off = v % n;
+                start->parts = n;
+                start->n = q.n;
+                start->ctx = q.ctx;
+                start->q0 = q.q0;
+            }
+        } else {
+        const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
         if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
             long long v = u0 - before;
-            PpSeq<D> q;
             int b = b0;
-            for (;; ++b) {
-                q.load(A, b, nullptr);
-                const long long w = (long long)A.Hkv * q.before(q.tiles);
-                if (v < w) break;
-                v -= w;
-            }
+            if (each > 1)
+                for (;; ++b) {
+                    q.load(A, b, nullptr);
+                    const long long w = (long long)A.Hkv * q.before(q.tiles);
+                    if (v < w) break;
+                    v -= w;
+                }
             int lo = 0, hi = q.tiles - 1;  // the last tile whose units start at or before v
             while (lo < hi) {
                 const int m = (lo + hi + 1) / 2;
@@ -718,6 +793,10 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             start->h = h;
             start->off = v - (long long)h * w;
             start->left = u1 - u0;
+            start->n = q.n;
+            start->ctx = q.ctx;
+            start->q0 = q.q0;
+        }
         }
     }
     tc_fence_before();
@@ -740,6 +819,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         p.blk = m->blk;
         p.kv_end = m->kv_end;
         p.pos0 = m->pos0;
+        p.tok0 = m->tok0;
+        p.rest = m->rest;
         __syncwarp();
         if (lane == 0) mbar_arrive(&job_free[job & 1]);
         ++job;
@@ -758,13 +839,24 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         const uint32_t at = a == 0 ? 0u : a == 1 ? N * D / 2 : a == 2 ? N * D : N * D + 4 * N;
         PpCursor cur = *start;
         PpSeq<D> seq;
-        if (cur.left > 0) seq.load(A, cur.b, nullptr);
+        if (cur.left > 0 || cur.parts > 0) seq.set(A, cur.n, cur.ctx, cur.q0);
         uint32_t tc = 0;
         int has = 0;  // parts left in the workspace
         bool ok = true;
         for (; ok; ++job) {
             PpPart u;
-            const bool more = pp_next<D>(A, cur, seq, u);
+            bool more;
+            if (cur.parts > 0) {  // the one part of this share
+                u.b = cur.b, u.i = cur.i, u.h = cur.h;
+                pp_rows<D>(A, seq, u);
+                u.blk0 = (int)((int64_t)u.nblk * cur.off / cur.parts);
+                u.blk1 = (int)((int64_t)u.nblk * (cur.off + 1) / cur.parts);
+                u.head = cur.off == 0;
+                u.whole = u.nblk == 0 ? u.head : (u.blk0 == 0 && u.blk1 == u.nblk);
+                more = job == 0 && (u.whole || u.blk1 > u.blk0);
+            } else {
+                more = pp_next<D>(A, cur, seq, u);
+            }
             if (job >= 2) ok = pp_wait(&job_free[job & 1], ((job >> 1) - 1) & 1, abort_f, status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
@@ -773,13 +865,16 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 m->nb = more ? u.blk1 - u.blk0 : -1;
                 if (more) {
                     m->flags = (u.pair ? kJobPair : 0) | (u.whole ? kJobWhole : 0) | (u.head ? kJobHead : 0);
-                    m->q0 = __ldcg(A.cu + u.b);
+                    m->q0 = seq.q0;
                     m->h = u.h;
                     m->row0 = u.row0;
                     m->rows = u.rows;
                     m->blk = u.lo_blk + u.blk0;
                     m->kv_end = u.kv_end;
                     m->pos0 = seq.ctx - seq.n;
+                    const int tok0 = u.row0 / seq.G;
+                    m->tok0 = tok0;
+                    m->rest = u.row0 - tok0 * seq.G;
                 }
                 mbar_arrive(&job_full[job & 1]);
             }
@@ -790,7 +885,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             auto page_of = [&](int j) {
                 const int pos = (u.lo_blk + j) * N + s * seg;
                 return s < nseg && j < u.blk1 && pos < u.kv_end
-                           ? __ldcg(A.bt + (int64_t)u.b * A.max_pages + (pos >> A.shift))
+                           ? A.bt[(int64_t)u.b * A.max_pages + (pos >> A.shift)]
                            : INT_MIN;
             };
             int next_page = page_of(u.blk0);
@@ -825,21 +920,27 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         // in this share and ends in a later one
         if (lane == 0) {
             int last = blockIdx.x;
-            bool owner = ok && cur.off > 0 &&
-                         !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
-            if (owner) {
-                const int64_t w = seq.weight(cur.i), per = *share;
-                const int nblk = pp_blocks<D>(A, seq, cur.i);
-                // no join where one share has all of the item's blocks
-                owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
-                for (int64_t x = cur.off; x < w; x += per) {
-                    ++last;
-                    if (pp_cut(nblk, x, w) == 0 && pp_cut(nblk, min(w, x + per), w) == nblk) owner = false;
+            bool owner;
+            if (cur.parts > 0) {
+                // (an item of one block is some share's whole)
+                owner = ok && cur.off == 0 && cur.parts > 1 && pp_blocks<D>(A, seq, cur.i) > 1;
+                last += cur.parts - 1;
+            } else {
+                owner = ok && cur.off > 0 &&
+                        !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
+                if (owner) {
+                    const int64_t w = seq.weight(cur.i), per = *share;
+                    const int nblk = pp_blocks<D>(A, seq, cur.i);
+                    // no join where one share has all of the item's blocks
+                    owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
+                    for (int64_t x = cur.off; x < w && pp_cut(nblk, x, w) == 0; x += per)
+                        if (pp_cut(nblk, min(w, x + per), w) == nblk) owner = false;
+                    last += (int)((w - cur.off + per - 1) / per);
                 }
             }
             const int row0 = cur.i * Z::kRows;
             int4* m = reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta);
-            m[0] = make_int4(has, owner ? last : -1, owner ? __ldcg(A.cu + cur.b) : 0, cur.h);
+            m[0] = make_int4(has, owner ? last : -1, owner ? seq.q0 : 0, cur.h);
             m[1] = make_int4(row0, owner ? min(Z::kRows, seq.rows - row0) : 0, 0, 0);
         }
         // the copies issued have landed before the CTA leaves (bounded)
@@ -1037,6 +1138,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t t_out = t_lane + Z::kTmemO + 128 * g;
         const int G = A.Hq / A.Hkv;
+        const uint32_t invG = (65536u + G - 1) / G;  // x / G = x invG >> 16 for x < 384, G <= 128
         const float q_sign = P.q_mul > 0.f ? 1.f : (P.q_mul < 0.f ? -1.f : 0.f);
         const float q_abs = P.q_mul == 0.f ? 1.f : fabsf(P.q_mul);
         uint32_t ns[2] = {0, 0}, npv[2] = {0, 0}, tc0 = 0, met = 0;
@@ -1050,30 +1152,56 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             __syncwarp();
             tc_fence_after();
         };
-        while (next_job()) {
+        // This warp's 32 rows of the next item's queries, into their places of the
+        // tile (all products with the item's before are done): asynchronous copies
+        // of 16 bytes a lane.
+        auto fetch = [&]() {
+            const bool ok = pp_wait(&job_full[job & 1], (job >> 1) & 1, abort_f, status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const volatile PpJob* m = reinterpret_cast<const volatile PpJob*>(sm + Z::kJobs) + (job & 1);
+            const bool pair = m->flags & kJobPair;
+            if (m->nb <= 0 || (g && !pair)) return;
+            const int lrow = r + (pair ? 128 * g : 0), left = m->rows - (pair ? 128 * g : 0) - 32 * (warp & 3);
+            if (left <= 0) return;
+            const int x = m->rest + lrow, tok = x * invG >> 16;  // from the item's first token on
+            const int rel = tok * A.Hq + x - tok * G;
+            const __nv_bfloat16* src = A.q + (((int64_t)m->q0 + m->tok0) * A.Hq + (int64_t)m->h * G) * D + 8 * (lane % (D / 8));
+            unsigned char* qt = sm + Z::kQ + (pair ? g * Z::kQTile : 0) + 4096 * (warp & 3);
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                const int rr = (32 * i + lane) / (D / 8);
+                const int at = __shfl_sync(0xFFFFFFFFu, rel, rr);
+                const bool in = rr < left;
+                cp_async16(smem_addr(pp_place(qt, rr, lane % (D / 8))), src + (int64_t)(in ? at : 0) * D, in ? 16 : 0);
+            }
+            cp_async_commit();
+        };
+        for (;;) {
+            fetch();
+            if (!next_job()) break;
             const int nb = p.nb;
             const bool pair = p.flags & kJobPair, split = Z::kStreams == 2 && !pair;
             // the row of this thread: in split mode both streams have row r
             const int lrow = pair ? 128 * g + r : r;
             const bool rvalid = lrow < p.rows;
-            const int tok = rvalid ? (p.row0 + lrow) / G : 0, hd = rvalid ? p.row0 + lrow - tok * G : 0;
+            const int x = rvalid ? p.rest + lrow : 0, dt = x * invG >> 16;
+            const int tok = p.tok0 + dt, hd = x - dt * G;
             const int64_t qrow = ((int64_t)p.q0 + tok) * A.Hq + (int64_t)p.h * G + hd;
             const int pos = rvalid ? p.pos0 + tok : -1;
             // a warp without rows only keeps the barriers' count
             const bool rows_here = __any_sync(0xFFFFFFFFu, rvalid);
             const int lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
-            // ---- queries: rotated in registers and tensor memory (the output
-            // columns, free until the item's first product), 64 dims at a time,
-            // and rounded to fp16 under a power of two per row
+            // ---- queries: each thread rotates its row in registers and tensor
+            // memory (the output columns, free until the item's first product), 64
+            // dims at a time, and rounds it to fp16 under a power of two.  A warp
+            // without rows leaves its part of the tile as it is: those rows' scores
+            // go nowhere.
             float cq = q_abs;
-            if (nb > 0 && (pair || g == 0)) {
+            if (nb > 0 && (pair || g == 0) && rows_here) {
                 float amax = 0.f;
-                const __nv_bfloat16* src = A.q + qrow * D;
-                if (rvalid) {  // the later pieces' lines are on their way during the first one's work
-#pragma unroll
-                    for (int h = 1; h < PARTS; ++h)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64 * h));
-                }
+                unsigned char* qt = sm + Z::kQ + (pair ? g * Z::kQTile : 0) + 4096 * (warp & 3);
+                cp_async_wait_all();
+                __syncwarp();
 #pragma unroll 1
                 for (int h = 0; h < PARTS; ++h) {
                     float y[E];
@@ -1081,8 +1209,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                         uint32_t u[E / 2];
 #pragma unroll
                         for (int k = 0; k < E / 8; ++k) {
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (rvalid) v = reinterpret_cast<const uint4*>(src + 64 * h)[k];
+                            const uint4 v = *reinterpret_cast<const uint4*>(pp_place(qt, lane, 8 * h + k));
                             u[4 * k] = v.x, u[4 * k + 1] = v.y, u[4 * k + 2] = v.z, u[4 * k + 3] = v.w;
                         }
 #pragma unroll
@@ -1106,7 +1233,6 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 }
                 cq = q_abs * pp_pow2(e);
                 const float inv = q_sign * pp_pow2(-e);
-                unsigned char* qt = sm + Z::kQ + (pair ? g * Z::kQTile : 0) + r * 128;
 #pragma unroll 1
                 for (int c = 0; c < E / 16; ++c) {
                     uint32_t y[PARTS][16];
@@ -1126,15 +1252,14 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                             for (int k = 0; k < 8; ++k)
                                 w[k] ^= ((flip << (15 - 2 * k)) & 0x8000u) | ((flip << (30 - 2 * k)) & 0x80000000u);
                         }
-                        unsigned char* qh = qt + h * 16384;
-                        *reinterpret_cast<uint4*>(qh + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(qh + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        *reinterpret_cast<uint4*>(pp_place(qt, lane, 8 * h + 2 * c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(pp_place(qt, lane, 8 * h + 2 * c + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
                 if constexpr (D < 64) {
 #pragma unroll
                     for (int k8 = D / 8; k8 < 8; ++k8)
-                        *reinterpret_cast<uint4*>(qt + ((k8 ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(pp_place(qt, lane, k8)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
@@ -1357,6 +1482,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             }
             tc0 += nb;
         }
+        cp_async_wait_all();
     }
     griddep_launch();
     tc_fence_before();
@@ -1375,6 +1501,7 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
     using Z = PpGeo<D>;
     constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
     __shared__ float tile[32][D + 1];
+    griddep_launch();
     griddep_wait();
     const int sh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int4* meta = reinterpret_cast<const int4*>(A.meta);
@@ -1530,7 +1657,10 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     }
     e = launch_pdl(k_prefill_paged<D>, dim3(shares), dim3(Z::kThreads), Z::kSmem, s, A, P, status_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_prefill_paged_join<D>, dim3(shares, Z::kRows / 32), dim3(256), 0, s, A, P);
+    // groups of 32 rows that an item can have
+    const int64_t rows = c.n_q * (c.Hq / c.Hkv);
+    const unsigned groups = (unsigned)((rows < Z::kRows ? rows : Z::kRows) + 31) / 32;
+    return launch_pdl(k_prefill_paged_join<D>, dim3(shares, groups), dim3(256), 0, s, A, P);
 }
 
 template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, cudaStream_t);

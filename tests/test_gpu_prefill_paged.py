@@ -197,6 +197,21 @@ def test_more_sequences_than_threads():
     run_both(Batch(3, lens, 2, 1, 64, 32, 3, 4), 0.125)
 
 
+@pytest.mark.parametrize("lens", [
+    [(1, 5000)],                                    # one item over all CTAs
+    [(1, 100), (1, 3000), (1, 90), (1, 129)],       # unequal items: few shares and many
+    [(200, 700), (1, 4000), (70, 70)],              # several tiles, paired and split
+    [(4, 1), (2, 0), (1, 128), (0, 500)],           # items of one block and of none
+    [(1, 900)] * 18,                                # nearly an item per CTA
+    [(1, 2000)] * 19 + [(1, 40)] * 19,              # as many items as CTAs, and more
+    [(0, 0)] * 700 + [(3, 1000), (1, 1)],           # empty sequences before a few items
+])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_few_items(lens, d):
+    """Shares that are parts of one item each, and the sizes about which that ends."""
+    run_both(Batch(16, lens, 16, 8 if len(lens) < 100 else 2, d, 64, 4, 3), 1 / math.sqrt(d))
+
+
 @pytest.mark.parametrize("flags", [1, 2, 3])
 @pytest.mark.parametrize("d", [32, 128, 256])
 def test_plan_variants(d, flags):
