@@ -531,7 +531,7 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
         _check("tq_attn_prefill_paged", lib().tq_attn_prefill_paged(
             plan.handle, q.data_ptr(), n_q, B, Hq, cache.Hkv, cache.view(), block_table.data_ptr(),
             block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), window, cache.k_bits, cache.v_bits,
-            scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev)))
+            scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
     return out
 
 
@@ -570,10 +570,14 @@ class PagedLayers:
 
 @dataclass
 class PageTable:
-    """The books of a paged cache's pages (caller-owned device tensors, int32)."""
+    """The books of a paged cache's pages (caller-owned device tensors, int32),
+    and what the last call that wrote them said, unless it was given a tensor
+    for that (made at the first such call)."""
     block_table: torch.Tensor  # [n_seqs, max_pages]: page ids, -1 past a row's pages
     lens: torch.Tensor         # [n_seqs]: positions in use
     refs: torch.Tensor         # [n_pages]: holders of a page, 0 for a free one
+    info: torch.Tensor | None = None      # [2]
+    moved_to: torch.Tensor | None = None  # [n_pages], by tq_pages_compact
 
     @staticmethod
     def empty(n_seqs, max_pages, n_pages, device="cuda"):
@@ -589,10 +593,13 @@ class PageTable:
         return PageTableView(b.data_ptr(), n.data_ptr(), r.data_ptr())
 
 
+_INT32 = torch.int32
+
+
 def _ints(device, *ts):
     """Contiguous int32 CUDA tensors on `device`."""
     for t in ts:
-        if t.dtype != torch.int32:
+        if t.dtype is not _INT32:
             raise TypeError("expected int32 tensors")
         if t.device != device or not t.is_contiguous():
             raise ValueError("expected contiguous CUDA tensors on one device")
@@ -609,9 +616,12 @@ def _same_device(device, *ts):
             raise ValueError("all tensors must be on one device")
 
 
+_STAY = nullcontext()
+
+
 def _on(device):
     """The device made current for a call, where it is not."""
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else nullcontext()
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else _STAY
 
 
 def _layers(x) -> PagedLayers:
@@ -649,7 +659,7 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
         ws = _scratch(workspace, dst.device, tq_pages_workspace_bytes, 0, 0, dst.n_pages)
         _check("tq_pages_copy", lib().tq_pages_copy(
             src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(),
-            src_ids.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dst.device)))
+            src_ids.numel(), ws.data_ptr(), ws.nbytes, _raw_stream(dst.device)))
 
 
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
@@ -663,7 +673,13 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         if out is None:
             out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
         if info is None:
-            info = table.lens.new_empty(2)
+            if out.info is None:
+                out.info = out.lens.new_empty(2)
+            info = out.info
+        if arg is None and moved is None:
+            if out.moved_to is None:
+                out.moved_to = out.refs.new_empty(layers.n_pages)
+            moved = out.moved_to
         other = moved if arg is None else arg
         _ints(dev, info, other)
         if info.numel() != 2 or other.numel() != (layers.n_pages if arg is None else n_seqs):
@@ -672,16 +688,16 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         ws = _scratch(workspace, dev, tq_pages_workspace_bytes, n_seqs, max_pages, layers.n_pages)
         middle = (a, b, other.data_ptr()) if arg is None else (a, other.data_ptr(), b)
         _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,
-                                      info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                      _raw_stream(dev)))
-    return out, info
+                                      info.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
+    return (out, info) if arg is not None else (out, moved, info)
 
 
 def tq_pages_fork(table: PageTable, parents: torch.Tensor, layers, out: PageTable | None = None,
                   info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Row i of the result is row parents[i] of `table` (int32; -1: empty):
     full pages shared, a partly filled last page copied for all children but
-    one.  Returns (table, info [2]: pages taken, pages missing)."""
+    one.  Returns (table, info [2]: pages taken, pages missing); without
+    `info`, the table's own, which the next call on it writes again."""
     return _pages("tq_pages_fork", table, parents, layers, out, None, info, workspace)
 
 
@@ -690,7 +706,8 @@ def tq_pages_resize(table: PageTable, new_lens: torch.Tensor, layers, out: PageT
     """Row i gets the length new_lens[i] (int32; negative: unchanged): pages
     past it are given back, missing ones taken, and a shared last page that
     the row goes on in replaced by a private copy.  `out` may be `table`.
-    Returns (table, info [2]: pages taken, pages missing)."""
+    Returns (table, info [2]: pages taken, pages missing), info as of
+    tq_pages_fork."""
     return _pages("tq_pages_resize", table, new_lens, layers, out, None, info, workspace)
 
 
@@ -698,12 +715,9 @@ def tq_pages_compact(table: PageTable, layers, out: PageTable | None = None, mov
                      info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The held pages moved to the lowest ids.  `out` may be `table`.  Returns
     (table, moved_to [n_pages]: each page's new id or -1, info [2]: pages
-    held, pages moved)."""
-    layers = _layers(layers)
-    if moved_to is None:
-        moved_to = torch.empty(layers.n_pages, dtype=torch.int32, device=layers.device)
-    out, info = _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
-    return out, moved_to, info
+    held, pages moved); without moved_to and info, the table's own, as of
+    tq_pages_fork."""
+    return _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
 
 
 def tq_device_status(reset: bool = False) -> int:

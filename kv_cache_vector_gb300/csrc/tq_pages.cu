@@ -15,12 +15,11 @@
 //     between them (hardware barriers: nothing spins).
 //   k_pages_copy   copies the pairs' pages, in every layer, 32 KB per CTA and
 //     step.  Bound by memory: a copied page is read once and written once.
-//     473 pages of 2 MB (32 layers): 295 us, 6.7 TB/s, against 6.8 TB/s of one
-//     contiguous copy; with 4, 8 and 16 KB steps 413, 322 and 304 us (too few
-//     bytes in flight).
+//     473 pages of 2 MB (32 layers): 293 us, 6.35 TB/s; with 4, 8 and 16 KB
+//     steps 413, 322 and 304 us (too few bytes in flight).
 // The copy is launched with programmatic stream serialization, so its CTAs are
 // resident when the plan ends.  Small calls are bound by the launches and the
-// plan's chain of dependent reads: 6 us for a copy of 5 pages, 10 to 20 us for
+// plan's chain of dependent reads: 4 us for a copy of 5 pages, 10 to 20 us for
 // a fork, resize or compaction without pages to copy (8 to 512 rows, 100 to
 // 6500 pages).
 #include <climits>
@@ -533,6 +532,39 @@ struct CopySizes {
     uint32_t n[4];
 };
 
+// A run of 32 KB of a page pair in one layer: the page's four arrays taken as
+// one run of words, from word w0 on (each thread's first).
+template <int MAX>
+__device__ __forceinline__ void copy_step(const CopyLayers<MAX>& P, const CopySizes& Z, int l, int64_t s, int64_t t,
+                                          uint32_t w0, uint32_t words) {
+    uint4 v[kPcUnroll];
+    uint4* to[kPcUnroll];
+#pragma unroll
+    for (int k = 0; k < kPcUnroll; ++k) {
+        uint32_t w = w0 + k * kPcThreads;
+        to[k] = nullptr;
+        if (w >= words) continue;
+        int a = 0;
+        if (w >= Z.n[0]) {
+            w -= Z.n[0];
+            a = 1;
+            if (w >= Z.n[1]) {
+                w -= Z.n[1];
+                a = 2;
+                if (w >= Z.n[2]) {
+                    w -= Z.n[2];
+                    a = 3;
+                }
+            }
+        }
+        to[k] = P.dst[l][a] + t * Z.n[a] + w;
+        v[k] = __ldcg(P.src[l][a] + s * Z.n[a] + w);
+    }
+#pragma unroll
+    for (int k = 0; k < kPcUnroll; ++k)
+        if (to[k]) __stcg(to[k], v[k]);
+}
+
 // Step u of the copy: words [u % steps * kPcChunk, ..) of page pair u / steps
 // / L in layer u / steps % L, the page's four arrays taken as one run of
 // words.
@@ -554,38 +586,57 @@ k_pages_copy(const __grid_constant__ CopyLayers<MAX> P, const CopySizes Z, int L
         const int l = (int)(pl - pair * L);
         const int64_t s = __ldcg(src + pair), t = __ldcg(dst + pair);
         if (s < 0) continue;
-        uint4 v[kPcUnroll];
-        uint4* to[kPcUnroll];
-#pragma unroll
-        for (int k = 0; k < kPcUnroll; ++k) {
-            uint32_t w = w0 + k * kPcThreads;
-            to[k] = nullptr;
-            if (w >= words) continue;
-            int a = 0;
-            if (w >= Z.n[0]) {
-                w -= Z.n[0];
-                a = 1;
-                if (w >= Z.n[1]) {
-                    w -= Z.n[1];
-                    a = 2;
-                    if (w >= Z.n[2]) {
-                        w -= Z.n[2];
-                        a = 3;
-                    }
-                }
-            }
-            to[k] = P.dst[l][a] + t * Z.n[a] + w;
-            v[k] = __ldcg(P.src[l][a] + s * Z.n[a] + w);
+        copy_step(P, Z, l, s, t, w0, words);
+    }
+}
+
+// tq_pages_copy with few pairs: every CTA looks all of them over for itself
+// (in n^2 / 256 comparisons a thread), so that there is no plan to wait for.
+// 5 pages of 2 layers: 6.6 us with the plan, 3.9 us so.
+constexpr int kPcFew = 128;
+
+template <int MAX>
+__global__ void __launch_bounds__(kPcThreads, kPcPerSm)
+k_pages_copy_few(const __grid_constant__ CopyLayers<MAX> P, const CopySizes Z, int L, const int32_t* src,
+                 const int32_t* dst, int n, int n_src, int n_dst, int same, int* status) {
+    __shared__ int s_src[kPcFew], s_dst[kPcFew];
+    __shared__ int s_skip[kPcFew];
+    griddep_wait();
+    const int tid = threadIdx.x;
+    if (tid < n) {
+        int s = __ldcg(src + tid), t = __ldcg(dst + tid);
+        if (s < 0 || t < 0) s = t = -1;
+        if (s >= n_src || t >= n_dst) {
+            if (blockIdx.x == 0) report_timeout(status, kPgStatusInput);
+            s = t = -1;
         }
-#pragma unroll
-        for (int k = 0; k < kPcUnroll; ++k)
-            if (to[k]) __stcg(to[k], v[k]);
+        s_src[tid] = s;
+        s_dst[tid] = t;
+        s_skip[tid] = s < 0;
+    }
+    __syncthreads();
+    // pair i is skipped if an earlier pair has its destination, or within one
+    // pool any pair has it as a source
+    for (int x = tid; x < n * n; x += kPcThreads) {
+        const int i = x / n, j = x - i * n, t = s_dst[i];
+        if (t >= 0 && ((j < i && s_dst[j] == t) || (same && s_src[j] == t))) s_skip[i] = 2;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid < n && s_skip[tid] == 2) report_timeout(status, kPgStatusConflict);
+    const uint32_t words = Z.n[0] + Z.n[1] + Z.n[2] + Z.n[3];
+    const uint32_t steps = (words + kPcChunk - 1) / kPcChunk;
+    const int64_t units = (int64_t)n * L * steps;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t pl = u / steps;
+        const uint32_t w0 = (uint32_t)(u - pl * steps) * kPcChunk + tid;
+        const int pair = (int)(pl / L), l = (int)(pl - (int64_t)pair * L);
+        if (!s_skip[pair]) copy_step(P, Z, l, s_src[pair], s_dst[pair], w0, words);
     }
 }
 
 template <int MAX>
 static cudaError_t launch_copy(const PagesCall& c, int l0, int L, const CopySizes& Z, const PagesWs& W, int64_t grid,
-                               cudaStream_t s) {
+                               bool few, cudaStream_t s) {
     CopyLayers<MAX> P;
     for (int l = 0; l < L; ++l) {
         const tq_paged_cache &f = c.src[l0 + l], &t = c.dst[l0 + l];
@@ -598,6 +649,9 @@ static cudaError_t launch_copy(const PagesCall& c, int l0, int L, const CopySize
         P.dst[l][2] = reinterpret_cast<uint4*>(t.v_packed);
         P.dst[l][3] = reinterpret_cast<uint4*>(t.v_norm);
     }
+    if (few)
+        return launch_pdl(k_pages_copy_few<MAX>, dim3((unsigned)grid), dim3(kPcThreads), 0, s, P, Z, L, c.arg, c.arg2,
+                          (int)c.n, (int)c.src[0].n_pages, (int)c.dst[0].n_pages, c.same, status_word());
     return launch_pdl(k_pages_copy<MAX>, dim3((unsigned)grid), dim3(kPcThreads), 0, s, P, Z, L,
                       (const int32_t*)W.head, (const int32_t*)W.src, (const int32_t*)W.dst);
 }
@@ -654,9 +708,12 @@ cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s) {
     A.n_src = (int)c.src[0].n_pages;
     A.shift = c.page_shift;
     A.same = c.same;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
+    const bool few = op == kPagesCopy && c.n <= kPcFew;
     switch (op) {
-        case kPagesCopy: e = launch_plan<kOpCopy>(A, s); break;
+        case kPagesCopy:
+            if (!few) e = launch_plan<kOpCopy>(A, s);
+            break;
         case kPagesFork: e = launch_plan<kOpFork>(A, s); break;
         case kPagesResize: e = launch_plan<kOpResize>(A, s); break;
         default: e = launch_plan<kOpCompact>(A, s); break;
@@ -677,7 +734,7 @@ cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s) {
         const int64_t cap = (int64_t)num_sms() * kPcPerSm;
         int64_t grid = most * L * steps;
         grid = grid < 1 ? 1 : (grid > cap ? cap : grid);
-        e = L <= 4 ? launch_copy<4>(c, l0, L, Z, W, grid, s) : launch_copy<kPcLayers>(c, l0, L, Z, W, grid, s);
+        e = L <= 4 ? launch_copy<4>(c, l0, L, Z, W, grid, few, s) : launch_copy<kPcLayers>(c, l0, L, Z, W, grid, few, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -254,6 +254,46 @@ def test_copy_conflicts_are_refused_by_pair(s, t, same, status):
     check_contents(dst, before, OP.copy_pairs(s, t, 12, 12, same), before_dst)
 
 
+@pytest.mark.parametrize("same", [True, False])
+@pytest.mark.parametrize("n", [2, 31, 127, 128, 129, 200, 3000])
+def test_copy_of_random_pairs(n, same):
+    """Ids out of range, skipped pairs, destinations given twice and destinations that are
+    sources, with as many pairs as one kernel looks over by itself and with more."""
+    rng = np.random.default_rng(n)
+    N = max(40, n + 3)
+    src = make_pool(12, N, L=3, Hkv=1)
+    dst = src if same else make_pool(13, N + 2, L=3, Hkv=1)
+    s = rng.integers(0, N, n).astype(np.int32)
+    t = rng.integers(0, dst.n_pages, n).astype(np.int32)
+    s[rng.random(n) < 0.1], t[rng.random(n) < 0.1] = -3, -1
+    s[0] = N                                   # past the pool
+    before, before_dst = contents(src), contents(dst)
+    want = OP.copy_pairs(s, t, N, dst.n_pages, same)
+    assert n < 20 or 0 < len(want) < n
+    abi.tq_pages_copy(src, dst, torch.from_numpy(s).cuda(), torch.from_numpy(t).cuda())
+    assert abi.tq_device_status(reset=True) in (61, 62)
+    check_contents(dst, before, want, before_dst)
+
+
+def test_what_a_call_says_stays_with_the_table_it_wrote():
+    page, N = 32, 12
+    pool = make_pool(14, N)
+    t = on_gpu(np.full((2, 4), -1, np.int32), np.zeros(2, np.int32), np.zeros(N, np.int32))
+    grow = lambda *k: torch.tensor(k, dtype=torch.int32).cuda()  # noqa: E731
+    out, info = abi.tq_pages_resize(t, grow(40, 10), pool)
+    assert info is out.info and out is not t and t.info is None and info.tolist() == [3, 0]
+    other, info2 = abi.tq_pages_resize(out, grow(100, 0), pool)
+    assert info2.tolist() == [2, 0] and info.tolist() == [3, 0]    # another table's
+    mine = torch.full((2,), 7, dtype=torch.int32, device="cuda")
+    same, info3 = abi.tq_pages_resize(other, grow(0, 0), pool, out=other, info=mine)
+    assert same is other and info3 is mine and mine.tolist() == [0, 0] and other.info.tolist() == [2, 0]
+    moved = torch.empty(N, dtype=torch.int32, device="cuda")
+    done, m, i = abi.tq_pages_compact(out, pool, moved_to=moved)
+    assert m is moved and i is done.info and done.moved_to is None and i.tolist() == [3, 0]
+    done2, m2, _ = abi.tq_pages_compact(out, pool, out=done)
+    assert done2 is done and m2 is done.moved_to and torch.equal(m2, moved)
+
+
 def test_captured_and_replayed_on_another_stream():
     """One decode step's books in a graph: the row lengths move on between replays."""
     page, n, mp, N = 32, 4, 5, 30
