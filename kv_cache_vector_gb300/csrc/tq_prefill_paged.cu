@@ -22,9 +22,10 @@
 //
 // The work is cut into equal shares, one per SM, along a line of all (query
 // tile, KV head, block of positions) units: a share may end inside an item.
-// The two (or more) parts of such an item go to the workspace and
-// k_prefill_paged_join adds them up in order.  All lengths are read on the
-// device: the launch is the same for every batch.
+// (With few items a share is a part of one item.)  The two or more parts of
+// such an item go to the workspace and k_prefill_paged_join adds them up in
+// order.  All lengths are read on the device: the launch is the same for every
+// batch.
 //
 // Two streams of steps keep the tensor cores and the softmax warps busy at
 // once (d <= 128): with more than 128 query rows, stream g takes row tile g
@@ -45,7 +46,7 @@
 // that attend to it see them) and its V row zero.
 //
 // What bounds it.  Two chunks of 4096 tokens over 12-16k positions (32 / 8
-// heads, d = 128, K4/V3): 1.39 ms, 1.13 PFLOP/s of useful products, 59% of the
+// heads, d = 128, K4/V3): 1.37 ms, 1.15 PFLOP/s of useful products, 60% of the
 // measured burst rate; about 4400 cycles per block and 256 rows, of which the
 // products need 2048.  A stream's step is a chain (scores 512 cycles and more,
 // as both operands come from shared memory that the expansion writes at the
@@ -53,9 +54,12 @@
 // about 110 between each), and two streams do not fill all of it.  With one
 // row tile the expansion's byte permutes set the pace, about 3800 cycles per
 // block: 24 sequences of 1-4 tokens over 6-9k positions read 1.1 TB/s of
-// packed rows.  Measured and not taken: score buffers of 64 columns, two per
-// stream (1886 us); two softmax threads per row (1532 us); separate warps for
-// the two kinds of products (1633 us); 4 or 16 expansion warps (1486 and 1570 us).
+// packed rows.  Measured and not taken, against 1418 us of that step: score
+// buffers of 64 columns, two per stream (1886 us); two softmax threads per row
+// (1532 us); separate warps for the two kinds of products (1633 us); 4 or 16
+// expansion warps (1486 and 1570 us).  Nor taken: the transform's stages across
+// the 64-dim pieces first, straight from the queries' tile, and outputs staged
+// there (d = 256: 120 us against 100; the same elements are read several times).
 //
 // Every wait on an mbarrier is bounded (2 s); one that gives up sets the
 // device status word and a flag that ends the others.  The softmax warps go
@@ -90,11 +94,12 @@ struct PpGeo {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     // The cost of a block for two row tiles and for one, and of an item's query
     // rotation and output, by which the line of work is cut into shares.  One row
-    // tile costs nearly what two do (the expansion is the same): 32 sequences of
+    // tile costs nearly what two do (the expansion is the same).  32 sequences of
     // 1-496 tokens over 0.2-8k positions took 339 us with 2 : 1 and 2 blocks an
-    // item, 233 us with these.
+    // item, 223 us with these (238 and 229 us with 3 and 7 blocks an item); at
+    // d = 256, 5 chunks with a window of 1024, 4 blocks 95 us and 5 blocks 98 us.
     static constexpr int kCostPair = kStreams == 2 ? 6 : 1, kCostSplit = kStreams == 2 ? 5 : 1;
-    static constexpr int kCostItem = 5 * kCostPair;
+    static constexpr int kCostItem = kStreams == 2 ? 5 * kCostPair : 4;
     static constexpr int kSoftWarps = 4 * kStreams;
     static constexpr int kDeqWarps = 8;
     static constexpr int kWarps = kSoftWarps + kDeqWarps + 3;
@@ -213,10 +218,14 @@ struct PpPart {
     bool head, whole;    // part starts the item; covers it
 };
 
-// The block at which a cut `off` units into an item of w units falls: any
-// rounding will do that never decreases and is the same for every CTA.
-__device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w) {
-    return off >= w ? nblk : min(nblk, (int)((float)nblk * __fdividef((float)off, (float)w)));
+// The block at which a cut `off` units into an item of w units falls.  The
+// item's own cost lies in front of its blocks: a share that starts inside an
+// item pays it once more, nearly every share does, and so the shares stay
+// equal.  Any rounding will do that never decreases and is the same for every
+// CTA.
+__device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w, int64_t over) {
+    return off >= w ? nblk
+                    : off <= over ? 0 : min(nblk, (int)((float)nblk * __fdividef((float)(off - over), (float)(w - over))));
 }
 
 // Blocks of row tile i, the first of them, and the end of its positions.
@@ -265,8 +274,8 @@ __device__ bool pp_next(const PpArgs& A, PpCursor& c, PpSeq<D>& q, PpPart& p) {
         p.i = c.i;
         p.h = c.h;
         pp_rows<D>(A, q, p);
-        p.blk0 = pp_cut(p.nblk, c.off, w);
-        p.blk1 = pp_cut(p.nblk, end, w);
+        p.blk0 = pp_cut(p.nblk, c.off, w, q.over);
+        p.blk1 = pp_cut(p.nblk, end, w, q.over);
         p.head = c.off == 0;
         p.whole = p.nblk == 0 ? p.head : (p.blk0 == 0 && p.blk1 == p.nblk);
         c.left -= end - c.off;
@@ -932,9 +941,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     const int64_t w = seq.weight(cur.i), per = *share;
                     const int nblk = pp_blocks<D>(A, seq, cur.i);
                     // no join where one share has all of the item's blocks
-                    owner = nblk > 0 && pp_cut(nblk, cur.off, w) < nblk;
-                    for (int64_t x = cur.off; x < w && pp_cut(nblk, x, w) == 0; x += per)
-                        if (pp_cut(nblk, min(w, x + per), w) == nblk) owner = false;
+                    owner = nblk > 0 && pp_cut(nblk, cur.off, w, seq.over) < nblk;
+                    for (int64_t x = cur.off; x < w && pp_cut(nblk, x, w, seq.over) == 0; x += per)
+                        if (pp_cut(nblk, min(w, x + per), w, seq.over) == nblk) owner = false;
                     last += (int)((w - cur.off + per - 1) / per);
                 }
             }
