@@ -672,6 +672,7 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
     with _on(dev):
         if out is None:
             out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
+        a, b = table._view(layers, shape), out._view(layers, shape)
         if info is None:
             if out.info is None:
                 out.info = out.lens.new_empty(2)
@@ -684,7 +685,6 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         _ints(dev, info, other)
         if info.numel() != 2 or other.numel() != (layers.n_pages if arg is None else n_seqs):
             raise ValueError("info has 2 entries, parents and new_lens one per row, moved_to one per page")
-        a, b = table._view(layers, shape), out._view(layers, shape)
         ws = _scratch(workspace, dev, tq_pages_workspace_bytes, n_seqs, max_pages, layers.n_pages)
         middle = (a, b, other.data_ptr()) if arg is None else (a, other.data_ptr(), b)
         _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,

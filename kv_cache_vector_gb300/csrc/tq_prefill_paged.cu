@@ -1510,7 +1510,6 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
     using Z = PpGeo<D>;
     constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
     __shared__ float tile[32][D + 1];
-    griddep_launch();
     griddep_wait();
     const int sh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int4* meta = reinterpret_cast<const int4*>(A.meta);

@@ -294,6 +294,25 @@ def test_what_a_call_says_stays_with_the_table_it_wrote():
     assert done2 is done and m2 is done.moved_to and torch.equal(m2, moved)
 
 
+def test_a_refused_call_leaves_the_table_as_it_was():
+    pool = make_pool(15, 12)
+    t = on_gpu(np.full((2, 4), -1, np.int32), np.zeros(2, np.int32), np.zeros(12, np.int32))
+    to = torch.tensor([40, 10], dtype=torch.int32).cuda()
+    out = on_gpu(np.zeros((2, 4), np.int32), np.zeros(2, np.int64), np.zeros(12, np.int32))
+    with pytest.raises(TypeError):
+        abi.tq_pages_resize(t, to, pool, out=out)
+    assert out.info is None
+    for bad in (dict(info=torch.zeros(3, dtype=torch.int32, device="cuda")), dict(out=abi.PageTable(
+            t.block_table[:, :3].contiguous(), t.lens, t.refs)), dict(workspace=torch.zeros(1 << 20))):
+        with pytest.raises(ValueError):
+            abi.tq_pages_resize(t, to, pool, **bad)
+    with pytest.raises(ValueError):
+        abi.tq_pages_resize(t, to[:1], pool)
+    with pytest.raises(abi.TQError):     # a workspace that is too small
+        abi.tq_pages_resize(t, to, pool, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert t.info is None and not t.lens.any() and not t.refs.any()
+
+
 def test_captured_and_replayed_on_another_stream():
     """One decode step's books in a graph: the row lengths move on between replays."""
     page, n, mp, N = 32, 4, 5, 30
