@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
     __shared__ long long s_scan64[kPgWarps];
     __shared__ int s_cnt[2];
     __shared__ int s_warp[2][kPgWarps];  // per-warp counts, then their exclusive sums
+    griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nb = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -279,11 +280,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
                     const int r = A.refs[tail] + W.delta[tail];
                     if (r > 1) {
                         int before = 0;
-                        for (int j0 = 0; j0 < i; j0 += 32) {
-                            const int j = j0 + lane;
-                            before += __popc(__ballot_sync(0xFFFFFFFFu, j < i && W.first[j] == tail));
-                        }
-                        own = r - before > 1;
+#pragma unroll 8
+                        for (int j = lane; j < i; j += 32) before += W.first[j] == tail;
+                        own = r - (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)before) > 1;
                     }
                 }
                 if (lane == 0) {
@@ -300,12 +299,16 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
             cnt += __popc(__ballot_sync(0xFFFFFFFFu, p < hi && A.refs[p] + W.delta[p] <= 0));
         if (lane == 0) s_warp[0][warp] = cnt;
         __syncthreads();
-        {
-            int total;
-            const int incl = block_scan(tid < kPgWarps ? s_warp[0][tid] : 0, s_scan, &total);
-            __syncthreads();
-            if (tid < kPgWarps) s_warp[0][tid] = incl - s_warp[0][tid];
-            cnt = total;
+        if (warp == 0) {  // the warps' counts to their exclusive sums
+            const int own = s_warp[0][lane];
+            int incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            s_warp[0][lane] = incl - own;
+            cnt = __shfl_sync(0xFFFFFFFFu, incl, 31);  // thread 0 passes it on
         }
         if (rank == nb - 1) {
             long long base = 0;  // takes in the low 32 bits' place, pairs above
@@ -681,13 +684,15 @@ static cudaError_t launch_plan(const PagesPlan& A, cudaStream_t s) {
     cfg.gridDim = dim3(nb);
     cfg.blockDim = dim3(kPgThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = nb;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = nb;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = nb > 1 ? 1 : 0;
+    cfg.numAttrs = nb > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pages_plan<OP>, A, status_word());
     return e != cudaSuccess ? e : cudaGetLastError();
 }
