@@ -413,7 +413,9 @@ size_t tq_pages_workspace_bytes(int n_seqs, int max_pages, int64_t n_pages);
  * is copied), and within one pool one whose destination is some pair's source
  * (status word 62).  n <= dst[0].n_pages.  Layer l of src and of dst are the
  * same memory for all l, or no arrays overlap; the ids are outside the
- * workspace (else TQ_ERR_INVALID_ARG). */
+ * workspace (else TQ_ERR_INVALID_ARG).  Up to TQ_PAGES_COPY_FEW pairs need no
+ * workspace (it is not looked at). */
+#define TQ_PAGES_COPY_FEW 128
 tq_status tq_pages_copy(const tq_paged_cache *src, const tq_paged_cache *dst, int n_layers, int Hkv,
                         int d, int k_bits, int v_bits, const int32_t *src_ids, const int32_t *dst_ids,
                         int64_t n, void *workspace, size_t workspace_bytes, tq_stream_t stream);

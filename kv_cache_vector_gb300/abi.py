@@ -641,6 +641,9 @@ def tq_pages_workspace_bytes(n_seqs: int, max_pages: int, n_pages: int) -> int:
     return int(lib().tq_pages_workspace_bytes(n_seqs, max_pages, n_pages))
 
 
+_PAGES_COPY_FEW = 128  # TQ_PAGES_COPY_FEW: up to so many pairs need no workspace
+
+
 def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
                   workspace: torch.Tensor | None = None):
     """Copy page src_ids[i] of `src` to page dst_ids[i] of `dst` (PagedLayers,
@@ -655,11 +658,15 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
         raise ValueError("src_ids and dst_ids must have one length")
     if src.device != dst.device:
         raise ValueError("src and dst must be on one device")
+    n = src_ids.numel()
     with _on(dst.device):
-        ws = _scratch(workspace, dst.device, tq_pages_workspace_bytes, 0, 0, dst.n_pages)
+        ws, size = None, 0
+        if n > _PAGES_COPY_FEW or workspace is not None:
+            ws = _scratch(workspace, dst.device, tq_pages_workspace_bytes, 0, 0, dst.n_pages)
+            ws, size = ws.data_ptr(), ws.nbytes
         _check("tq_pages_copy", lib().tq_pages_copy(
-            src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(),
-            src_ids.numel(), ws.data_ptr(), ws.nbytes, _raw_stream(dst.device)))
+            src.views, dst.views, len(dst.views), *dst.args, src_ids.data_ptr(), dst_ids.data_ptr(), n, ws, size,
+            _raw_stream(dst.device)))
 
 
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):

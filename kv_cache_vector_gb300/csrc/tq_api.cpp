@@ -915,6 +915,7 @@ tq_status check_layers(const tq_paged_cache* layers, int n_layers, int Hkv, int 
 }
 
 bool layers_accessible(const tq_paged_cache* layers, int n_layers) {
+    if (pageable_access()) return true;
     for (int l = 0; l < n_layers; ++l)
         if (!paged_accessible(layers[l])) return false;
     return true;
@@ -927,15 +928,38 @@ Span layer_span(const tq_paged_cache& c, int a, int Hkv, int d, int k_bits, int 
     return {reinterpret_cast<uintptr_t>(p), rows * (a == 0 ? d * k_bits / 8 : a == 2 ? d * v_bits / 8 : 4)};
 }
 
-// From the first byte of a layer's arrays to the last.
-Span layer_run(const tq_paged_cache& c, int Hkv, int d, int k_bits, int v_bits) {
-    uintptr_t lo = UINTPTR_MAX, hi = 0;
-    for (int a = 0; a < 4; ++a) {
-        const Span s = layer_span(c, a, Hkv, d, k_bits, v_bits);
-        lo = s.at < lo ? s.at : lo;
-        hi = s.at + s.bytes > hi ? s.at + s.bytes : hi;
+// The arrays of n layers in the order of their addresses.  (Layers made one
+// after the other mostly are in it already.)
+int sorted_spans(const tq_paged_cache* layers, int n, int Hkv, int d, int k_bits, int v_bits, Span* out) {
+    for (int i = 0; i < 4 * n; ++i) {
+        const Span s = layer_span(layers[i >> 2], i & 3, Hkv, d, k_bits, v_bits);
+        int j = i;
+        for (; j > 0 && out[j - 1].at > s.at; --j) out[j] = out[j - 1];
+        out[j] = s;
     }
-    return {lo, hi - lo};
+    return 4 * n;
+}
+
+// Do an array of a and one of b overlap?
+bool layers_overlap(const tq_paged_cache* a, const tq_paged_cache* b, int n, int Hkv, int d, int k_bits, int v_bits) {
+    constexpr int kAt = 64;  // layers at a time
+    Span x[4 * kAt], y[4 * kAt];
+    for (int l = 0; l < n; l += kAt) {
+        const int nx = sorted_spans(a + l, n - l < kAt ? n - l : kAt, Hkv, d, k_bits, v_bits, x);
+        for (int m = 0; m < n; m += kAt) {
+            const int ny = sorted_spans(b + m, n - m < kAt ? n - m : kAt, Hkv, d, k_bits, v_bits, y);
+            // along both: a span that starts before the other side's furthest end overlaps it
+            uint64_t ex = 0, ey = 0;
+            for (int i = 0, j = 0; i < nx || j < ny;) {
+                const bool of_x = j == ny || (i < nx && x[i].at <= y[j].at);
+                const Span& s = of_x ? x[i++] : y[j++];
+                if (s.at < (of_x ? ey : ex)) return true;
+                uint64_t& e = of_x ? ex : ey;
+                if (s.at + s.bytes > e) e = s.at + s.bytes;
+            }
+        }
+    }
+    return false;
 }
 
 // Fork, resize and compaction: the checks they share, then the launch.
@@ -1018,30 +1042,19 @@ tq_status tq_pages_copy(const tq_paged_cache* src, const tq_paged_cache* dst, in
             a.n_pages != b.n_pages)
             return TQ_ERR_INVALID_ARG;
     }
-    // (an array against an array only where the runs of memory that the layers' arrays lie in meet)
-    for (int m0 = 0; !same && m0 < n_layers; m0 += 64) {
-        Span run[64];
-        const int mn = n_layers - m0 < 64 ? n_layers - m0 : 64;
-        for (int m = 0; m < mn; ++m) run[m] = layer_run(dst[m0 + m], Hkv, d, k_bits, v_bits);
-        for (int l = 0; l < n_layers; ++l) {
-            const Span r = layer_run(src[l], Hkv, d, k_bits, v_bits);
-            for (int m = 0; m < mn; ++m)
-                for (int k = 0; overlap(r, run[m]) && k < 16; ++k)
-                    if (overlap(layer_span(src[l], k & 3, Hkv, d, k_bits, v_bits),
-                                layer_span(dst[m0 + m], k >> 2, Hkv, d, k_bits, v_bits)))
-                        return TQ_ERR_INVALID_ARG;
-        }
-    }
+    if (!same && layers_overlap(src, dst, n_layers, Hkv, d, k_bits, v_bits)) return TQ_ERR_INVALID_ARG;
     if (n == 0) return TQ_OK;
     if (!src_ids || !dst_ids) return TQ_ERR_INVALID_ARG;
     if (!aligned4(src_ids) || !aligned4(dst_ids)) return TQ_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < tq::pages_workspace_bytes(0, dst[0].n_pages)) return TQ_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
-    const Span ws{reinterpret_cast<uintptr_t>(workspace), tq::pages_workspace_bytes(0, dst[0].n_pages)};
-    if (overlap(ws, {reinterpret_cast<uintptr_t>(src_ids), 4 * (uint64_t)n}) ||
-        overlap(ws, {reinterpret_cast<uintptr_t>(dst_ids), 4 * (uint64_t)n}))
-        return TQ_ERR_INVALID_ARG;
-    if (!device_accessible(src_ids) || !device_accessible(dst_ids) || !device_accessible(workspace) ||
+    if (n > TQ_PAGES_COPY_FEW) {
+        if (!workspace || workspace_bytes < tq::pages_workspace_bytes(0, dst[0].n_pages)) return TQ_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
+        const Span ws{reinterpret_cast<uintptr_t>(workspace), tq::pages_workspace_bytes(0, dst[0].n_pages)};
+        if (overlap(ws, {reinterpret_cast<uintptr_t>(src_ids), 4 * (uint64_t)n}) ||
+            overlap(ws, {reinterpret_cast<uintptr_t>(dst_ids), 4 * (uint64_t)n}) || !device_accessible(workspace))
+            return TQ_ERR_INVALID_ARG;
+    }
+    if (!device_accessible(src_ids) || !device_accessible(dst_ids) ||
         !layers_accessible(src, n_layers) || !layers_accessible(dst, n_layers))
         return TQ_ERR_INVALID_ARG;
     tq::PagesCall c = {};

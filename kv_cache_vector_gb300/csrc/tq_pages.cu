@@ -597,7 +597,7 @@ k_pages_copy(const __grid_constant__ CopyLayers<MAX> P, const CopySizes Z, int L
 // that there is no plan to wait for.  In a graph, with the plan and so: 5 pages
 // of 2 layers 6.5 and 3.6 us; 128 pages of 768 bytes 4.9 and 3.2 us; 128 of
 // 0.25 MB in 2 layers 23.8 and 21.3 us.
-constexpr int kPcFew = 128;
+constexpr int kPcFew = TQ_PAGES_COPY_FEW;
 
 template <int MAX>
 __global__ void __launch_bounds__(kPcThreads, kPcPerSm)
@@ -740,7 +740,7 @@ cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s) {
     Z.n[0] = rows * (uint32_t)(c.d * c.k_bits / 8) / 16;
     Z.n[1] = Z.n[3] = rows / 4;
     Z.n[2] = rows * (uint32_t)(c.d * c.v_bits / 8) / 16;
-    const PagesWs W = pages_ws(c.ws, A.n_pages, A.n_seqs);
+    const PagesWs W = few ? PagesWs{} : pages_ws(c.ws, A.n_pages, A.n_seqs);
     // the most pairs that the plan can ask for: a small call gets a small grid
     const int64_t most = op == kPagesCopy ? c.n : (op == kPagesCompact ? (int64_t)A.n_pages / 2 : (int64_t)c.n_seqs);
     const uint32_t words = Z.n[0] + Z.n[1] + Z.n[2] + Z.n[3];

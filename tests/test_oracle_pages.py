@@ -156,11 +156,15 @@ def test_refusals_of_the_copy(L):
     far = [_cache((40 + i) << 32) for i in range(70)]
     assert copy(s=_layers(*far[:69], abi.PagedCacheView(1 << 32, 1 << 33, 1 << 34, (109 << 32) + (1 << 24), 4, 64)),
                 t=_layers(*[_cache((200 + i) << 32) for i in range(69)], far[69]), nl=70) == 1
-    assert copy(s=_layers(*far), t=_layers(*[_cache((200 + i) << 32) for i in range(70)]), nl=70, ws=None) == 5
-    assert copy(si=W + 64) == 1 and copy(ti=W + need - 4) == 1             # ids inside the workspace
+    assert copy(s=_layers(*far), t=_layers(*[_cache((200 + i) << 32) for i in range(70)]), nl=70, ti=ids + 2) == 3
+    # many pairs: with a workspace, and the ids outside of it
+    many = dict(s=_layers(_cache(n_pages=200)), t=_layers(_cache(1 << 36, 200)), n=129,
+                size=L.tq_pages_workspace_bytes(0, 0, 200))
+    assert copy(**{**many, "si": W + 64}) == 1 and copy(**{**many, "ti": W + many["size"] - 4}) == 1
+    assert copy(**{**many, "ws": None}) == 5 and copy(**{**many, "size": many["size"] - 1}) == 5
+    assert copy(**{**many, "ws": W + 8}) == 3
     assert copy(d=48) == 2 and copy(kb=1) == 2
     assert copy(si=None) == 1 and copy(ti=ids + 2) == 3
-    assert copy(ws=None) == 5 and copy(size=need - 1) == 5 and copy(ws=W + 8) == 3
 
 
 def test_python_layer_refusals():
