@@ -3,7 +3,7 @@
 //
 // A page table holds, per sequence row, its page ids and its length, and per
 // page the number of rows that hold it (0: free).  Every operator is two
-// launches:
+// launches (a copy of few pairs one, k_pages_copy_few):
 //   k_pages_plan   one thread-block cluster (1 or 8 CTAs of 1024 threads)
 //     works out the new table and the list of (source, destination) page
 //     pairs to copy.  All of its decisions follow row order and take the
@@ -17,11 +17,11 @@
 //     step.  Bound by memory: a copied page is read once and written once.
 //     473 pages of 2 MB (32 layers): 293 us, 6.35 TB/s; with 4, 8 and 16 KB
 //     steps 413, 322 and 304 us (too few bytes in flight).
-// The copy is launched with programmatic stream serialization, so its CTAs are
-// resident when the plan ends.  Small calls are bound by the launches and the
-// plan's chain of dependent reads: 4 us for a copy of 5 pages, 10 to 20 us for
-// a fork, resize or compaction without pages to copy (8 to 512 rows, 100 to
-// 6500 pages).
+// Both are launched with programmatic stream serialization, so that their CTAs
+// are there when the kernel before ends.  Small calls are bound by the launches
+// and the plan's chain of dependent reads (steps of 1 to 2 us each): 4 us for a
+// copy of 5 pages, 10 to 17 us for a fork, resize or compaction with few pages
+// to copy (8 to 512 rows, 100 to 6500 pages).
 #include <climits>
 
 #include <cooperative_groups.h>
