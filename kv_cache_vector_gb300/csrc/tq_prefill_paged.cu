@@ -858,8 +858,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             if (cur.parts > 0) {  // the one part of this share
                 u.b = cur.b, u.i = cur.i, u.h = cur.h;
                 pp_rows<D>(A, seq, u);
-                u.blk0 = (int)((int64_t)u.nblk * cur.off / cur.parts);
-                u.blk1 = (int)((int64_t)u.nblk * (cur.off + 1) / cur.parts);
+                const uint32_t nb = u.nblk, at = (uint32_t)cur.off, of = cur.parts;  // nb of < 2^32
+                u.blk0 = nb * at / of;
+                u.blk1 = nb * (at + 1) / of;
                 u.head = cur.off == 0;
                 u.whole = u.nblk == 0 ? u.head : (u.blk0 == 0 && u.blk1 == u.nblk);
                 more = job == 0 && (u.whole || u.blk1 > u.blk0);
@@ -1503,10 +1504,11 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
 }
 
 // Block (share, y): rows 32 y .. + 31 of the item that the share owns, its
-// parts summed in the order of the shares, divided and rotated back.
-template <int D>
-__global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constant__ PpArgs A,
-                                                            const __grid_constant__ PagedPrefillConsts P) {
+// parts summed in the order of the shares, AT parts' loads in flight, divided
+// and rotated back.
+template <int D, int AT>
+__global__ void __launch_bounds__(256, D < 256 && AT == 2 ? 3 : 2)
+k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefillConsts P) {
     using Z = PpGeo<D>;
     constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
     __shared__ float tile[32][D + 1];
@@ -1533,7 +1535,6 @@ __global__ void __launch_bounds__(256) k_prefill_paged_join(const __grid_constan
         unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && (near & (cl == sh ? 2 : 1)));
         while (has && in) {
             // a few parts' loads in flight at once
-            constexpr int AT = D >= 256 ? 2 : 4;
             float4 v[AT][C];
             float m[AT], lc[AT], ec[AT];
             unsigned left = has;
@@ -1668,7 +1669,13 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     // groups of 32 rows that an item can have
     const int64_t rows = c.n_q * (c.Hq / c.Hkv);
     const unsigned groups = (unsigned)((rows < Z::kRows ? rows : Z::kRows) + 31) / 32;
-    return launch_pdl(k_prefill_paged_join<D>, dim3(shares, groups), dim3(256), 0, s, A, P);
+    // Few rows: few items in many parts, four parts' loads in flight.  More: mostly
+    // two parts an item, and three CTAs per SM count for more (two in flight: drafts
+    // 21.1 -> 21.5 us, but 32 mixed sequences 222 -> 220, 2048 tokens after 4000 238
+    // -> 235).
+    if (D < 256 && rows < Z::kRows)
+        return launch_pdl(k_prefill_paged_join<D, D < 256 ? 4 : 2>, dim3(shares, groups), dim3(256), 0, s, A, P);
+    return launch_pdl(k_prefill_paged_join<D, 2>, dim3(shares, groups), dim3(256), 0, s, A, P);
 }
 
 template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, cudaStream_t);
