@@ -275,6 +275,20 @@ def test_copy_of_random_pairs(n, same):
     check_contents(dst, before, want, before_dst)
 
 
+@pytest.mark.parametrize("L", [1, 4, 5, 64, 65, 130])
+@pytest.mark.parametrize("n", [3, 150])
+def test_copy_of_many_layers(L, n):
+    """As many layers as a launch takes and more, with few pairs and many."""
+    N = 310
+    src = make_pool(16, N, L=L, Hkv=1)
+    ids = np.random.default_rng(L).permutation(N).astype(np.int32)
+    s, t = ids[:n].copy(), ids[n:2 * n].copy()
+    before = contents(src)
+    abi.tq_pages_copy(src, src, torch.from_numpy(s).cuda(), torch.from_numpy(t).cuda())
+    assert abi.tq_device_status(reset=True) == 0
+    check_contents(src, before, list(zip(s.tolist(), t.tolist())))
+
+
 def test_what_a_call_says_stays_with_the_table_it_wrote():
     page, N = 32, 12
     pool = make_pool(14, N)
