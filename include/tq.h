@@ -343,9 +343,10 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  *   ctx_lens: [B] int32, device, at most max_pages * page_size
  *   block_table: [B][max_pages] int32, device
  * d in {32, 64, 128, 256}, Hq / Hkv up to 128.  Both products run on the
- * tensor cores with fp16 operands and fp32 sums; norms up to 2^100, the largest
- * V norms of a sequence's 128-position blocks within 2^120 of one another.
- * Positions past a row's range do not reach it, whatever their rows hold.
+ * tensor cores with fp16 operands and fp32 sums; norms of 0 and from 2^-86 to
+ * 2^100, in any order (smaller ones lose bits; blocks of 128 positions whose K
+ * norms are more than 2^15 or V norms more than 2^10 apart take longer).
+ * Positions outside a row's range do not reach it, whatever their rows hold.
  * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
  * rows are not written) and sets the device status word to 71.  A page id
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and

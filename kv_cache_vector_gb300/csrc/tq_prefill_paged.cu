@@ -34,12 +34,21 @@
 // output fills tensor memory: one stream, with two score buffers.
 //
 // Numbers.  fp16 operands, fp32 sums.  A block's K rows are scaled by a power
-// of two 2^-Ek (its largest norm is below 2^Ek), its V rows by 2^-Ev; Ek goes
-// into the factor of the scores, Ev into the exponent of the probabilities,
-//   P' = 2^(s + Ev - M),  M a running maximum of s + Ev,
+// of two 2^-Ek (its largest norm is below 2^(Ek + 14)), its V rows by 2^-Ev; Ek
+// goes into the factor of the scores, Ev into the exponent of the probabilities,
+//   P' = 2^(s + Ev - M),  M a running maximum of s + Ev, less 7,
 // so that O = sum P' V' keeps its precision however the norms vary from block
-// to block, and the denominator sums P' 2^(Eb - Ev) in fp32 (Eb: Ev of the
-// first block).  M moves only when it grows by more than 8, so P' < 2^8.
+// to block.  M moves only when it grows by more than 8, so P' < 2^15.  The
+// denominator is held apart, l = sum 2^(s - m) with m the running maximum of the
+// scores, from a block's sum of P' times 2^(M - Ev - m).
+//   The norms that set a block's powers may belong to positions that a row does
+// not attend to.  Its own K rows keep all their bits down to 2^-16 of the
+// largest (fp16 has 28 powers of two below 2^14, the levels use 7 of them) and
+// its V rows and probabilities to 2^-10.  A block whose norms (0 left out) are
+// further apart, or whose Ev is 60 below an earlier one (the sum of P' could lose
+// what l needs), is "wide": every position has its own Ek and Ev, and the softmax
+// warps first put them into the scores (pp_wide).  Such steps are slower, and no
+// size of norms that a row does not attend to changes its result.
 // The query, P and the products of level and norm are rounded to fp16 once,
 // 2^-11 relative, an eighth of the bf16 output's step (V's norms once more,
 // before the product).  A non-finite norm makes the scores of its row NaN (only rows
@@ -67,6 +76,7 @@
 // no output is written after the flag.
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "tq_async.cuh"
 #include "tq_device.cuh"
@@ -111,14 +121,16 @@ struct PpGeo {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kQ + kStreams * kQTile;  // 4 tiles: K, V of two blocks
     static constexpr uint32_t kStg = kRing + 4 * kTile;
-    static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [8] float2: 2^Ek, Ev
+    static constexpr uint32_t kMeta = kStg + kStages * kStage;  // [8] float2: 2^Ek (0: wide), Ev
     static constexpr uint32_t kSegs = kMeta + 64;               // [kStages] segments staged
-    static constexpr uint32_t kRed = kSegs + 16;                // scan and merge scratch
+    static constexpr uint32_t kRed = kSegs + 16;                // scan scratch, then
+    static constexpr uint32_t kCols = kRed;  // [kN] the wide block's Ek and Ev per position, a signed byte each
     static constexpr uint32_t kRedBytes = 2 * 8 * kWarps;
+    static_assert(2 * kN <= kRedBytes && kRed % 16 == 0, "the positions' powers of two");
     static constexpr uint32_t kCur = (kRed + kRedBytes + 15) / 16 * 16;  // start cursor
     static constexpr uint32_t kJobs = kCur + 80;                // [2] jobs
     static constexpr uint32_t kBar = kJobs + 2 * 48;
-    static constexpr int kBars = 2 * kStages + 4 + 4 + 8 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1;
+    static constexpr int kBars = 2 * kStages + 4 + 4 + 8 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr uint32_t kSmem = (kMisc + 8 + 127) / 128 * 128;
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // buffer b at kN b; output g at 128 g further
@@ -618,6 +630,82 @@ __device__ __forceinline__ void pp_mask(uint32_t (&s)[32], int c0, int c1) {
     for (int k = 0; k < 32; ++k) s[k] = (on >> k) & 1u ? s[k] : 0xFF800000u;
 }
 
+// A wide block's scores, 16 columns from column c on, times their own factors;
+// columns outside [c0, c1) become -inf.
+__device__ __forceinline__ void pp_wide16(uint32_t t_s, const unsigned char* cols, float cq, int c, int c0, int c1,
+                                          float (&x)[16]) {
+    uint32_t s[16];
+    tmem_ld16(t_s + c, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int e = *reinterpret_cast<const volatile int8_t*>(cols + 2 * (c + k));
+        x[k] = c + k < c0 || c + k >= c1 ? -INFINITY : __uint_as_float(s[k]) * (cq * pp_pow2(e));
+    }
+}
+// A wide block becomes one without powers of two: its scores times their factors
+// plus the positions' V exponents, in the scores' place.  Returns the larger of m
+// and the block's maximum score, and the row's sum of 2^(s - that).  (A call by
+// itself, with values only: as part of the step it took registers and
+// instruction cache from all steps, 1.37 -> 1.50 ms for the long chunks; 1.39 so.)
+template <int N>
+__device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, float cq, int c0, int c1, float m) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < N; c += 16) {
+        float x[16];
+        pp_wide16(t_s, cols, cq, c, c0, c1, x);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m = fmaxf(m, x[k]);
+    }
+    const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+    for (int c = 0; c < N; c += 16) {
+        float x[16];
+        uint32_t w[16];
+        pp_wide16(t_s, cols, cq, c, c0, c1, x);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            sum += pp_exp2(x[k] - mr);
+            w[k] = __float_as_uint(x[k] + (float)*reinterpret_cast<const volatile int8_t*>(cols + 2 * (c + k) + 1));
+        }
+        tmem_st16(t_s + c, w);
+    }
+    tmem_wait_st();
+    return make_float2(m, sum);
+}
+// Sums of 2^(s - m) of two sets of positions put together (m -inf: an empty set,
+// its sum 0 or NaN).
+__device__ __forceinline__ void pp_join_sums(float& l, float& m, float l1, float m1) {
+    const float mx = fmaxf(m, m1), mr = mx == -INFINITY ? 0.f : mx;
+    l = l * pp_exp2(m - mr) + l1 * pp_exp2(m1 - mr);
+    m = mx;
+}
+
+// The finite norms' bits, 0 for the others; the power of two that goes with them:
+// norms below 2^(e + 14), and a range that keeps every factor of the kernel a
+// normal fp32.
+__device__ __forceinline__ uint32_t pp_finite(float v) {
+    const uint32_t x = __float_as_uint(v) & 0x7FFFFFFFu;
+    return x < 0x7F800000u ? x : 0u;
+}
+__device__ __forceinline__ int pp_exponent(uint32_t m) { return min(100, max(-100, (int)(m >> 23) - 140)); }
+
+// The factors of a wide block (norms kn and, behind them, vn), and its
+// positions' powers of two.
+template <int N>
+__device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint32_t segs, int lim, int seg_sh) {
+#pragma unroll 1
+    for (int r = threadIdx.x & 31; r < N; r += 32) {
+        const bool in = r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+        const float k = in ? kn[r] : 0.f, v = in ? kn[N + r] : 0.f;
+        const int ek = pp_exponent(pp_finite(k)), ev = pp_exponent(pp_finite(v));
+        kn[r] = fmaf(v, 0.f, k * pp_pow2(-ek));  // NaN if either norm is not finite
+        kn[N + r] = fabsf(v) <= FLT_MAX ? v * pp_pow2(-ev) : 0.f;
+        reinterpret_cast<uint16_t*>(cols)[r] = (uint16_t)((ek & 0xFF) | (ev & 0xFF) << 8);
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <int D>
@@ -645,6 +733,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     uint64_t* q_full = job_free + 2;          // the item's queries are in shared memory
     uint64_t* meet = q_full + 1;              // all softmax warps are here
     uint64_t* drain = meet + 1;               // products in flight, on the abort path
+    uint64_t* cols_free = drain + 1;          // the softmax warps have read a wide block's powers
     volatile int* abort_f = reinterpret_cast<volatile int*>(sm + Z::kMisc + 4);
     uint32_t* slot = reinterpret_cast<uint32_t*>(sm + Z::kMisc);
     PpCursor* start = reinterpret_cast<PpCursor*>(sm + Z::kCur);
@@ -681,6 +770,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         mbar_init(q_full, SW);
         mbar_init(meet, SW);
         mbar_init(drain, 1);
+        mbar_init(cols_free, SW);
         *abort_f = 0;
         mbar_fence_init();
         start->left = 0;
@@ -1046,10 +1136,10 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     } else if (warp == SW + DW + 2) {
         // ---- norms: a block's powers of two, and its rows' factors in the
         // norms' place
-        uint32_t tc = 0;
+        uint32_t tc = 0, wides = 0;
         bool ok = true;
         while (ok && next_job()) {
-            int eprev = 0, emax = -1000;
+            int emax = -1000;
             for (int j = 0; j < p.nb; ++j, ++tc) {
                 const int st = tc % NS;
                 float* knp = reinterpret_cast<float*>(sm + Z::kStg + st * Z::kStage + N * D);
@@ -1060,39 +1150,46 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 const int lim = p.kv_end - (p.blk + j) * N;  // the block's positions below it count
                 const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
                 float kn[N / 32], vn[N / 32];
-                uint32_t mk = 0, mv = 0;  // the largest finite norms, as bits
+                // the largest finite norms, as bits
+                uint32_t mk = 0, mv = 0;
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
                     const int r = 32 * k + lane;
                     const bool in = r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
                     kn[k] = in ? knp[r] : 0.f;
                     vn[k] = in ? vnp[r] : 0.f;
-                    const uint32_t x = __float_as_uint(kn[k]) & 0x7FFFFFFFu, y = __float_as_uint(vn[k]) & 0x7FFFFFFFu;
-                    mk = max(mk, x < 0x7F800000u ? x : 0u);
-                    mv = max(mv, y < 0x7F800000u ? y : 0u);
+                    const uint32_t x = pp_finite(kn[k]), y = pp_finite(vn[k]);
+                    mk = max(mk, x), mv = max(mv, y);
                 }
                 mk = __reduce_max_sync(0xFFFFFFFFu, mk);
                 mv = __reduce_max_sync(0xFFFFFFFFu, mv);
-                // below 2^e; the range keeps every factor of the kernel a normal fp32
-                auto exponent = [](uint32_t m) { return min(100, max(-100, (int)(m >> 23) - 126)); };
-                const int ek = mk ? exponent(mk) : 0;
-                int ev = mv ? exponent(mv) : eprev;
-                if (mv) {
-                    // a block of far smaller values rides on the largest so far
-                    ev = max(ev, emax - 60);
-                    emax = max(emax, ev);
-                    eprev = ev;
-                }
+                // (a block without a V norm must not raise the running maximum)
+                const int ek = mk ? pp_exponent(mk) : 0, ev = pp_exponent(mv);
+                emax = max(emax, ev);
                 const float sk = pp_pow2(-ek), sv = pp_pow2(-ev);
+                bool far = ev < emax - 60;
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
-                    const int r = 32 * k + lane;
-                    knp[r] = fmaf(vn[k], 0.f, kn[k] * sk);  // NaN if either norm is not finite
-                    vnp[r] = fabsf(vn[k]) <= FLT_MAX ? vn[k] * sv : 0.f;
+                    const float x = fabsf(kn[k] * sk), y = fabsf(vn[k] * sv);  // the largest: 2^13 to 2^14
+                    far = far || (x < 0.25f && x > 0.f) || (y < 8.f && y > 0.f);
+                }
+                const bool wide = __any_sync(0xFFFFFFFFu, far);
+                if (!wide) {
+#pragma unroll
+                    for (int k = 0; k < N / 32; ++k) {
+                        const int r = 32 * k + lane;
+                        knp[r] = fmaf(vn[k], 0.f, kn[k] * sk);  // NaN if either norm is not finite
+                        vnp[r] = fabsf(vn[k]) <= FLT_MAX ? vn[k] * sv : 0.f;
+                    }
+                } else {
+                    if (wides) ok = __all_sync(0xFFFFFFFFu, pp_wait(cols_free, (wides - 1) & 1, abort_f, status));
+                    if (!ok) break;
+                    ++wides;
+                    pp_wide_norms<N>(knp, sm + Z::kCols, segs, lim, seg_sh);
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 7] = make_float2(pp_pow2(ek), (float)ev);
+                    reinterpret_cast<float2*>(sm + Z::kMeta)[tc & 7] = make_float2(wide ? 0.f : pp_pow2(ek), (float)ev);
                     mbar_arrive(&meta_full[tc & 7]);
                 }
             }
@@ -1285,99 +1382,118 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             if (lane == 0 && nb > 0) mbar_arrive(q_full);
 
             // ---- the steps
-            float M = -INFINITY, l = 0.f, eb = 0.f;
+            float M = -INFINITY, l = 0.f, m = -INFINITY;
             int lastb = -1;  // buffer of this stream's last step
-            for (int j = split ? g : 0; j < nb; j += split ? 2 : 1) {
-                const int buf = Z::kStreams == 2 ? g : (j & 1);
-                const uint32_t tc = tc0 + j;
-                pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status);
-                const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 7);
-                const float2 meta = make_float2(mp[0], mp[1]);
-                if (lastb < 0) eb = meta.y;
-                pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
-                ++ns[buf];
-                __syncwarp();
-                lastb = buf;
-                if (!rows_here) {
-                    tc_fence_before();
+            int j = split ? g : 0;
+            // Twice in the code: up to the first wide block, and from there on (in one
+            // loop, with the call in it, all steps were 4% slower)
+            auto steps = [&](auto with) __attribute__((always_inline)) {
+                constexpr bool kWide = decltype(with)::value;
+                for (; j < nb; j += split ? 2 : 1) {
+                    const int buf = Z::kStreams == 2 ? g : (j & 1);
+                    const uint32_t tc = tc0 + j;
+                    pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status);
+                    const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 7);
+                    const float2 meta = make_float2(mp[0], mp[1]);
+                    const bool wide = meta.x == 0.f;
+                    if (!kWide && wide) break;
+                    pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
+                    ++ns[buf];
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[buf]);
-                    ++npv[buf];
-                    continue;
-                }
-                tc_fence_after();
-                const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
-                const int t0 = (p.blk + j) * N;
-                // columns [c0, c1) of the block are this row's
-                const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
-                const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
-                float mx = -INFINITY;
-                if (full) {
+                    lastb = buf;
+                    if (!rows_here) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (kWide && wide && lane <= (split ? 1 : 0)) mbar_arrive(cols_free);
+                        if (lane == 0) mbar_arrive(&p_full[buf]);
+                        ++npv[buf];
+                        continue;
+                    }
+                    tc_fence_after();
+                    const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
+                    const int t0 = (p.blk + j) * N;
+                    // columns [c0, c1) of the block are this row's
+                    const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
+                    const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
+                    float cs = cq * meta.x, ev = meta.y;
+                    float2 w2;  // a wide block's
+                    if (kWide && wide) {
+                        w2 = pp_wide<N>(t_s, sm + Z::kCols, cq, c0, c1, m);
+                        cs = 1.f, ev = 0.f;
+                        __syncwarp();
+                        if (lane <= (split ? 1 : 0)) mbar_arrive(cols_free);
+                    }
+                    float mx = -INFINITY;
+                    if (full) {
 #pragma unroll 1
-                    for (int c = 0; c < N; c += 32) mx = fmaxf(mx, tmem_max32(t_s + c));
-                } else {
+                        for (int c = 0; c < N; c += 32) mx = fmaxf(mx, tmem_max32(t_s + c));
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < N; c += 32) {
+                            uint32_t s[32];
+                            tmem_ld32(t_s + c, s);
+                            tmem_wait_ld();
+                            pp_mask(s, c0 - c, c1 - c);
+                            mx = fmaxf(mx, pp_max32(s));
+                        }
+                    }
+                    const float top = mx * cs, cand = top + ev;  // -inf where nothing is attended
+                    const bool move = cand > M + 15.f || (M == -INFINITY && cand > -INFINITY);
+                    const bool rescale = move && M != -INFINITY;
+                    if (__any_sync(0xFFFFFFFFu, rescale)) {
+                        const float alpha = rescale ? pp_exp2(M - (cand - 7.f)) : 1.f;
+                        if (Z::kStreams == 1)  // the other buffer's product wrote the output last
+                            pp_wait(&pv_done[buf ^ 1], (npv[buf ^ 1] - 1) & 1, abort_f, status);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < W; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(t_out + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st32(t_out + c, o);
+                        }
+                    }
+                    if (move) M = cand - 7.f;
+                    const float m1 = kWide && wide ? w2.x : fmaxf(m, top), mr = m1 == -INFINITY ? 0.f : m1;
+                    l *= pp_exp2(m - mr);  // (NaN stays)
+                    m = m1;
+                    const float off = M == -INFINITY ? 0.f : ev - M;
+                    const F2 CS = f2(cs, cs), OFF = f2(off, off);
+                    F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
                     for (int c = 0; c < N; c += 32) {
                         uint32_t s[32];
                         tmem_ld32(t_s + c, s);
                         tmem_wait_ld();
-                        pp_mask(s, c0 - c, c1 - c);
-                        mx = fmaxf(mx, pp_max32(s));
+                        if (!full) pp_mask(s, c0 - c, c1 - c);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float a0, a1;
+                            f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), CS, OFF), a0, a1);
+                            a0 = pp_exp2(a0);
+                            a1 = pp_exp2(a1);
+                            sum[k & 1] = f2_add(sum[k & 1], f2(a0, a1));
+                            const __half2 hh = __floats2half2_rn(a0, a1);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&hh);
+                        }
+                        tmem_st16(t_s + c / 2, w);
                     }
-                }
-                const float cs = cq * meta.x;
-                const float cand = mx * cs + meta.y;  // -inf where nothing is attended
-                const bool move = cand > M + 8.f || (M == -INFINITY && cand > -INFINITY);
-                const bool rescale = move && M != -INFINITY;
-                if (__any_sync(0xFFFFFFFFu, rescale)) {
-                    const float alpha = rescale ? pp_exp2(M - cand) : 1.f;
-                    if (Z::kStreams == 1)  // the other buffer's product wrote the output last
-                        pp_wait(&pv_done[buf ^ 1], (npv[buf ^ 1] - 1) & 1, abort_f, status);
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < W; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(t_out + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st32(t_out + c, o);
-                    }
-                    l *= alpha;
+                    if (lane == 0) mbar_arrive(&p_full[buf]);
+                    ++npv[buf];
+                    float s0, s1;
+                    f2_split(f2_add(sum[0], sum[1]), s0, s1);
+                    l = kWide && wide ? l + w2.y : fmaf(s0 + s1, pp_exp2(M - ev - mr), l);
                 }
-                if (move) M = cand;
-                const float off = M == -INFINITY ? 0.f : meta.y - M;
-                const F2 CS = f2(cs, cs), OFF = f2(off, off);
-                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll 1
-                for (int c = 0; c < N; c += 32) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + c, s);
-                    tmem_wait_ld();
-                    if (!full) pp_mask(s, c0 - c, c1 - c);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float a0, a1;
-                        f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), CS, OFF), a0, a1);
-                        a0 = pp_exp2(a0);
-                        a1 = pp_exp2(a1);
-                        sum[k & 1] = f2_add(sum[k & 1], f2(a0, a1));
-                        const __half2 hh = __floats2half2_rn(a0, a1);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&hh);
-                    }
-                    tmem_st16(t_s + c / 2, w);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[buf]);
-                ++npv[buf];
-                float s0, s1;
-                f2_split(f2_add(sum[0], sum[1]), s0, s1);
-                l = fmaf(s0 + s1, pp_exp2(eb - meta.y), l);
-            }
+            };
+            steps(std::false_type{});
+            if (j < nb) steps(std::true_type{});
             if (lastb >= 0) {
                 if (Z::kStreams == 1 && nb > 1) pp_wait(&pv_done[lastb ^ 1], (npv[lastb ^ 1] - 1) & 1, abort_f, status);
                 pp_wait(&pv_done[lastb], (npv[lastb] - 1) & 1, abort_f, status);
@@ -1389,11 +1505,11 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 if (g == 1) {
                     xs[r] = M;
                     xs[128 + r] = l;
-                    xs[256 + r] = eb;
+                    xs[256 + r] = m;
                 }
                 meet_all();
                 if (g == 0 && nb > 1 && rows_here) {
-                    const float M1 = xs[r], l1 = xs[128 + r], eb1 = xs[256 + r];
+                    const float M1 = xs[r], l1 = xs[128 + r], m1 = xs[256 + r];
                     const float Mx = fmaxf(M, M1);
                     const float a0 = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = M1 == -INFINITY ? 0.f : pp_exp2(M1 - Mx);
 #pragma unroll 1
@@ -1408,7 +1524,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                         tmem_st16(t_out + c, o);
                     }
                     tmem_wait_st();
-                    l = (M == -INFINITY ? l : l * a0) + (M1 == -INFINITY ? l1 : l1 * a1) * pp_exp2(eb - eb1);
+                    pp_join_sums(l, m, l1, m1);
                     M = Mx;
                 }
                 meet_all();
@@ -1416,7 +1532,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             // ---- the rows leave: finished, or as a part
             if ((pair || g == 0) && rows_here) {
                 if (p.flags & kJobWhole) {
-                    float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
+                    float inv = l == 0.f ? 0.f : pp_exp2(M - m) * P.out_mul * P.inv_sqrt_d / l;
                     // rotated back, s . H (s2 . o): 64 dims at a time, then across
 #pragma unroll 1
                     for (int h = 0; h < PARTS; ++h) {
@@ -1486,7 +1602,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     float* x = w + D * Z::kRows;
                     x[lrow] = M;
                     x[Z::kRows + lrow] = l;
-                    x[2 * Z::kRows + lrow] = eb;
+                    x[2 * Z::kRows + lrow] = m;
                 }
                 tc_fence_before();
             }
@@ -1524,8 +1640,7 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
     const int lrow = 32 * blockIdx.y + lane;  // every warp: the same 32 rows
     constexpr int64_t PF = PagedPrefillGeo<D>::kPartFloats;
     const bool in = lrow < rows;
-    float M = -INFINITY, l = 0.f, eb = 0.f;
-    bool first = true;
+    float M = -INFINITY, l = 0.f, m = -INFINITY;
     float4 o[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1536,17 +1651,17 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
         while (has && in) {
             // a few parts' loads in flight at once
             float4 v[AT][C];
-            float m[AT], lc[AT], ec[AT];
+            float Mc[AT], lc[AT], mc[AT];
             unsigned left = has;
 #pragma unroll
             for (int t = 0; t < AT; ++t) {
-                m[t] = -INFINITY, lc[t] = 0.f, ec[t] = 0.f;
+                Mc[t] = -INFINITY, lc[t] = 0.f, mc[t] = -INFINITY;
                 if (left) {
                     const int c = c0 + __ffs(left) - 1;
                     left &= left - 1;
                     const float* pt = A.part + ((int64_t)c * 2 + (c == sh)) * PF;
                     const float* x = pt + D * Z::kRows + lrow;
-                    m[t] = __ldcg(x), lc[t] = __ldcg(x + Z::kRows), ec[t] = __ldcg(x + 2 * Z::kRows);
+                    Mc[t] = __ldcg(x), lc[t] = __ldcg(x + Z::kRows), mc[t] = __ldcg(x + 2 * Z::kRows);
 #pragma unroll
                     for (int k = 0; k < C; ++k)
                         v[t][k] = __ldcg(reinterpret_cast<const float4*>(pt) + lrow + (warp + 8 * k) * Z::kRows);
@@ -1556,13 +1671,11 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
             for (int t = 0; t < AT; ++t) {
                 if (!has) break;
                 has &= has - 1;
-                if (first) eb = ec[t];
-                first = false;
                 // both sides to the larger maximum; a side that attended to nothing
                 // has -inf, no output and the sum 0 (or NaN)
-                const float Mx = fmaxf(M, m[t]);
-                const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = m[t] == -INFINITY ? 0.f : pp_exp2(m[t] - Mx);
-                l = (M == -INFINITY ? l : l * a) + (m[t] == -INFINITY ? lc[t] : lc[t] * a1) * pp_exp2(eb - ec[t]);
+                const float Mx = fmaxf(M, Mc[t]);
+                const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = Mc[t] == -INFINITY ? 0.f : pp_exp2(Mc[t] - Mx);
+                pp_join_sums(l, m, lc[t], mc[t]);
                 M = Mx;
 #pragma unroll
                 for (int k = 0; k < C; ++k) {
@@ -1574,7 +1687,7 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
             }
         }
     }
-    const float inv = l == 0.f ? 0.f : pp_exp2(eb) * P.out_mul * P.inv_sqrt_d / l;
+    const float inv = l == 0.f ? 0.f : pp_exp2(M - m) * P.out_mul * P.inv_sqrt_d / l;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
         const float v[4] = {o[k].x, o[k].y, o[k].z, o[k].w};

@@ -1,0 +1,152 @@
+"""tq_attn_prefill_paged over norms of every size, with a tolerance that comes
+from what each token attends to and how much.
+
+Tolerance.  Four roundings to fp16 per product, SIGMA = 2 * 2^-11 / sqrt(3) in
+the root mean square (each at most eps / 2 = 2^-11 relative).  A score's error
+has at most the standard deviation SIGMA S_j, S_j = scale |q| |k_j| / sqrt(d),
+and moves element i of the output by p_j S_j SIGMA |v_ji - out_i|; the second
+product's roundings by SIGMA p_j |v_j| / sqrt(d), as the rotation spreads them
+over the row.  The deviations are added up as if they were all of one sign, and
+taken six times:
+  6 SIGMA sum_j p_j (S_j |v_ji - out_i| + |v_j| / sqrt(d)).
+Probabilities that leave fp16's normal range are off by 2^-25 where the largest
+is at least 2^-8, less than a thousandth of the second term at these lengths.
+No term knows a position that the token does not attend to."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_vector_gb300 import abi
+from test_gpu_prefill_paged import SIGMA, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from kv_cache_vector_gb300 import build
+    build.build()
+    abi.lib()
+    abi.tq_device_status(reset=True)
+
+
+def reference(bt, scale, window=0):
+    """(attention in 64 bits, its tolerance), both [rows of q, Hq, d]."""
+    q = bt.q.double().numpy()
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    G, rd = bt.Hq // bt.Hkv, math.sqrt(bt.d)
+    for b, (n, c) in enumerate(bt.lens):
+        k, v = bt.decoded(b) if n and c else (None, None)
+        for t in range(n):
+            p1 = c - n + t + 1
+            lo = max(0, p1 - window) if window else 0
+            if p1 <= 0:
+                continue
+            for h in range(bt.Hq):
+                kk, vv, qq = k[h // G, lo:p1], v[h // G, lo:p1], q[bt.cu[b] + t, h]
+                s = kk @ qq * scale
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                o = p @ vv
+                S = abs(scale) * np.linalg.norm(qq) * np.linalg.norm(kk, axis=1) / rd
+                out[bt.cu[b] + t, h] = o
+                tol[bt.cu[b] + t, h] = 6 * SIGMA * ((p * S) @ np.abs(vv - o) + (p @ np.linalg.norm(vv, axis=1)) / rd)
+    return out, tol
+
+
+def compare(bt, scale, window=0, rows=None):
+    """Both output types against the reference; rows [rows of q, Hkv]: the ones that are compared."""
+    args = bt.gpu()
+    want, tol = reference(bt, scale, window)
+    on = np.ones(want.shape[:2], bool) if rows is None else np.repeat(rows, bt.Hq // bt.Hkv, 1)
+    for dt in (torch.float32, torch.bfloat16):
+        got = abi.tq_attn_prefill_paged(*args, scale, window=window, out_dtype=dt)
+        assert abi.tq_device_status(reset=True) == 0
+        got = got.double().cpu().numpy()
+        err = np.abs(got - want)
+        over = np.where(on[..., None], err - tol - (np.abs(want) * 2.0 ** -8 if dt == torch.bfloat16 else 0.0), -np.inf)
+        over = np.where(np.isnan(got) & on[..., None], np.inf, over)
+        at = np.unravel_index(np.argmax(over), over.shape)
+        assert over[at] <= 0, (at, got[at], want[at], tol[at])
+    return got, want, tol
+
+
+def attends(bt, marks, window=0):
+    """Which rows of q, per KV head, attend to one of the (sequence, head, position) marks."""
+    hit = np.zeros((bt.q.shape[0], bt.Hkv), bool)
+    for b, h, pos in marks:
+        n, c = bt.lens[b]
+        p = np.arange(c - n, c)
+        hit[bt.cu[b]:bt.cu[b + 1], h] |= (p >= pos) & (p - pos < (window or 1 << 40))
+    return hit
+
+
+OUTSIDE = [
+    # lengths, window, marked (sequence, head, position): behind the causal mask of most
+    # tokens, in front of the window of most, and in an earlier block than theirs
+    ([(40, 200), (1, 70)], 0, [(0, 0, 199), (0, 1, 170)]),
+    ([(150, 300), (3, 90)], 0, [(0, 1, 299), (0, 0, 260), (1, 0, 89)]),
+    ([(180, 420)], 64, [(0, 0, 180), (0, 1, 230), (0, 1, 240)]),
+    ([(20, 500), (130, 700)], 100, [(0, 0, 381), (1, 1, 471), (1, 0, 560)]),
+]
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("ratio", [4, 9, 12, 15, 18, 24, 40, 90])
+@pytest.mark.parametrize("d,kb,vb", [(32, 4, 4), (64, 3, 4), (128, 4, 3), (256, 4, 4)])
+def test_a_large_norm_does_not_reach_rows_that_do_not_attend_to_it(d, kb, vb, ratio, which):
+    for i, (lens, window, marks) in enumerate(OUTSIDE):
+        bt = Batch(20 + i, lens, 4, 2, d, 64, kb, vb)
+        for b, h, pos in marks:
+            bt.set_norm(b, which, h, pos, math.sqrt(d) * 2.0 ** ratio)
+        # a token that attends to so large a key has a softmax of steps: any rounding of a
+        # score may turn it, so those rows are left out (a large value changes no score)
+        rows = ~attends(bt, marks, window) if which == "k" else None
+        assert rows is None or 0.2 < rows.mean() < 1
+        compare(bt, 1 / math.sqrt(d), window, rows)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(1, 3000)], [(300, 900)], [(9, 400), (2, 1100)]])
+@pytest.mark.parametrize("name,vnorm", [
+    ("blocks far apart", lambda p: 2.0 ** np.array([60, -60, 3, -75, 80, 0])[p // 128 % 6]),
+    ("growing far", lambda p: 2.0 ** np.minimum(80, -80 + p / 3)),
+    ("falling far", lambda p: 2.0 ** np.maximum(-80, 80 - p / 3)),
+    ("zeros, then tiny", lambda p: np.where(p < 150, 0.0, 2.0 ** -60)),
+    ("tiny, then zeros", lambda p: np.where(p < 150, 2.0 ** -60, 0.0)),
+    ("mixed within blocks", lambda p: 2.0 ** ((p * 37 % 121) - 60.0)),
+])
+def test_values_of_all_sizes(name, vnorm, lens, d):
+    """Scores of all sizes too: where the values are small they take most of the weight."""
+    bt = Batch(30, lens, 4, 2, d, 64, 4, 4)
+    for b, (_, c) in enumerate(lens):
+        v = vnorm(np.arange(c)).astype(np.float32)
+        for h in range(2):
+            for p in range(c):
+                bt.set_norm(b, "v", h, p, v[p])
+    compare(bt, 0.2)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_small_values_with_all_the_weight(d):
+    """Sharp softmaxes whose winners have far smaller V norms than the rest."""
+    bt = Batch(31, [(40, 900)], 4, 1, d, 64, 4, 4)
+    for pos in (0, 200, 511, 850):
+        bt.set_norm(0, "k", 0, pos, 60.0 * d / 128)
+        bt.set_norm(0, "v", 0, pos, 1e-3)
+    got, want, tol = compare(bt, 0.5)
+    won = np.linalg.norm(want, axis=-1) < 2e-3
+    assert won.mean() > 0.3
+    # rows of zeros in their place would not pass, nor rows 5% off
+    assert (np.abs(want[won]) > tol[won]).any(-1).all()
+    assert (0.05 * np.abs(want[won]) > tol[won] + np.abs(want[won]) * 2.0 ** -8).any(-1).mean() > 0.5
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_spread_over_many_powers(d):
+    """Norms with a log-normal spread of four powers of two, judged row by row."""
+    bt = Batch(32, [(60, 500), (1, 700), (140, 140)], 4, 2, d, 32, 4, 4,
+               norm=lambda r, n: np.exp(3 * r.standard_normal(n)))
+    compare(bt, 0.002)
