@@ -1415,7 +1415,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     // columns [c0, c1) of the block are this row's
                     const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
                     const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
-                    float cs = cq * meta.x, ev = meta.y;
+                    // not 0, which a masked score of -inf would make NaN: tiny queries over tiny norms
+                    float cs = fmaxf(cq * meta.x, FLT_MIN), ev = meta.y;
                     float2 w2;  // a wide block's
                     if (kWide && wide) {
                         w2 = pp_wide<N>(t_s, sm + Z::kCols, cq, c0, c1, m);

@@ -150,3 +150,17 @@ def test_values_spread_over_many_powers(d):
     bt = Batch(32, [(60, 500), (1, 700), (140, 140)], 4, 2, d, 32, 4, 4,
                norm=lambda r, n: np.exp(3 * r.standard_normal(n)))
     compare(bt, 0.002)
+
+
+@pytest.mark.parametrize("lens", [[(40, 200), (1, 70)], [(150, 300)]])
+@pytest.mark.parametrize("d", [32, 128, 256])
+@pytest.mark.parametrize("scale", [0.1, -0.1, 1e-38])
+def test_scores_below_the_smallest_number_are_zero(scale, d, lens):
+    """Tiny queries over tiny keys: the product of their powers of two is no fp32 number, and all
+    that a token attends to has the same weight."""
+    bt = Batch(33, lens, 4, 2, d, 64, 4, 4, qmul=2.0 ** -70)
+    for b, (_, c) in enumerate(lens):
+        for h in range(2):
+            for pos in range(c):
+                bt.set_norm(b, "k", h, pos, 2.0 ** -85)
+    compare(bt, scale)
