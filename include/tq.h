@@ -350,7 +350,9 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
  * rows are not written) and sets the device status word to 71.  A page id
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and
- * the device status word is set to 72.  73: a bounded wait gave up.
+ * the device status word is set to 72 (entries of pages wholly in front of the
+ * window of a sequence's first token are not looked at).  73: a bounded wait
+ * gave up.
  * workspace: tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte
  * aligned like q, out and every array of the cache; calls that overlap on the
  * GPU need one each.

@@ -225,7 +225,7 @@ struct PpPart {
     int row0, rows;      // first row within (sequence, KV head); valid rows
     int lo_blk;          // first block of the item
     int blk0, blk1, nblk;
-    int kv_end;
+    int kv_lo, kv_end;   // the positions that some row attends to
     int pair;            // the two streams take two row tiles
     bool head, whole;    // part starts the item; covers it
 };
@@ -240,16 +240,17 @@ __device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w, int64_t 
                     : off <= over ? 0 : min(nblk, (int)((float)nblk * __fdividef((float)(off - over), (float)(w - over))));
 }
 
-// Blocks of row tile i, the first of them, and the end of its positions.
+// Blocks of row tile i, the first of them, and its first position and their end.
 template <int D>
 __device__ __forceinline__ int pp_blocks(const PpArgs& A, const PpSeq<D>& q, int i, int* lo_blk = nullptr,
-                                         int* kv_end = nullptr) {
+                                         int* kv_lo = nullptr, int* kv_end = nullptr) {
     using Z = PpGeo<D>;
     const int row0 = i * Z::kRows, rows = min(Z::kRows, q.rows - row0);
     const int first_pos = q.ctx - q.n + row0 / q.G;
     const int end = max(0, q.ctx - q.n + (row0 + rows - 1) / q.G + 1);
-    const int lo = (A.window > 0 ? max(0, first_pos - A.window + 1) : 0) / Z::kN;
+    const int at = A.window > 0 ? max(0, first_pos - A.window + 1) : 0, lo = at / Z::kN;
     if (lo_blk) *lo_blk = lo;
+    if (kv_lo) *kv_lo = at;
     if (kv_end) *kv_end = end;
     return max(0, (end + Z::kN - 1) / Z::kN - lo);
 }
@@ -261,7 +262,7 @@ __device__ __forceinline__ void pp_rows(const PpArgs& A, const PpSeq<D>& q, PpPa
     p.row0 = p.i * Z::kRows;
     p.rows = min(Z::kRows, q.rows - p.row0);
     p.pair = Z::kStreams == 2 && p.rows > 128;
-    p.nblk = pp_blocks<D>(A, q, p.i, &p.lo_blk, &p.kv_end);
+    p.nblk = pp_blocks<D>(A, q, p.i, &p.lo_blk, &p.kv_lo, &p.kv_end);
 }
 
 // The share's next part with work in it; advances the cursor.  False at the
@@ -312,10 +313,9 @@ struct PpJob {
     int h;         // KV head
     int row0, rows;  // first row within (sequence, KV head); valid rows
     int blk;       // first block
-    int kv_end;    // positions at or past it are not read
+    int kv_lo, kv_end;  // positions before the one and from the other on are not read
     int pos0;      // position of the sequence's token 0
     int tok0, rest;  // row0 / G and row0 % G
-    int pad;
 };
 enum { kJobPair = 1, kJobWhole = 2, kJobHead = 4 };
 
@@ -694,10 +694,11 @@ __device__ __forceinline__ int pp_exponent(uint32_t m) { return min(100, max(-10
 // The factors of a wide block (norms kn and, behind them, vn), and its
 // positions' powers of two.
 template <int N>
-__device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint32_t segs, int lim, int seg_sh) {
+__device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint32_t segs, int from, int lim,
+                                           int seg_sh) {
 #pragma unroll 1
     for (int r = threadIdx.x & 31; r < N; r += 32) {
-        const bool in = r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+        const bool in = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
         const float k = in ? kn[r] : 0.f, v = in ? kn[N + r] : 0.f;
         const int ek = pp_exponent(pp_finite(k)), ev = pp_exponent(pp_finite(v));
         kn[r] = fmaf(v, 0.f, k * pp_pow2(-ek));  // NaN if either norm is not finite
@@ -916,6 +917,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         p.row0 = m->row0;
         p.rows = m->rows;
         p.blk = m->blk;
+        p.kv_lo = m->kv_lo;
         p.kv_end = m->kv_end;
         p.pos0 = m->pos0;
         p.tok0 = m->tok0;
@@ -970,6 +972,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     m->row0 = u.row0;
                     m->rows = u.rows;
                     m->blk = u.lo_blk + u.blk0;
+                    m->kv_lo = u.kv_lo;
                     m->kv_end = u.kv_end;
                     m->pos0 = seq.ctx - seq.n;
                     const int tok0 = u.row0 / seq.G;
@@ -984,7 +987,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             // this lane's segment of block j: its page, or -1; looked up a block ahead
             auto page_of = [&](int j) {
                 const int pos = (u.lo_blk + j) * N + s * seg;
-                return s < nseg && j < u.blk1 && pos < u.kv_end
+                return s < nseg && j < u.blk1 && pos < u.kv_end && pos + seg > u.kv_lo
                            ? A.bt[(int64_t)u.b * A.max_pages + (pos >> A.shift)]
                            : INT_MIN;
             };
@@ -1147,7 +1150,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 ok = __all_sync(0xFFFFFFFFu, pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status));
                 if (!ok) break;
                 const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
-                const int lim = p.kv_end - (p.blk + j) * N;  // the block's positions below it count
+                const int t0 = (p.blk + j) * N, from = p.kv_lo - t0, lim = p.kv_end - t0;  // the block's positions that count
                 const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
                 float kn[N / 32], vn[N / 32];
                 // the largest finite norms, as bits
@@ -1155,7 +1158,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
                     const int r = 32 * k + lane;
-                    const bool in = r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+                    const bool in = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
                     kn[k] = in ? knp[r] : 0.f;
                     vn[k] = in ? vnp[r] : 0.f;
                     const uint32_t x = pp_finite(kn[k]), y = pp_finite(vn[k]);
@@ -1185,7 +1188,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     if (wides) ok = __all_sync(0xFFFFFFFFu, pp_wait(cols_free, (wides - 1) & 1, abort_f, status));
                     if (!ok) break;
                     ++wides;
-                    pp_wide_norms<N>(knp, sm + Z::kCols, segs, lim, seg_sh);
+                    pp_wide_norms<N>(knp, sm + Z::kCols, segs, from, lim, seg_sh);
                 }
                 __syncwarp();
                 if (lane == 0) {

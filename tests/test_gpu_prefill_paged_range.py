@@ -164,3 +164,28 @@ def test_scores_below_the_smallest_number_are_zero(scale, d, lens):
             for pos in range(c):
                 bt.set_norm(b, "k", h, pos, 2.0 ** -85)
     compare(bt, scale)
+
+
+@pytest.mark.parametrize("entry", ["gone", "another's"])
+@pytest.mark.parametrize("page,window", [(32, 1), (32, 40), (64, 100), (256, 300)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pages_in_front_of_the_window_are_not_read(d, page, window, entry):
+    """A cache that keeps only a window's pages has given the ones before it back: their entries are
+    -1, or hold rows of something else."""
+    lens = [(1, 500), (40, 700), (300, 1000), (3, 3)]
+    bt = Batch(34, lens, 4, 2, d, page, 4, 3)
+    want, tol = reference(bt, 0.1, window)
+    for b, (n, c) in enumerate(lens):
+        for j in range(max(0, c - n - window + 1) // page):
+            if entry == "gone":
+                bt.bt_host[b, j] = -1
+            else:
+                for a in ("kn", "vn"):
+                    bt.arrays[a][bt.bt_host[b, j]] = 2.0 ** 60
+    out = abi.tq_attn_prefill_paged(*bt.gpu(), 0.1, window=window, out_dtype=torch.float32)
+    assert abi.tq_device_status(reset=True) == 0
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    if entry == "gone":  # the same bits as with the pages there
+        full = abi.tq_attn_prefill_paged(*Batch(34, lens, 4, 2, d, page, 4, 3).gpu(), 0.1, window=window,
+                                         out_dtype=torch.float32)
+        assert torch.equal(out, full)
