@@ -72,8 +72,9 @@
 //
 // Every wait on an mbarrier is bounded (2 s); one that gives up sets the
 // device status word and a flag that ends the others.  The softmax warps go
-// on through their (then failing) waits so that their barriers stay paired;
-// no output is written after the flag.
+// on through their (then failing) waits so that their barriers stay paired.  No
+// output is written after the flag, and the join leaves out every item that a
+// share with the flag may have had a part of.
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -151,8 +152,10 @@ struct PpArgs {
 };
 // what a share left: bit 0 a part of the item it starts in, bit 1 one of the
 // item it owns (which starts in this share and ends in the share kMetaLast;
-// -1: none), that item's first row of q, KV head, rows
+// -1: none), that item's first row of q, KV head, rows.  kShareFailed: a wait
+// gave up in the share, and its parts may be missing
 enum { kMetaHas = 0, kMetaLast, kMetaQ0, kMetaH, kMetaRow0, kMetaRows, kPpMeta = 8 };
+constexpr int kShareFailed = 4;
 
 // Where a share starts or goes on: sequence, row tile, KV head, and the units
 // (or, where the share is one part of an item, the parts) of the item that
@@ -745,7 +748,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         if (tid == 0) {
             report_timeout(status, kPpStatusAlign);
             griddep_wait();
-            *reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta) = make_int4(0, -1, 0, 0);
+            *reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta) = make_int4(kShareFailed, -1, 0, 0);
         }
         return;
     }
@@ -1617,6 +1620,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     griddep_launch();
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && *abort_f)  // over what the copy warp wrote
+        *reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta) = make_int4(kShareFailed, -1, 0, 0);
     if (warp == SW + DW) {
         tc_fence_after();
         tmem_dealloc<512>(tmem);
@@ -1652,6 +1657,7 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
         const int cl = c0 + lane;
         if (c0 > sh && cl <= last) near = __ldcg(A.meta + cl * kPpMeta + kMetaHas);
         unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && (near & (cl == sh ? 2 : 1)));
+        if (__any_sync(0xFFFFFFFFu, cl <= last && (near & kShareFailed))) return;  // every warp sees the same
         while (has && in) {
             // a few parts' loads in flight at once
             float4 v[AT][C];
