@@ -977,8 +977,7 @@ tq_status pages_call(int op, tq_page_table in, tq_page_table out, const int32_t*
         !aligned4(out.lens) || !aligned4(out.refs) || !aligned4(info) || !aligned4(arg) || !aligned4(moved))
         return TQ_ERR_ALIGNMENT;
     const int shift = page_shift_of(layers[0].page_size);
-    // lengths are int32; a row's place among the copied pages has 23 bits, and rows that
-    // go on in one shared page are counted one after the other
+    // lengths are int32, and a row's place among the copied pages has 23 bits
     if (((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows) return TQ_ERR_UNSUPPORTED;
     const int64_t n_pages = layers[0].n_pages;
     if (!workspace || workspace_bytes < tq::pages_workspace_bytes(n_seqs, n_pages)) return TQ_ERR_WORKSPACE;

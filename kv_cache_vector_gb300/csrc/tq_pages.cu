@@ -47,8 +47,8 @@ struct PagesWs {
     int32_t* delta;  // [n_pages] change of the holders (copy: first pair per destination; compact: holders of movers)
     int32_t* cow;    // [n_pages] fork, resize: holders lost to private copies (copy: page is a source)
     int32_t* fresh;  // [n_pages] free pages, ascending (compact: holes)
-    int32_t* src;    // [n_pages] pairs: source page, or -1 for none
-    int32_t* dst;    // [n_pages] pairs: destination page
+    int32_t* src;    // [n_pages] pairs: source page, or -1 for none (resize, first: rows that write into the page)
+    int32_t* dst;    // [n_pages] pairs: destination page (resize, first: the last such row)
     int32_t* first;  // [n_seqs] fork: first child of a row; resize: the tail page the row writes into, or -1
     int32_t* start;  // [n_seqs] the row's place in the list of fresh pages
     int32_t* pair;   // [n_seqs] the row's place in the list of pairs; bit 31: it has one
@@ -176,6 +176,10 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
         for (int p = gt; p < N; p += GT) {
             W.delta[p] = OP == kOpCopy ? INT_MAX : 0;
             W.cow[p] = 0;
+            if constexpr (OP == kOpResize) {
+                W.src[p] = 0;
+                W.dst[p] = -1;
+            }
         }
     if constexpr (OP == kOpFork)
         for (int i = gt; i < A.n_seqs; i += GT) W.first[i] = INT_MAX;
@@ -262,15 +266,19 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
                     const bool writes = len > old && (old & (ps - 1)) != 0;
                     const int tail = writes ? row[had - 1] : -1;
                     W.first[i] = in_range(tail) ? tail : -1;
+                    if (in_range(tail)) {
+                        atomicAdd(&W.src[tail], 1);
+                        atomicMax(&W.dst[tail], i);
+                    }
                 }
             }
         }
         cl.sync();
         if constexpr (OP == kOpResize) {
             // in row order, a row whose last page has other holders takes a
-            // private copy of it: of k such rows on a page with r holders, the
-            // first min(k, r - 1) do
-            for (int i = gw; i < A.n_seqs; i += GW) {
+            // private copy of it: of k such rows on a page with r >= k holders,
+            // all but the last if k = r, else all
+            for (int i = gt; i < A.n_seqs; i += GT) {
                 const int old = clamp_len(A.lens[i]);
                 const int len = A.arg[i] < 0 ? old : clamp_len(A.arg[i]);
                 const int more = pages_of(len) - pages_of(old);
@@ -278,18 +286,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_pages_plan(const PagesPlan A,
                 int own = 0;
                 if (tail >= 0) {
                     const int r = A.refs[tail] + W.delta[tail];
-                    if (r > 1) {
-                        int before = 0;
-#pragma unroll 8
-                        for (int j = lane; j < i; j += 32) before += W.first[j] == tail;
-                        own = r - (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)before) > 1;
-                    }
-                }
-                if (lane == 0) {
+                    own = r > 1 && (W.src[tail] < r || W.dst[tail] != i);
                     if (own) atomicAdd(&W.cow[tail], 1);
-                    W.start[i] = own + (more > 0 ? more : 0);
-                    W.pair[i] = own;
                 }
+                W.start[i] = own + (more > 0 ? more : 0);
+                W.pair[i] = own;
             }
             cl.sync();
         }

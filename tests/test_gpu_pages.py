@@ -352,3 +352,43 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
         check_books(t, info, want)
         books = want[:3]
+
+
+@pytest.mark.parametrize("n,holders", [(1 << 17, 0), (40000, 3), (257, 0), (257, 1)])
+def test_many_rows_go_on_in_one_shared_page(n, holders):
+    """All rows are branches of one prompt: all but the last take a private copy (all of them where
+    something else holds the page too), in a time that grows with the rows, not with their square."""
+    page, N = 32, n + 9
+    pool = make_pool(17, N, L=1, Hkv=1, d=32, kb=2, vb=2)
+    table, lens, refs = np.full((n, 3), -1, np.int32), np.full(n, 40, np.int32), np.zeros(N, np.int32)
+    table[:, 0], table[:, 1] = 4, 2
+    refs[4], refs[2] = n, n + holders
+    to = np.full(n, 41, np.int32)
+    to[5::7] = -1                              # some stay as they are
+    want = OP.resize(table, lens, refs, to, page)
+    grows = int((to > 0).sum())
+    assert want[-1] == (min(grows, n + holders - 1), 0)
+    before, t, new = contents(pool), on_gpu(table, lens, refs), torch.from_numpy(to).cuda()
+    out, info = abi.tq_pages_resize(t, new, pool)
+    check_books(out, info, want)
+    check_contents(pool, before, want[3])
+    assert abi.tq_device_status(reset=True) == 0
+    alone = table.copy()                       # the same rows with last pages of their own
+    alone[:, 1] = np.delete(np.arange(n + 1), 4)
+    refs2 = np.zeros(N, np.int32)
+    refs2[:n + 1] = 1
+    refs2[4] = n
+    t2, ws = on_gpu(alone, lens, refs2), torch.empty(abi.tq_pages_workspace_bytes(n, 3, N), dtype=torch.uint8, device="cuda")
+
+    def ms(table):
+        best = 1e9
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            abi.tq_pages_resize(table, new, pool, out=out, workspace=ws)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert ms(t) <= 4 * ms(t2) + 1.0
