@@ -572,7 +572,7 @@ class PagedLayers:
 class PageTable:
     """The books of a paged cache's pages (caller-owned device tensors, int32),
     and what the last call that wrote them said, unless it was given a tensor
-    for that (made at the first such call)."""
+    for that: a tensor of that call alone, on its stream."""
     block_table: torch.Tensor  # [n_seqs, max_pages]: page ids, -1 past a row's pages
     lens: torch.Tensor         # [n_seqs]: positions in use
     refs: torch.Tensor         # [n_pages]: holders of a page, 0 for a free one
@@ -669,6 +669,21 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
             _raw_stream(dst.device)))
 
 
+_FRESH: dict = {}  # per device, stream and length: int32 tensors that no call has had yet
+
+
+def _fresh(device, stream, n):
+    """A new int32 tensor [n], several to an allocation (one costs more than half
+    of a small call); in a capture one of the graph's own memory."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(n, dtype=_INT32, device=device)
+    free = _FRESH.get((device.index, stream, n))
+    if not free:
+        _FRESH[device.index, stream, n] = free = list(
+            torch.empty(max(1, min(64, 65536 // n)), n, dtype=_INT32, device=device).unbind())
+    return free.pop()
+
+
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
     layers = _layers(layers)
     shape = table.block_table.shape
@@ -680,14 +695,11 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         if out is None:
             out = PageTable(*(torch.empty_like(t) for t in (table.block_table, table.lens, table.refs)))
         a, b = table._view(layers, shape), out._view(layers, shape)
-        if info is None:
-            if out.info is None:
-                out.info = out.lens.new_empty(2)
-            info = out.info
-        if arg is None and moved is None:
-            if out.moved_to is None:
-                out.moved_to = out.refs.new_empty(layers.n_pages)
-            moved = out.moved_to
+        stream = _raw_stream(dev)
+        says, info = info is None, _fresh(dev, stream, 2) if info is None else info
+        says_moved = arg is None and moved is None
+        if says_moved:
+            moved = _fresh(dev, stream, layers.n_pages)
         other = moved if arg is None else arg
         _ints(dev, info, other)
         if info.numel() != 2 or other.numel() != (layers.n_pages if arg is None else n_seqs):
@@ -695,7 +707,11 @@ def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
         ws = _scratch(workspace, dev, tq_pages_workspace_bytes, n_seqs, max_pages, layers.n_pages)
         middle = (a, b, other.data_ptr()) if arg is None else (a, other.data_ptr(), b)
         _check(fn, getattr(lib(), fn)(*middle, n_seqs, max_pages, layers.views, len(layers.views), *layers.args,
-                                      info.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
+                                      info.data_ptr(), ws.data_ptr(), ws.nbytes, stream))
+        if says:
+            out.info = info
+        if says_moved:
+            out.moved_to = moved
     return (out, info) if arg is not None else (out, moved, info)
 
 
@@ -704,7 +720,7 @@ def tq_pages_fork(table: PageTable, parents: torch.Tensor, layers, out: PageTabl
     """Row i of the result is row parents[i] of `table` (int32; -1: empty):
     full pages shared, a partly filled last page copied for all children but
     one.  Returns (table, info [2]: pages taken, pages missing); without
-    `info`, the table's own, which the next call on it writes again."""
+    `info`, a new tensor, which the table keeps as its own."""
     return _pages("tq_pages_fork", table, parents, layers, out, None, info, workspace)
 
 
@@ -722,8 +738,7 @@ def tq_pages_compact(table: PageTable, layers, out: PageTable | None = None, mov
                      info: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The held pages moved to the lowest ids.  `out` may be `table`.  Returns
     (table, moved_to [n_pages]: each page's new id or -1, info [2]: pages
-    held, pages moved); without moved_to and info, the table's own, as of
-    tq_pages_fork."""
+    held, pages moved); moved_to and info as of tq_pages_fork."""
     return _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
 
 

@@ -392,3 +392,36 @@ def test_many_rows_go_on_in_one_shared_page(n, holders):
         return best
 
     assert ms(t) <= 4 * ms(t2) + 1.0
+
+
+def test_what_a_call_said_is_not_written_again():
+    """Steps of a loop in place: what each said stays as it was, on whichever stream it is read, and
+    in a graph of several steps too."""
+    page, N = 32, 12
+    pool = make_pool(18, N)
+    t = on_gpu(np.full((2, 4), -1, np.int32), np.zeros(2, np.int32), np.zeros(N, np.int32))
+    grow = lambda *k: torch.tensor(k, dtype=torch.int32).cuda()  # noqa: E731
+    said = []
+    for step in (grow(40, 10), grow(100, 0), grow(128, 128), grow(0, 0)):
+        said.append(abi.tq_pages_resize(t, step, pool, out=t)[1])
+        assert t.info is said[-1]
+    moved = [abi.tq_pages_compact(t, pool, out=t)[1:]]
+    abi.tq_pages_resize(t, grow(60, 60), pool, out=t)
+    moved.append(abi.tq_pages_compact(t, pool, out=t)[1:])
+    assert [x.tolist() for x in said] == [[3, 0], [2, 0], [4, 0], [0, 0]]
+    assert moved[0][1].tolist() == [0, 0] and (moved[0][0] == -1).all()
+    assert moved[1][1].tolist() == [4, 0] and moved[1][0].tolist() == [0, 1, 2, 3] + [-1] * 8
+    assert t.moved_to is moved[1][0] and t.info is moved[1][1]
+    # captured: each step of the graph has its own, and a call outside of it another
+    abi.tq_pages_resize(t, grow(0, 0), pool, out=t)
+    a, b = grow(40, 10), grow(100, 0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        i1 = abi.tq_pages_resize(t, a, pool, out=t)[1]
+        i2 = abi.tq_pages_resize(t, b, pool, out=t)[1]
+    g.replay()
+    torch.cuda.synchronize()
+    assert i1.tolist() == [3, 0] and i2.tolist() == [2, 0]
+    abi.tq_pages_resize(t, grow(0, 0), pool, out=t)
+    assert i1.tolist() == [3, 0] and i2.tolist() == [2, 0] and t.info.tolist() == [0, 0]
