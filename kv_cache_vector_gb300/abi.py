@@ -539,7 +539,8 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
 
 class PagedLayers:
     """The layers of one pool: paged caches of one geometry that share a block
-    table.  Holds their addresses, so that a call passes them as they are."""
+    table.  Holds their tensors with the addresses, so that a call passes them
+    as they are; a cache that is given other tensors needs new PagedLayers."""
 
     def __init__(self, layers):
         layers = [layers] if isinstance(layers, PagedCache) else list(layers)
@@ -557,7 +558,9 @@ class PagedLayers:
             if (x.k_packed.shape, x.v_packed.shape, x.k_norm.shape, x.v_norm.shape, x.k_bits, x.v_bits) != \
                     (c.k_packed.shape, c.v_packed.shape, c.k_norm.shape, c.k_norm.shape, c.k_bits, c.v_bits):
                 raise ValueError("the layers must have one geometry")
-        self.layers = layers  # keeps the tensors alive
+        self.layers = layers
+        # the tensors themselves: a PagedCache may be given others
+        self._tensors = [(x.k_packed, x.k_norm, x.v_packed, x.v_norm) for x in layers]
         self.k_bits, self.v_bits, self.device = c.k_bits, c.v_bits, c.k_norm.device
         self.n_pages, self.Hkv, self.page_size = c.k_norm.shape
         self.d = c.k_packed.shape[-1] * 8 // c.k_bits

@@ -425,3 +425,19 @@ def test_what_a_call_said_is_not_written_again():
     assert i1.tolist() == [3, 0] and i2.tolist() == [2, 0]
     abi.tq_pages_resize(t, grow(0, 0), pool, out=t)
     assert i1.tolist() == [3, 0] and i2.tolist() == [2, 0] and t.info.tolist() == [0, 0]
+
+
+def test_layers_keep_the_tensors_whose_addresses_they_pass():
+    """A PagedCache may get other tensors later: the pool's calls go on with the ones that it was made of."""
+    import gc
+    import weakref
+    c = abi.PagedCache.empty(12, 1, 32, 64, 4, 3)
+    c.k_packed.copy_(torch.arange(12, dtype=torch.uint8).view(12, 1, 1, 1).expand_as(c.k_packed))
+    pool, was = abi.PagedLayers(c), c.k_packed.data_ptr()
+    kept = [weakref.ref(t) for t in (c.k_packed, c.k_norm, c.v_packed, c.v_norm)]
+    c.k_packed, c.k_norm, c.v_packed, c.v_norm = (torch.zeros_like(t) for t in (c.k_packed, c.k_norm, c.v_packed, c.v_norm))
+    gc.collect()
+    assert all(k() is not None for k in kept) and kept[0]().data_ptr() == was
+    ids = lambda *k: torch.tensor(k, dtype=torch.int32).cuda()  # noqa: E731
+    abi.tq_pages_copy(pool, pool, ids(3), ids(7))
+    assert (kept[0]()[7] == 3).all() and not c.k_packed.any()
