@@ -395,8 +395,8 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
  * Where refs counts fewer holders than the rows have, the results are not
  * specified (no access leaves its array).
  * Alignment: 16 bytes for every cache array (norms too) and the workspace, 4
- * for the books.  d is a power of two in [32, 256]; n_pages < 2^31; n_seqs in
- * [1, 2^18].
+ * for the books.  d is a power of two in [32, 256]; n_pages <= 2^30; n_seqs in
+ * [1, 2^18]; a page of one layer at most 2 GB with four bits.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, bits, page_size),
  * TQ_ERR_ALIGNMENT, TQ_ERR_WORKSPACE. */
 typedef struct {

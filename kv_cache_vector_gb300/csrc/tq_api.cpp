@@ -882,10 +882,11 @@ tq_status tq_attn_decode_append_paged(const tq_plan* plan, const void* q, const 
 
 // ------------------------------------------------------------ upkeep of the pages
 
-static constexpr int kMaxRows = 1 << 18;  // of a page table
+static constexpr int kMaxRows = 1 << 18;       // of a page table
+static constexpr int64_t kMaxPages = 1 << 30;  // of a pool: a page number plus a loop's step stays in 32 bits
 
 size_t tq_pages_workspace_bytes(int n_seqs, int max_pages, int64_t n_pages) {
-    if (n_seqs < 0 || n_seqs > kMaxRows || max_pages < 0 || n_pages < 1 || n_pages > INT32_MAX) return 0;
+    if (n_seqs < 0 || n_seqs > kMaxRows || max_pages < 0 || n_pages < 1 || n_pages > kMaxPages) return 0;
     return tq::pages_workspace_bytes(n_seqs, n_pages);
 }
 
@@ -902,9 +903,9 @@ tq_status check_layers(const tq_paged_cache* layers, int n_layers, int Hkv, int 
     if (!valid_bits(k_bits) || !valid_bits(v_bits) || d < 32 || d > tq::kMaxD || !is_pow2(d)) return TQ_ERR_UNSUPPORTED;
     const int shift = page_shift_of(layers[0].page_size);
     if (shift < 0) return TQ_ERR_UNSUPPORTED;
-    if (layers[0].n_pages < 1 || layers[0].n_pages > INT32_MAX) return TQ_ERR_INVALID_ARG;
-    // a page's 16-byte words are counted in 32 bits
-    if (((int64_t)Hkv << shift) * (d / 2 + 8) * 2 > (int64_t(1) << 31)) return TQ_ERR_UNSUPPORTED;
+    if (layers[0].n_pages < 1 || layers[0].n_pages > kMaxPages) return TQ_ERR_INVALID_ARG;
+    // a page's 16-byte words are counted in 32 bits (and Hkv << shift times the bytes may leave 64)
+    if (Hkv > (int64_t(1) << 31) / (d + 16) >> shift) return TQ_ERR_UNSUPPORTED;
     for (int l = 0; l < n_layers; ++l) {
         const tq_paged_cache& c = layers[l];
         if (c.n_pages != layers[0].n_pages || c.page_size != layers[0].page_size || !paged_pointers_ok(c))

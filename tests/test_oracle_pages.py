@@ -243,3 +243,32 @@ def test_prefill_paged_python_refusals():
         call(q=q.float())
     with pytest.raises(TypeError):
         call(abi.PagedCache(good.k_packed, good.k_norm.half(), good.v_packed, good.v_norm, 4, 3))
+
+
+def test_pages_and_pools_past_the_kernels_counters_are_refused(L):
+    """Sizes whose products leave 64 bits, and pools whose page numbers leave 32 bits in a loop's step."""
+    A, W = 1 << 20, 1 << 28
+    tab = lambda a: abi.PageTableView(a, a + 4096, a + 8192)  # noqa: E731
+
+    def fork(cache, hkv, d=128, kb=4, vb=3):
+        return L.tq_pages_fork(tab(A), A + (1 << 18), tab(A + (1 << 16)), 4, 1, _layers(cache), 1, hkv, d, kb, vb,
+                               A + (1 << 19), W, 64, None)
+
+    def copy(cache, hkv, d=128):
+        return L.tq_pages_copy(_layers(cache), _layers(cache), 1, hkv, d, 4, 3, A, A + 4096, 0, None, 0, None)
+
+    for hkv, page in ((1 << 30, 1 << 30), ((1 << 31) - 1, 1 << 30), (1 << 29, 1 << 30), (1 << 24, 1 << 5), (1, 1 << 24)):
+        for d in (32, 64, 128, 256):
+            if hkv * page * (d + 16) <= 1 << 31:
+                continue
+            assert fork(_cache(page_size=page), hkv, d) == 2, (hkv, page, d)
+            assert copy(_cache(page_size=page), hkv, d) == 2, (hkv, page, d)
+    assert copy(_cache(page_size=64), 8) == 0
+    # the largest page of 32-bit counters passes, a size further does not
+    most = (1 << 31) // ((128 + 16) * 64)
+    assert copy(_cache(page_size=64), most) == 0 and copy(_cache(page_size=64), most + 1) == 2
+    for n in ((1 << 30) + 1, (1 << 31) - 8000, (1 << 31) - 1):
+        assert fork(_cache(n_pages=n), 2) == 1
+        assert copy(_cache(n_pages=n), 2) == 1
+        assert L.tq_pages_workspace_bytes(4, 8, n) == 0
+    assert L.tq_pages_workspace_bytes(4, 8, 1 << 30) > 0 and copy(_cache(n_pages=1 << 30), 2) == 0
