@@ -332,7 +332,9 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
 /* Attention of several query tokens per sequence over a paged cache: prompt
  * chunks, drafted tokens to be checked, and single tokens, ragged in one batch
  * ("TurboQuant KV Cache Compression -- Spec", fa_tq_attention_cached;
- * Optimization: Fused dequant-dot).  Sequence b's n_b = cu_q[b + 1] - cu_q[b]
+ * Optimization: Fused dequant-dot).  For a step of one token per sequence and no
+ * more, tq_attn_decode_paged reads long contexts twice as fast and is more exact.
+ * Sequence b's n_b = cu_q[b + 1] - cu_q[b]
  * query tokens are the last n_b of its ctx_lens[b] positions (their K and V
  * rows are in the cache already): token t sits at p = ctx_lens[b] - n_b + t
  * and attends over positions max(0, p - window + 1) .. p (window 0: 0 .. p).
@@ -347,6 +349,12 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * 2^100, in any order (smaller ones lose bits; blocks of 128 positions whose K
  * norms are more than 2^15 or V norms more than 2^10 apart take longer).
  * Positions outside a row's range do not reach it, whatever their rows hold.
+ * Accuracy, whichever type the output has: with S_j = scale |q| |k_j| / sqrt(d)
+ * a row is off by at most 6 * 2^-10 / sqrt(3) * sum_j p_j (S_j |v_j - out| +
+ * |v_j| / sqrt(d)) per element (six standard deviations of its roundings): about
+ * 1e-3 of ordinary values, but up to 0.07 on rows with outlier channels and
+ * values up to 28, where tq_attn_decode_paged and tq_attn_prefill, which carry
+ * their operands in two parts, hold 2e-3.  |q| below 2^120.
  * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
  * rows are not written) and sets the device status word to 71.  A page id
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and

@@ -18,7 +18,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cache_vector_gb300 import abi
+from kv_cache_vector_gb300 import abi, synth
+from oracle import oracle as O
 from test_gpu_prefill_paged import SIGMA, Batch
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +190,34 @@ def test_pages_in_front_of_the_window_are_not_read(d, page, window, entry):
         full = abi.tq_attn_prefill_paged(*Batch(34, lens, 4, 2, d, page, 4, 3).gpu(), 0.1, window=window,
                                          out_dtype=torch.float32)
         assert torch.equal(out, full)
+
+
+def set_rows(bt, b, k, v):
+    """Sequence b's positions hold the rows k and v [Hkv, positions, d]."""
+    pos, page = np.arange(bt.lens[b][1]), bt.page
+    pg, off, hh = bt.bt_host[b, pos // page][:, None], (pos % page)[:, None], np.arange(bt.Hkv)[None]
+    enc = []
+    for x, bits in ((k, bt.kb), (v, bt.vb)):
+        p, n = O.encode(bt.s, bits, x.reshape(-1, bt.d), s2=bt.s2, kind=bt.kind)
+        enc += [p.reshape(bt.Hkv, len(pos), -1), n.reshape(bt.Hkv, len(pos))]
+    bt.rows[b] = enc
+    for a, src in zip(("kp", "kn", "vp", "vn"), enc):
+        bt.arrays[a][pg, hh, off] = src.swapaxes(0, 1)
+
+
+@pytest.mark.parametrize("d,kb,vb", [(64, 4, 4), (128, 4, 3), (256, 4, 4)])
+def test_rows_with_outlier_channels(d, kb, vb):
+    """Correlated rows with a few channels eight times as large: sharp softmaxes over large values,
+    where the fp16 operands show most.  The decode attention of the same tokens is closer."""
+    lens = [(120, 120), (40, 700)]
+    bt = Batch(35, lens, 8, 2, d, 64, kb, vb)
+    for b, (_, c) in enumerate(lens):
+        set_rows(bt, b, *(np.stack([synth.lowrank_rows(40 + which, c, d, stream=10 * b + h).double().numpy()
+                                    for h in range(2)]) for which in (0, 1)))
+    bt.q = torch.stack([synth.lowrank_rows(42, 160, d, stream=h) for h in range(8)], 1)
+    got, want, _ = compare(bt, 1 / math.sqrt(d))
+    assert np.abs(want).max() > 10
+    plan, q, _, cache, table, ctx = bt.gpu()
+    last = torch.tensor([119, 159]).cuda()
+    one = abi.tq_attn_decode_paged(plan, q[last].contiguous(), cache, table, ctx, 700, 1 / math.sqrt(d))
+    assert np.abs(one.double().cpu().numpy() - want[[119, 159]]).max() <= 2e-3
