@@ -334,10 +334,10 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * ("TurboQuant KV Cache Compression -- Spec", fa_tq_attention_cached;
  * Optimization: Fused dequant-dot).  For a step of one token per sequence and no
  * more, tq_attn_decode_paged reads long contexts twice as fast and is more exact.
- * Sequence b's n_b = cu_q[b + 1] - cu_q[b]
- * query tokens are the last n_b of its ctx_lens[b] positions (their K and V
- * rows are in the cache already): token t sits at p = ctx_lens[b] - n_b + t
- * and attends over positions max(0, p - window + 1) .. p (window 0: 0 .. p).
+ * Sequence b's n_b = cu_q[b + 1] - cu_q[b] query tokens are the last n_b of its
+ * ctx_lens[b] positions (their K and V rows are in the cache already): token t
+ * sits at p = ctx_lens[b] - n_b + t and attends over positions
+ * max(0, p - window + 1) .. p (window 0: 0 .. p).
  * A token with p < 0 attends to nothing and gets a zero row.
  *   q:   [n_q][Hq][d] bf16, device;  out: [n_q][Hq][d] out_dtype, device
  *   cu_q: [B + 1] int32, device, ascending from cu_q[0] >= 0 to cu_q[B] <= n_q;
@@ -354,7 +354,7 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * |v_j| / sqrt(d)) per element (six standard deviations of its roundings): about
  * 1e-3 of ordinary values, but up to 0.07 on rows with outlier channels and
  * values up to 28, where tq_attn_decode_paged and tq_attn_prefill, which carry
- * their operands in two parts, hold 2e-3.  |q| below 2^120.
+ * their operands in two parts, hold 2e-3.  Elements of q below 2^100.
  * A sequence whose cu_q or ctx_lens entries are out of range is left out (its
  * rows are not written) and sets the device status word to 71.  A page id
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and

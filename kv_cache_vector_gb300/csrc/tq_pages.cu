@@ -671,11 +671,14 @@ static cudaError_t launch_copy(const PagesCall& c, int l0, int L, const CopySize
                       (const int32_t*)W.head, (const int32_t*)W.src, (const int32_t*)W.dst);
 }
 
-// One cluster suits every size: 8 CTAs once the books are long enough for the
-// barriers between more CTAs to cost less than they save.
+// One CTA, or a cluster of 8 once the books are long enough for the barriers
+// between CTAs to cost less than they save.  A resize, fork and compaction of
+// 4048 words of books took 9.1, 10.1 and 10.8 us with one CTA and 10.5, 11.6 and
+// 13.4 with 8; of 8096 words 13.1, 12.8 and 14.3 against 11.0, 11.5 and 14.7; of
+// 16,000 words 19.0, 18.0 and 21.0 against 11.4, 12.2 and 17.3.
 static int plan_ctas(const PagesPlan& A) {
     const int64_t words = (int64_t)A.n_pages + (int64_t)A.n_seqs * A.max_pages + A.n;
-    return words > 16384 ? kPgClusterMax : 1;
+    return words > 6144 ? kPgClusterMax : 1;
 }
 
 template <int OP>
