@@ -1,5 +1,6 @@
 // tq_api.cpp -- the C ABI: plan construction (codebooks, signs), argument
 // validation, and dispatch to the sm_103a kernels.  See include/tq.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -929,19 +930,15 @@ Span layer_span(const tq_paged_cache& c, int a, int Hkv, int d, int k_bits, int 
     return {reinterpret_cast<uintptr_t>(p), rows * (a == 0 ? d * k_bits / 8 : a == 2 ? d * v_bits / 8 : 4)};
 }
 
-// The arrays of n layers in the order of their addresses.  (Layers made one
-// after the other mostly are in it already.)
+// The arrays of n layers in the order of their addresses.
 int sorted_spans(const tq_paged_cache* layers, int n, int Hkv, int d, int k_bits, int v_bits, Span* out) {
-    for (int i = 0; i < 4 * n; ++i) {
-        const Span s = layer_span(layers[i >> 2], i & 3, Hkv, d, k_bits, v_bits);
-        int j = i;
-        for (; j > 0 && out[j - 1].at > s.at; --j) out[j] = out[j - 1];
-        out[j] = s;
-    }
+    for (int i = 0; i < 4 * n; ++i) out[i] = layer_span(layers[i >> 2], i & 3, Hkv, d, k_bits, v_bits);
+    std::sort(out, out + 4 * n, [](const Span& x, const Span& y) { return x.at < y.at; });
     return 4 * n;
 }
 
-// Do an array of a and one of b overlap?
+// Do an array of a and one of b overlap?  (Sorted 64 layers at a time and compared
+// group by group: past 64 layers the time grows with their square.)
 bool layers_overlap(const tq_paged_cache* a, const tq_paged_cache* b, int n, int Hkv, int d, int k_bits, int v_bits) {
     constexpr int kAt = 64;  // layers at a time
     Span x[4 * kAt], y[4 * kAt];
