@@ -680,11 +680,14 @@ def _fresh(device, stream, n):
     of a small call); in a capture one of the graph's own memory."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(n, dtype=_INT32, device=device)
-    free = _FRESH.get((device.index, stream, n))
-    if not free:
-        _FRESH[device.index, stream, n] = free = list(
-            torch.empty(max(1, min(64, 65536 // n)), n, dtype=_INT32, device=device).unbind())
-    return free.pop()
+    key = (device.index, stream, n)
+    try:
+        return _FRESH[key].pop()
+    except (KeyError, IndexError):  # none left, maybe since another thread took the last
+        new = list(torch.empty(max(1, min(64, 65536 // n)), n, dtype=_INT32, device=device).unbind())
+        first = new.pop()
+        _FRESH[key] = new
+        return first
 
 
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):

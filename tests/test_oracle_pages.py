@@ -272,3 +272,34 @@ def test_pages_and_pools_past_the_kernels_counters_are_refused(L):
         assert copy(_cache(n_pages=n), 2) == 1
         assert L.tq_pages_workspace_bytes(4, 8, n) == 0
     assert L.tq_pages_workspace_bytes(4, 8, 1 << 30) > 0 and copy(_cache(n_pages=1 << 30), 2) == 0
+
+
+def test_reported_values_from_many_threads(monkeypatch):
+    """No two calls get one tensor, and none finds the list empty that another thread emptied."""
+    import threading
+
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    monkeypatch.setattr(abi, "_FRESH", {})
+    dev, out, wrong = torch.device("cpu"), [], []
+
+    def take(n):
+        try:
+            for _ in range(700):
+                out.append(abi._fresh(dev, 0, n))
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=take, args=(n,)) for n in (2, 2, 2, 2, 5, 70000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and len({t.data_ptr() for t in out}) == len(out) == 6 * 700
+
+    class Emptied(list):  # between the look and the taking
+        def __bool__(self):
+            return True
+
+    abi._FRESH[dev.index, 0, 2] = Emptied()
+    assert abi._fresh(dev, 0, 2).shape == (2,)
