@@ -221,3 +221,29 @@ def test_rows_with_outlier_channels(d, kb, vb):
     last = torch.tensor([119, 159]).cuda()
     one = abi.tq_attn_decode_paged(plan, q[last].contiguous(), cache, table, ctx, 700, 1 / math.sqrt(d))
     assert np.abs(one.double().cpu().numpy() - want[[119, 159]]).max() <= 2e-3
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_seeded_sweep(seed):
+    """Lengths, heads, pages, windows, widths and spreads of norms drawn together; slots without a
+    position hold NaN norms, as in all of these batches."""
+    g = np.random.default_rng(1000 + seed)
+    d = int(g.choice([32, 64, 128, 256]))
+    Hkv, G = int(g.integers(1, 4)), int(g.choice([1, 2, 3, 5, 8]))
+    lens = []
+    for _ in range(int(g.integers(1, 6))):
+        n = int(g.choice([0, 1, 2, int(g.integers(1, 40)), int(g.integers(1, 150))]))
+        lens.append((n, max(0, n - int(g.integers(0, 3))) + int(g.choice([0, 1, 130, int(g.integers(0, 900))]))))
+    if not sum(n for n, _ in lens):
+        lens.append((3, 200))
+    window = int(g.choice([0, 0, 1, int(g.integers(1, 300)), 5000]))
+    bt = Batch(seed, lens, Hkv * G, Hkv, d, int(g.choice([32, 64, 128, 512])), int(g.integers(2, 5)),
+               int(g.integers(2, 5)), flags=int(g.integers(0, 4)))
+    ks, vs = (float(g.choice([0, 2, 9, 14, 30, 60])) for _ in range(2))
+    vbase = float(g.integers(-30, 30))
+    for b, (_, c) in enumerate(lens):
+        for h in range(Hkv):
+            for p in range(c):
+                bt.set_norm(b, "k", h, p, math.sqrt(d) * 2.0 ** -(g.random() * ks))
+                bt.set_norm(b, "v", h, p, 0.0 if g.random() < 0.05 else 2.0 ** (vbase + vs * (g.random() - 0.5)))
+    compare(bt, float(g.choice([1.0, -0.7, 0.3])) / math.sqrt(d), window)
