@@ -350,8 +350,9 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * norms are more than 2^15 or V norms more than 2^10 apart take longer).
  * Positions outside a row's range do not reach it, whatever their rows hold.
  * Accuracy, whichever type the output has: with S_j = scale |q| |k_j| / sqrt(d)
- * a row is off by at most 6 * 2^-10 / sqrt(3) * sum_j p_j (S_j |v_j - out| +
- * |v_j| / sqrt(d)) per element (six standard deviations of its roundings): about
+ * element i of a row is off by at most 3.4e-3 sum_j p_j (S_j |v_ji - out_i| +
+ * |v_j| / sqrt(d)) + 1.5e-3 sum_j p_j |v_ji| (six standard deviations of the
+ * roundings that differ by coordinate, and the most of those that do not): about
  * 1e-3 of ordinary values, but up to 0.07 on rows with outlier channels and
  * values up to 28, where tq_attn_decode_paged and tq_attn_prefill, which carry
  * their operands in two parts, hold 2e-3.  Elements of q below 2^100.

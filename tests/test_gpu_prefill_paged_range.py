@@ -9,6 +9,13 @@ product's roundings by SIGMA p_j |v_j| / sqrt(d), as the rotation spreads them
 over the row.  The deviations are added up as if they were all of one sign, and
 taken six times:
   6 SIGMA sum_j p_j (S_j |v_ji - out_i| + |v_j| / sqrt(d)).
+Three of the second product's roundings may be the same for all coordinates of a
+position, and then scale it instead: of the probability, of the norm, and of the
+levels, which at 2 bits are of only two sizes.  Each is at most half a step, 2^-11:
+  + 3 * 2^-11 sum_j p_j |v_ji|.
+(A row of a single position, d = 64, 2 bits: all its elements off by 9.1e-4 of
+themselves, of which the first sum allows 3.4e-3 |v| / sqrt(d), less than that for an
+element of four times the mean size.)
 Probabilities that leave fp16's normal range are off by 2^-25 where the largest
 is at least 2^-8, less than a thousandth of the second term at these lengths.
 No term knows a position that the token does not attend to."""
@@ -53,7 +60,8 @@ def reference(bt, scale, window=0):
                 o = p @ vv
                 S = abs(scale) * np.linalg.norm(qq) * np.linalg.norm(kk, axis=1) / rd
                 out[bt.cu[b] + t, h] = o
-                tol[bt.cu[b] + t, h] = 6 * SIGMA * ((p * S) @ np.abs(vv - o) + (p @ np.linalg.norm(vv, axis=1)) / rd)
+                tol[bt.cu[b] + t, h] = 6 * SIGMA * ((p * S) @ np.abs(vv - o) + (p @ np.linalg.norm(vv, axis=1)) / rd) + \
+                    3 * 2.0 ** -11 * (p @ np.abs(vv))
     return out, tol
 
 
