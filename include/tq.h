@@ -347,7 +347,8 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * d in {32, 64, 128, 256}, Hq / Hkv up to 128.  Both products run on the
  * tensor cores with fp16 operands and fp32 sums; norms of 0 and from 2^-86 to
  * 2^100, in any order (smaller ones lose bits; blocks of 128 positions whose K
- * norms are more than 2^15 or V norms more than 2^10 apart take longer).
+ * norms are more than 2^15 or V norms more than 2^10 apart, or with V norms of 0
+ * beside others, take longer).
  * Positions outside a row's range do not reach it, whatever their rows hold.
  * Accuracy, whichever type the output has: with S_j = scale |q| |k_j| / sqrt(d)
  * element i of a row is off by at most 3.4e-3 sum_j p_j (S_j |v_ji - out_i| +

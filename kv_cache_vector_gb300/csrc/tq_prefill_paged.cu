@@ -44,8 +44,8 @@
 //   The norms that set a block's powers may belong to positions that a row does
 // not attend to.  Its own K rows keep all their bits down to 2^-16 of the
 // largest (fp16 has 28 powers of two below 2^14, the levels use 7 of them) and
-// its V rows and probabilities to 2^-10.  A block whose norms (0 left out) are
-// further apart, or whose Ev is 60 below an earlier one (the sum of P' could lose
+// its V rows and probabilities to 2^-10.  A block whose norms are further apart (a
+// K norm of 0 left out, and a block without any V norm), or whose Ev is 60 below an earlier one (the sum of P' could lose
 // what l needs), is "wide": every position has its own Ek and Ev, and the softmax
 // warps first put them into the scores (pp_wide).  Such steps are slower, and no
 // size of norms that a row does not attend to changes its result.
@@ -55,9 +55,9 @@
 // that attend to it see them) and its V row zero.
 //
 // What bounds it.  Two chunks of 4096 tokens over 12-16k positions (32 / 8
-// heads, d = 128, K4/V3): 1.37 ms, 1.15 PFLOP/s of useful products, 60% of the
-// measured burst rate; about 4400 cycles per block and 256 rows, of which the
-// products need 2048.  A stream's step is a chain (scores 512 cycles and more,
+// heads, d = 128, K4/V3): 1.37 to 1.43 ms by box, 1.15 to 1.10 PFLOP/s of useful
+// products, 60 to 57% of the measured burst rate; about 4400 cycles per block and
+// 256 rows, of which the products need 2048.  A stream's step is a chain (scores 512 cycles and more,
 // as both operands come from shared memory that the expansion writes at the
 // same time; softmax about 2300; product with V 512; a barrier's wake-up of
 // about 110 between each), and two streams do not fill all of it.  With one
@@ -649,8 +649,8 @@ __device__ __forceinline__ void pp_wide16(uint32_t t_s, const unsigned char* col
 // A wide block becomes one without powers of two: its scores times their factors
 // plus the positions' V exponents, in the scores' place.  Returns the larger of m
 // and the block's maximum score, and the row's sum of 2^(s - that).  (A call by
-// itself, with values only: as part of the step it took registers and
-// instruction cache from all steps, 1.37 -> 1.50 ms for the long chunks; 1.39 so.)
+// itself, with values only: inlined in the step it took registers and instruction
+// cache from all steps, 1.37 -> 1.63 ms for the long chunks.)
 template <int N>
 __device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, float cq, int c0, int c1, float m) {
     float sum = 0.f;
@@ -1156,14 +1156,15 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 const int t0 = (p.blk + j) * N, from = p.kv_lo - t0, lim = p.kv_end - t0;  // the block's positions that count
                 const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
                 float kn[N / 32], vn[N / 32];
+                bool in[N / 32];
                 // the largest finite norms, as bits
                 uint32_t mk = 0, mv = 0;
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
                     const int r = 32 * k + lane;
-                    const bool in = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
-                    kn[k] = in ? knp[r] : 0.f;
-                    vn[k] = in ? vnp[r] : 0.f;
+                    in[k] = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+                    kn[k] = in[k] ? knp[r] : 0.f;
+                    vn[k] = in[k] ? vnp[r] : 0.f;
                     const uint32_t x = pp_finite(kn[k]), y = pp_finite(vn[k]);
                     mk = max(mk, x), mv = max(mv, y);
                 }
@@ -1177,7 +1178,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
                     const float x = fabsf(kn[k] * sk), y = fabsf(vn[k] * sv);  // the largest: 2^13 to 2^14
-                    far = far || (x < 0.25f && x > 0.f) || (y < 8.f && y > 0.f);
+                    // (a V norm of 0 beside others: a row that attends to it alone has no use for their exponent)
+                    far = far || (x < 0.25f && x > 0.f) || (y < 8.f && in[k] && mv > 0u);
                 }
                 const bool wide = __any_sync(0xFFFFFFFFu, far);
                 if (!wide) {

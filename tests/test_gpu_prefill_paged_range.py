@@ -40,12 +40,18 @@ def _lib():
     abi.tq_device_status(reset=True)
 
 
+# Sequences that fill the GPU: with few items each is cut into parts of about a block, with these
+# behind them items are mostly whole and their blocks follow one another in one running softmax.
+CROWD = [(1, 20)] * 400
+both_ways = pytest.mark.parametrize("crowd", [[], CROWD], ids=["few", "many"])
+
+
 def reference(bt, scale, window=0):
-    """(attention in 64 bits, its tolerance), both [rows of q, Hq, d]."""
+    """(attention in 64 bits, its tolerance), both [rows of q, Hq, d]; zero for a crowd's rows."""
     q = bt.q.double().numpy()
     out, tol = np.zeros(q.shape), np.zeros(q.shape)
     G, rd = bt.Hq // bt.Hkv, math.sqrt(bt.d)
-    for b, (n, c) in enumerate(bt.lens):
+    for b, (n, c) in enumerate(bt.lens[:-len(CROWD)] if bt.lens[-len(CROWD):] == CROWD else bt.lens):
         k, v = bt.decoded(b) if n and c else (None, None)
         for t in range(n):
             p1 = c - n + t + 1
@@ -70,6 +76,8 @@ def compare(bt, scale, window=0, rows=None):
     args = bt.gpu()
     want, tol = reference(bt, scale, window)
     on = np.ones(want.shape[:2], bool) if rows is None else np.repeat(rows, bt.Hq // bt.Hkv, 1)
+    if bt.lens[-len(CROWD):] == CROWD:
+        on[-len(CROWD):] = False
     for dt in (torch.float32, torch.bfloat16):
         got = abi.tq_attn_prefill_paged(*args, scale, window=window, out_dtype=dt)
         assert abi.tq_device_status(reset=True) == 0
@@ -102,12 +110,13 @@ OUTSIDE = [
 ]
 
 
+@both_ways
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("ratio", [4, 9, 12, 15, 18, 24, 40, 90])
 @pytest.mark.parametrize("d,kb,vb", [(32, 4, 4), (64, 3, 4), (128, 4, 3), (256, 4, 4)])
-def test_a_large_norm_does_not_reach_rows_that_do_not_attend_to_it(d, kb, vb, ratio, which):
+def test_a_large_norm_does_not_reach_rows_that_do_not_attend_to_it(d, kb, vb, ratio, which, crowd):
     for i, (lens, window, marks) in enumerate(OUTSIDE):
-        bt = Batch(20 + i, lens, 4, 2, d, 64, kb, vb)
+        bt = Batch(20 + i, lens + crowd, 4, 2, d, 64, kb, vb)
         for b, h, pos in marks:
             bt.set_norm(b, which, h, pos, math.sqrt(d) * 2.0 ** ratio)
         # a token that attends to so large a key has a softmax of steps: any rounding of a
@@ -117,6 +126,7 @@ def test_a_large_norm_does_not_reach_rows_that_do_not_attend_to_it(d, kb, vb, ra
         compare(bt, 1 / math.sqrt(d), window, rows)
 
 
+@both_ways
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("lens", [[(1, 3000)], [(300, 900)], [(9, 400), (2, 1100)]])
 @pytest.mark.parametrize("name,vnorm", [
@@ -127,9 +137,9 @@ def test_a_large_norm_does_not_reach_rows_that_do_not_attend_to_it(d, kb, vb, ra
     ("tiny, then zeros", lambda p: np.where(p < 150, 2.0 ** -60, 0.0)),
     ("mixed within blocks", lambda p: 2.0 ** ((p * 37 % 121) - 60.0)),
 ])
-def test_values_of_all_sizes(name, vnorm, lens, d):
+def test_values_of_all_sizes(name, vnorm, lens, d, crowd):
     """Scores of all sizes too: where the values are small they take most of the weight."""
-    bt = Batch(30, lens, 4, 2, d, 64, 4, 4)
+    bt = Batch(30, lens + crowd, 4, 2, d, 64, 4, 4)
     for b, (_, c) in enumerate(lens):
         v = vnorm(np.arange(c)).astype(np.float32)
         for h in range(2):
@@ -138,14 +148,16 @@ def test_values_of_all_sizes(name, vnorm, lens, d):
     compare(bt, 0.2)
 
 
+@both_ways
 @pytest.mark.parametrize("d", [128, 256])
-def test_small_values_with_all_the_weight(d):
+def test_small_values_with_all_the_weight(d, crowd):
     """Sharp softmaxes whose winners have far smaller V norms than the rest."""
-    bt = Batch(31, [(40, 900)], 4, 1, d, 64, 4, 4)
+    bt = Batch(31, [(40, 900)] + crowd, 4, 1, d, 64, 4, 4)
     for pos in (0, 200, 511, 850):
         bt.set_norm(0, "k", 0, pos, 60.0 * d / 128)
         bt.set_norm(0, "v", 0, pos, 1e-3)
     got, want, tol = compare(bt, 0.5)
+    got, want, tol = (x[:40] for x in (got, want, tol))
     won = np.linalg.norm(want, axis=-1) < 2e-3
     assert won.mean() > 0.3
     # rows of zeros in their place would not pass, nor rows 5% off
@@ -153,10 +165,11 @@ def test_small_values_with_all_the_weight(d):
     assert (0.05 * np.abs(want[won]) > tol[won] + np.abs(want[won]) * 2.0 ** -8).any(-1).mean() > 0.5
 
 
+@both_ways
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_values_spread_over_many_powers(d):
+def test_values_spread_over_many_powers(d, crowd):
     """Norms with a log-normal spread of four powers of two, judged row by row."""
-    bt = Batch(32, [(60, 500), (1, 700), (140, 140)], 4, 2, d, 32, 4, 4,
+    bt = Batch(32, [(60, 500), (1, 700), (140, 140)] + crowd, 4, 2, d, 32, 4, 4,
                norm=lambda r, n: np.exp(3 * r.standard_normal(n)))
     compare(bt, 0.002)
 
@@ -231,8 +244,9 @@ def test_rows_with_outlier_channels(d, kb, vb):
     assert np.abs(one.double().cpu().numpy() - want[[119, 159]]).max() <= 2e-3
 
 
+@both_ways
 @pytest.mark.parametrize("seed", range(40))
-def test_seeded_sweep(seed):
+def test_seeded_sweep(seed, crowd):
     """Lengths, heads, pages, windows, widths and spreads of norms drawn together; slots without a
     position hold NaN norms, as in all of these batches."""
     g = np.random.default_rng(1000 + seed)
@@ -245,7 +259,7 @@ def test_seeded_sweep(seed):
     if not sum(n for n, _ in lens):
         lens.append((3, 200))
     window = int(g.choice([0, 0, 1, int(g.integers(1, 300)), 5000]))
-    bt = Batch(seed, lens, Hkv * G, Hkv, d, int(g.choice([32, 64, 128, 512])), int(g.integers(2, 5)),
+    bt = Batch(seed, lens + crowd, Hkv * G, Hkv, d, int(g.choice([32, 64, 128, 512])), int(g.integers(2, 5)),
                int(g.integers(2, 5)), flags=int(g.integers(0, 4)))
     ks, vs = (float(g.choice([0, 2, 9, 14, 30, 60])) for _ in range(2))
     vbase = float(g.integers(-30, 30))
@@ -255,3 +269,20 @@ def test_seeded_sweep(seed):
                 bt.set_norm(b, "k", h, p, math.sqrt(d) * 2.0 ** -(g.random() * ks))
                 bt.set_norm(b, "v", h, p, 0.0 if g.random() < 0.05 else 2.0 ** (vbase + vs * (g.random() - 0.5)))
     compare(bt, float(g.choice([1.0, -0.7, 0.3])) / math.sqrt(d), window)
+
+
+@both_ways
+@pytest.mark.parametrize("ratio", [8, 20, 40, 90])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_zero_values_beside_a_large_one_that_is_not_attended(d, ratio, crowd):
+    """Tokens that attend, in one block, to positions with a V norm of 0 only, while the block holds a
+    large one in front of their window or behind the causal mask."""
+    for lens, window, marks in (([(120, 260), (20, 150)], 0, [(0, 128, 256, 252), (1, 128, 149, 149)]),
+                                ([(180, 420), (300, 900)], 150, [(0, 128, 256, 130), (1, 640, 768, 641)])):
+        bt = Batch(36, lens + crowd, 4, 2, d, 64, 4, 4)
+        for b, z0, z1, large in marks:
+            for h in range(2):
+                for p in range(z0, z1):
+                    bt.set_norm(b, "v", h, p, 0.0)
+                bt.set_norm(b, "v", h, large, math.sqrt(d) * 2.0 ** ratio)
+        compare(bt, 1 / math.sqrt(d), window)
