@@ -8,20 +8,20 @@
 //     works out the new table and the list of (source, destination) page
 //     pairs to copy.  All of its decisions follow row order and take the
 //     lowest free page ids first, so the result does not depend on timing;
-//     the only atomics are integer sums and minima.  Nothing is written to
+//     the only atomics are integer sums, minima and maxima.  Nothing is written to
 //     the output table before the call is known to succeed (valid input,
 //     enough free pages): a call that fails returns the table as it was.
 //     The steps exchange data through the workspace with a cluster barrier
 //     between them (hardware barriers: nothing spins).
 //   k_pages_copy   copies the pairs' pages, in every layer, 32 KB per CTA and
 //     step.  Bound by memory: a copied page is read once and written once.
-//     473 pages of 2 MB (32 layers): 293 us, 6.35 TB/s; with 4, 8 and 16 KB
+//     473 pages of 2 MB (32 layers): 293 to 297 us, 6.35 TB/s; with 4, 8 and 16 KB
 //     steps 413, 322 and 304 us (too few bytes in flight).
 // Both are launched with programmatic stream serialization, so that their CTAs
 // are there when the kernel before ends.  Small calls are bound by the launches
 // and the plan's chain of dependent reads (steps of 1 to 2 us each): 4 us for a
-// copy of 5 pages, 10 to 17 us for a fork, resize or compaction with few pages
-// to copy (8 to 512 rows, 100 to 6500 pages).
+// copy of 5 pages, 9 to 16 us for a fork, resize or compaction with few pages
+// to copy (8 to 512 rows, 100 to 6500 pages), in a graph.
 #include <climits>
 
 #include <cooperative_groups.h>
