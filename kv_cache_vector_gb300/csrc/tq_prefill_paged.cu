@@ -1403,7 +1403,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status);
                     const volatile float* mp = reinterpret_cast<const volatile float*>(sm + Z::kMeta) + 2 * (tc & 7);
                     const float2 meta = make_float2(mp[0], mp[1]);
-                    const bool wide = meta.x == 0.f;
+                    // a vote, so that the warp stays together also where a wait gave up and the lanes
+                    // read the slot at different times
+                    const bool wide = __any_sync(0xFFFFFFFFu, meta.x == 0.f);
                     if (kWide != wide) break;
                     pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
                     ++ns[buf];
