@@ -55,7 +55,7 @@
 // that attend to it see them) and its V row zero.
 //
 // What bounds it.  Two chunks of 4096 tokens over 12-16k positions (32 / 8
-// heads, d = 128, K4/V3): 1.37 to 1.43 ms by box, 1.15 to 1.10 PFLOP/s of useful
+// heads, d = 128, K4/V3): 1.37 to 1.43 ms by GPU, 1.15 to 1.10 PFLOP/s of useful
 // products, 60 to 57% of the measured burst rate; about 4400 cycles per block and
 // 256 rows, of which the products need 2048.  A stream's step is a chain (scores 512 cycles and more,
 // as both operands come from shared memory that the expansion writes at the

@@ -155,3 +155,39 @@ def test_a_serving_loop(d, kb, vb):
     sv.append([1, 1, 3, 1, 1, 1])
     sv.sound()
     assert abi.tq_device_status(reset=True) == 0
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes an array: pages at its end are copied, attended to and moved as
+    those at its start."""
+    n_pages, Hkv, page, d = 140000, 8, 64, 128
+    pool = abi.PagedLayers(abi.PagedCache.empty(n_pages, Hkv, page, d, 4, 4))
+    c = pool.layers[0]
+    assert c.k_packed.numel() > 2 ** 32 and c.v_packed.numel() > 2 ** 32
+    g = torch.Generator().manual_seed(3)
+    low, high = torch.arange(1, 8), torch.arange(n_pages - 7, n_pages)
+    for t in (c.k_packed, c.v_packed):
+        t[1:8] = torch.randint(0, 256, t[1:8].shape, generator=g, dtype=torch.uint8).cuda()
+    for t in (c.k_norm, c.v_norm):
+        t[1:8] = 5 + 5 * torch.rand(t[1:8].shape, generator=g).cuda()
+    ids = lambda x: x.to(torch.int32).cuda()  # noqa: E731
+    abi.tq_pages_copy(pool, pool, ids(low), ids(high))
+    for t in (c.k_packed, c.k_norm, c.v_packed, c.v_norm):
+        assert torch.equal(t[1:8], t[n_pages - 7:]) and t[1:8].any()
+    n, ctx = 130, 7 * page - 5
+    q = torch.randn(n + 1, 32, d, generator=g).to(torch.bfloat16).cuda()
+    cu, lens = ids(torch.tensor([0, n, n + 1])), ids(torch.tensor([ctx, ctx]))
+    outs = [abi.tq_attn_prefill_paged(abi.Plan(d, 42), q, cu, c, ids(torch.stack([x, x])), lens, 0.1) for x in (low, high)]
+    assert torch.equal(*outs) and outs[0].any()
+    books = abi.PageTable.empty(2, 7, n_pages)
+    books.block_table[0], books.lens[0] = ids(high), ctx
+    books.refs[n_pages - 7:] = 1
+    books, info = abi.tq_pages_fork(books, ids(torch.tensor([0, 0])), pool)
+    assert info.tolist() == [1, 0] and books.block_table[1].tolist() == high.tolist()[:6] + [0]
+    for t in (c.k_packed, c.k_norm, c.v_packed, c.v_norm):
+        assert torch.equal(t[0], t[n_pages - 1])
+    books, moved, info = abi.tq_pages_compact(books, pool, out=books)
+    assert info.tolist() == [8, 7] and books.block_table[0].tolist() == list(range(1, 8))
+    for t in (c.k_packed, c.k_norm, c.v_packed, c.v_norm):
+        assert torch.equal(t[1:8], t[n_pages - 7:])
+    assert abi.tq_device_status(reset=True) == 0
