@@ -375,6 +375,42 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
                                 int v_bits, float scale, void *out, tq_dtype out_dtype, void *workspace,
                                 size_t workspace_bytes, tq_stream_t stream);
 
+/* The same with first positions that stay visible ("sinks") while a sliding
+ * window moves on, for conversations longer than the window: the token at
+ * position p attends over positions j <= p with j > p - window or j < sinks.
+ * A window of 0 is none, and with 0 sinks this is tq_attn_prefill_paged.  Prompt
+ * chunks, drafts and single tokens, ragged in one batch.  Pages between the
+ * sinks and the window of a sequence's first token are not looked at.
+ * Arguments, accuracy, status words and errors as tq_attn_prefill_paged
+ * (TQ_ERR_INVALID_ARG also for sinks < 0). */
+size_t tq_attn_sinks_paged_workspace_bytes(int Hq, int Hkv, int d);
+tq_status tq_attn_sinks_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
+                              tq_paged_cache cache, const int32_t *block_table, int max_pages,
+                              const int32_t *cu_q, const int32_t *ctx_lens, int window, int sinks, int k_bits,
+                              int v_bits, float scale, void *out, tq_dtype out_dtype, void *workspace,
+                              size_t workspace_bytes, tq_stream_t stream);
+
+/* Attention of the nodes of drafted trees over a paged cache, ragged in one
+ * batch: sequence b's n_b = cu_q[b + 1] - cu_q[b] tokens are the last n_b of its
+ * ctx_lens[b] positions (their K and V rows are in the cache already), and token
+ * t attends over all positions in front of the n_b and, of those, over position
+ * i's where bit i % 32 of word i / 32 of its mask row is set -- its ancestors and
+ * itself, as tq_pages_slots writes them, or any other set.  A token that attends
+ * to nothing (no bit, nothing in front) gets a zero row.
+ *   mask: [n_q][mask_words] uint32, device; bits from n_b on do not count;
+ *     mask_words up to TQ_TREE_MAX_WORDS
+ * A sequence with more tokens than positions or than 32 mask_words is left out
+ * (its rows are not written) and sets the device status word to 75.
+ * Other arguments, accuracy, status words and errors as tq_attn_prefill_paged
+ * (TQ_ERR_INVALID_ARG also for a mask that overlaps out or the workspace). */
+#define TQ_TREE_MAX_WORDS 32
+size_t tq_attn_tree_paged_workspace_bytes(int Hq, int Hkv, int d);
+tq_status tq_attn_tree_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
+                             tq_paged_cache cache, const int32_t *block_table, int max_pages, const int32_t *cu_q,
+                             const int32_t *ctx_lens, const uint32_t *mask, int mask_words, int k_bits,
+                             int v_bits, float scale, void *out, tq_dtype out_dtype, void *workspace,
+                             size_t workspace_bytes, tq_stream_t stream);
+
 /* ---------------------------------------------------- upkeep of the pages
  * The pages of a paged cache as a serving loop keeps them: which sequence row
  * holds which pages, branches that share pages, growth, ends, and closing up
@@ -463,6 +499,66 @@ tq_status tq_pages_compact(tq_page_table in, tq_page_table out, int32_t *moved_t
                            int max_pages, const tq_paged_cache *layers, int n_layers, int Hkv, int d,
                            int k_bits, int v_bits, int32_t *info, void *workspace, size_t workspace_bytes,
                            tq_stream_t stream);
+
+/* ------------------------------------------------------- a step's tokens
+ * Where the new tokens of a step go, from the rows' lengths alone: row b's last
+ * counts[b] of its lens[b] positions are new (their pages are in the table, as
+ * after tq_pages_resize).  The tokens of all rows follow one another:
+ *   cu_q      [n_seqs + 1]  row b's tokens are cu_q[b] .. cu_q[b + 1] - 1
+ *   positions [n_tokens]    a token's position in its row; with parents the
+ *                           position that its depth gives it (for rotary
+ *                           encodings): siblings share one
+ *   slots     [n_tokens] int64  page * page_size + offset (tq_append_slots)
+ *   mask      [n_tokens][mask_words]  with parents: bit i of token t's row is
+ *                           set if token i of its row is its ancestor or itself
+ *                           (tq_attn_tree_paged)
+ * n_tokens is the room in the outputs: tokens past the rows' get slot -1,
+ * position 0 and an empty mask row.
+ *   parents: [n_tokens] int32 or NULL: the number within its row of the node that
+ *     a node follows, less than its own, or -1 for one that follows the last
+ *     token in front of the draft
+ * table.refs is not looked at (may be NULL).  mask_words and mask are not looked
+ * at without parents.
+ * A call with a count or length out of range (counts[b] < 0 or > lens[b], a length
+ * past max_pages * page_size, a tree of more than 32 mask_words nodes) or more
+ * tokens than n_tokens writes a step without tokens (cu_q all 0) and sets the
+ * device status word to 63.  A page id outside [0, n_pages) gives slot -1 and
+ * status 64.  A parent out of range counts as -1 and sets 65.
+ * Alignment: 4 bytes, slots 8.  No output may overlap an input or another
+ * output.  Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (page_size, mask_words
+ * above TQ_TREE_MAX_WORDS, n_seqs above 2^18), TQ_ERR_ALIGNMENT. */
+tq_status tq_pages_slots(tq_page_table table, int n_seqs, int max_pages, int64_t n_pages, int page_size,
+                         const int32_t *counts, const int32_t *parents, int mask_words, int64_t n_tokens,
+                         int32_t *cu_q, int32_t *positions, int64_t *slots, uint32_t *mask, tq_stream_t stream);
+
+/* Append a step's tokens to one layer at their slots, as tq_append_paged encodes
+ * them.
+ *   k_new, v_new: token t's row of KV head h at element t * stride + h * d (dtype),
+ *     device; the strides at least Hkv * d elements and a multiple of 16 bytes
+ *   slots: [n_tokens] int64, device; a negative one has no token (nothing is read
+ *     or written for it), one past the last page writes nothing and sets the device
+ *     status word to 42.  Two tokens of one slot: one of the two rows, or a mix.
+ * d >= 32.  Errors: as tq_append_paged. */
+tq_status tq_append_slots(const tq_plan *plan, int k_bits, int v_bits, const void *k_new, int64_t k_stride,
+                          const void *v_new, int64_t v_stride, tq_dtype dtype, int64_t n_tokens, int Hkv,
+                          tq_paged_cache cache, const int64_t *slots, tq_stream_t stream);
+
+/* After drafted tokens were checked: of row b's last counts[b] tokens those with
+ * the numbers keep[b][0 .. n_keep[b]) stay (ascending, each once), and their K and
+ * V rows move to the front of the counts[b], in every layer.
+ *   keep [n_seqs][max_keep], counts, n_keep [n_seqs] int32, device
+ *   new_lens [n_seqs] int32, device: lens[b] - counts[b] + n_keep[b], which
+ *     tq_pages_resize takes to give back the pages that are left over
+ * The books themselves are not written.  The tokens that move and the places that
+ * they move to must lie in pages that the row does not share.
+ * A row whose numbers are out of range or order, or whose pages are shared
+ * (refs above 1) or out of range, stays as it is (new_lens[b] = lens[b]) and sets
+ * the device status word to 66.
+ * layers, alignment and errors as for the calls above (no workspace; new_lens
+ * overlaps none of the inputs). */
+tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const int32_t *counts, const int32_t *keep,
+                        int max_keep, const int32_t *n_keep, int32_t *new_lens, const tq_paged_cache *layers,
+                        int n_layers, int Hkv, int d, int k_bits, int v_bits, tq_stream_t stream);
 
 /* Workspace bytes tq_attn_prefill needs for a cache of capacity `cap`: 32 KB
  * for the query rotation matrix, then the expanded K/V tiles, 99332 bytes per

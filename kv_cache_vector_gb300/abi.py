@@ -32,6 +32,8 @@ EXPORTS = ("tq_codebook_init", "tq_plan_create", "tq_plan_destroy", "tq_plan_sig
            "tq_attn_prefill_workspace_bytes", "tq_attn_prefill", "tq_qjl_matrix", "tq_encode_qjl",
            "tq_decode_qjl", "tq_attn_qjl_workspace_bytes", "tq_attn_decode_qjl",
            "tq_attn_prefill_paged_workspace_bytes", "tq_attn_prefill_paged",
+           "tq_attn_sinks_paged_workspace_bytes", "tq_attn_sinks_paged", "tq_attn_tree_paged_workspace_bytes",
+           "tq_attn_tree_paged", "tq_pages_slots", "tq_append_slots", "tq_pages_keep",
            "tq_pages_workspace_bytes", "tq_pages_copy", "tq_pages_fork", "tq_pages_resize", "tq_pages_compact")
 
 
@@ -106,6 +108,15 @@ def lib() -> ctypes.CDLL:
         ("tq_attn_prefill_paged_workspace_bytes", ctypes.c_size_t, [i32, i32, i32]),
         ("tq_attn_prefill_paged", i32, [vp, vp, i64, i32, i32, i32, PagedCacheView, vp, i32, vp, vp, i32, i32, i32,
                                         f32, vp, i32, vp, ctypes.c_size_t, vp]),
+        ("tq_attn_sinks_paged_workspace_bytes", ctypes.c_size_t, [i32, i32, i32]),
+        ("tq_attn_sinks_paged", i32, [vp, vp, i64, i32, i32, i32, PagedCacheView, vp, i32, vp, vp, i32, i32, i32, i32,
+                                      f32, vp, i32, vp, ctypes.c_size_t, vp]),
+        ("tq_attn_tree_paged_workspace_bytes", ctypes.c_size_t, [i32, i32, i32]),
+        ("tq_attn_tree_paged", i32, [vp, vp, i64, i32, i32, i32, PagedCacheView, vp, i32, vp, vp, vp, i32, i32, i32,
+                                     f32, vp, i32, vp, ctypes.c_size_t, vp]),
+        ("tq_pages_slots", i32, [PageTableView, i32, i32, i64, i32, vp, vp, i32, i64, vp, vp, vp, vp, vp]),
+        ("tq_append_slots", i32, [vp, i32, i32, vp, i64, vp, i64, i32, i64, i32, PagedCacheView, vp, vp]),
+        ("tq_pages_keep", i32, [PageTableView, i32, i32, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
         ("tq_pages_workspace_bytes", ctypes.c_size_t, [i32, i32, i64]),
         ("tq_pages_copy", i32, [vp, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp, ctypes.c_size_t, vp]),
         ("tq_pages_fork", i32, [PageTableView, vp, PageTableView, i32, i32, vp, i32, i32, i32, i32, i32, vp, vp,
@@ -500,6 +511,15 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
     (over the last `window` positions, 0: all) -> out [n_q, Hq, d] bf16 or
     fp32.  Rows outside every sequence keep what `out` held (zeros if none is
     passed)."""
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be in [0, 2^31)")
+    return _tokens_paged("tq_attn_prefill_paged", plan, q, cu_q, cache, block_table, ctx_lens, (window,), scale, out,
+                         out_dtype, workspace)
+
+
+def _tokens_paged(fn, plan, q, cu_q, cache, block_table, ctx_lens, seen, scale, out, out_dtype, workspace):
+    """The checks and the call that the attentions of several tokens per
+    sequence share; seen: what the rows attend to, as the C call takes it."""
     n_q, Hq, d = q.shape
     B = ctx_lens.numel()
     rows = cache.k_norm.shape
@@ -509,8 +529,6 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
         raise ValueError("q and the cache's arrays must have the plan's head dimension and one geometry")
     if cu_q.numel() != B + 1 or block_table.shape[0] != B:
         raise ValueError("cu_q [B + 1], ctx_lens [B] and block_table [B, max_pages] expected")
-    if not 0 <= window < 2 ** 31:
-        raise ValueError("window must be in [0, 2^31)")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
     if (cache.k_packed.dtype, cache.v_packed.dtype, cache.k_norm.dtype, cache.v_norm.dtype) != \
@@ -527,12 +545,49 @@ def tq_attn_prefill_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache
         _same_device(dev, out)
         if out.shape != q.shape:
             raise ValueError("out must be [n_q, Hq, d]")
-        ws = _scratch(workspace, dev, tq_attn_prefill_paged_workspace_bytes, Hq, cache.Hkv, d)
-        _check("tq_attn_prefill_paged", lib().tq_attn_prefill_paged(
+        ws = _scratch(workspace, dev, getattr(lib(), fn + "_workspace_bytes"), Hq, cache.Hkv, d)
+        _check(fn, getattr(lib(), fn)(
             plan.handle, q.data_ptr(), n_q, B, Hq, cache.Hkv, cache.view(), block_table.data_ptr(),
-            block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), window, cache.k_bits, cache.v_bits,
+            block_table.shape[1], cu_q.data_ptr(), ctx_lens.data_ptr(), *seen, cache.k_bits, cache.v_bits,
             scale, out.data_ptr(), _dt(out), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
     return out
+
+
+def tq_attn_sinks_paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().tq_attn_sinks_paged_workspace_bytes(Hq, Hkv, d))
+
+
+def tq_attn_sinks_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache: PagedCache,
+                        block_table: torch.Tensor, ctx_lens: torch.Tensor, scale: float, window: int, sinks: int,
+                        out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """tq_attn_prefill_paged over a sliding window with first positions that
+    stay visible: the token at position p attends over positions j <= p with
+    j > p - window or j < sinks (window 0: all).  One token per sequence or
+    several."""
+    if not 0 <= window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
+        raise ValueError("window and sinks must be in [0, 2^31)")
+    return _tokens_paged("tq_attn_sinks_paged", plan, q, cu_q, cache, block_table, ctx_lens, (window, sinks), scale,
+                         out, out_dtype, workspace)
+
+
+def tq_attn_tree_paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().tq_attn_tree_paged_workspace_bytes(Hq, Hkv, d))
+
+
+def tq_attn_tree_paged(plan: Plan, q: torch.Tensor, cu_q: torch.Tensor, cache: PagedCache,
+                       block_table: torch.Tensor, ctx_lens: torch.Tensor, mask: torch.Tensor, scale: float,
+                       out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """tq_attn_prefill_paged for the nodes of drafted trees: a sequence's tokens
+    attend over all positions in front of them and, among themselves, over those
+    whose bits are set in their rows of mask [n_q, words] int32 (bit i % 32 of
+    word i / 32: token i of the sequence; tq_pages_slots writes it)."""
+    if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
+        raise ValueError("mask must be [n_q, words]")
+    _ints(q.device, mask)
+    return _tokens_paged("tq_attn_tree_paged", plan, q, cu_q, cache, block_table, ctx_lens,
+                         (mask.data_ptr(), mask.shape[1]), scale, out, out_dtype, workspace)
 
 
 # ------------------------------------------------------------ upkeep of the pages
@@ -746,6 +801,107 @@ def tq_pages_compact(table: PageTable, layers, out: PageTable | None = None, mov
     (table, moved_to [n_pages]: each page's new id or -1, info [2]: pages
     held, pages moved); moved_to and info as of tq_pages_fork."""
     return _pages("tq_pages_compact", table, None, layers, out, moved_to, info, workspace)
+
+
+# ------------------------------------------------------------ a step's tokens
+
+@dataclass
+class TokenSlots:
+    """Where a step's new tokens go (device tensors)."""
+    cu_q: torch.Tensor       # [n_seqs + 1] int32: row b's tokens are cu_q[b] .. cu_q[b + 1] - 1
+    positions: torch.Tensor  # [n_tokens] int32: in the row (with parents: by depth); 0 past the rows' tokens
+    slots: torch.Tensor      # [n_tokens] int64: page * page_size + offset; -1: no token
+    mask: torch.Tensor | None = None  # [n_tokens, words] int32: the ancestors of a tree's node, and itself
+
+
+def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_size: int,
+                   parents: torch.Tensor | None = None, mask_words: int = 1,
+                   out: TokenSlots | None = None) -> TokenSlots:
+    """The slot map of a step whose new tokens are the last counts[b] (int32) of
+    row b's positions (table.lens, grown already); n_tokens: room for them.  With
+    parents [n_tokens] int32 (the number within its row of the node that a node
+    follows, -1: none) also the trees' masks of mask_words words, and positions by
+    depth.  All on the device."""
+    bt, dev = table.block_table, table.block_table.device
+    if bt.dim() != 2 or table.lens.numel() != bt.shape[0] or counts.numel() != bt.shape[0]:
+        raise ValueError("block_table [n_seqs, max_pages], lens and counts [n_seqs] expected")
+    if not bt.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    _ints(dev, bt, table.lens, counts)
+    if parents is not None:
+        _ints(dev, parents)
+        if parents.numel() != n_tokens or mask_words < 1:
+            raise ValueError("parents has one entry per token and its masks at least one word")
+    n_seqs, max_pages = bt.shape
+    with _on(dev):
+        if out is None:
+            out = TokenSlots(torch.empty(n_seqs + 1, dtype=_INT32, device=dev),
+                             torch.empty(n_tokens, dtype=_INT32, device=dev),
+                             torch.empty(n_tokens, dtype=torch.int64, device=dev),
+                             None if parents is None else torch.empty(n_tokens, mask_words, dtype=_INT32, device=dev))
+        else:
+            _ints(dev, out.cu_q, out.positions)
+            if out.slots.dtype != torch.int64 or out.slots.device != dev or not out.slots.is_contiguous():
+                raise ValueError("slots must be a contiguous int64 tensor on the table's device")
+            if out.cu_q.numel() != n_seqs + 1 or out.positions.numel() != n_tokens or out.slots.numel() != n_tokens:
+                raise ValueError("cu_q [n_seqs + 1], positions and slots [n_tokens] expected")
+            if parents is not None:
+                if out.mask is None or out.mask.shape != (n_tokens, mask_words):
+                    raise ValueError("mask must be [n_tokens, mask_words]")
+                _ints(dev, out.mask)
+        _check("tq_pages_slots", lib().tq_pages_slots(
+            PageTableView(bt.data_ptr(), table.lens.data_ptr(), None), n_seqs, max_pages, table.refs.numel(), page_size,
+            counts.data_ptr(), None if parents is None else parents.data_ptr(), mask_words, n_tokens,
+            out.cu_q.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+            None if parents is None else out.mask.data_ptr(), _raw_stream(dev)))
+    return out
+
+
+def tq_append_slots(plan: Plan, cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor):
+    """k_new, v_new: [n_tokens, Hkv, d] fp32/bf16, heads contiguous, tokens at any
+    stride of 16 bytes (a slice of a fused projection); token t goes to slots[t]
+    (int64), nowhere if that is negative."""
+    n, Hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or d != plan.d or Hkv != cache.Hkv:
+        raise ValueError("k_new / v_new must both be [n_tokens, Hkv, d] of one dtype")
+    if cache.k_packed.shape[-1] * 8 != d * cache.k_bits or cache.v_packed.shape[-1] * 8 != d * cache.v_bits:
+        raise ValueError("the cache's rows must have the plan's head dimension")
+    dev = slots.device
+    if slots.dtype != torch.int64 or not slots.is_cuda or not slots.is_contiguous() or slots.numel() != n:
+        raise ValueError("slots must be a contiguous int64 CUDA tensor [n_tokens]")
+    _same_device(dev, k_new, v_new, cache.k_packed, cache.k_norm, cache.v_packed, cache.v_norm)
+    for t in (k_new, v_new):
+        if n and ((d > 1 and t.stride(2) != 1) or (Hkv > 1 and t.stride(1) != d)):
+            raise ValueError("the heads of a token must be contiguous")
+    with _on(dev):
+        _check("tq_append_slots", lib().tq_append_slots(
+            plan.handle, cache.k_bits, cache.v_bits, k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(),
+            v_new.stride(0), _dt(k_new), n, Hkv, cache.view(), slots.data_ptr(), _raw_stream(dev)))
+
+
+def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor, layers,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Of row b's last counts[b] tokens those with the numbers keep[b, :n_keep[b]]
+    (int32, ascending) stay: their rows move to the front of the counts[b] in
+    every layer.  Returns the new lengths [n_seqs], for tq_pages_resize."""
+    layers = _layers(layers)
+    dev = layers.device
+    bt = table.block_table
+    if bt.dim() != 2 or keep.dim() != 2 or keep.shape[0] != bt.shape[0] or counts.numel() != bt.shape[0] or \
+            n_keep.numel() != bt.shape[0]:
+        raise ValueError("keep [n_seqs, max_keep], counts and n_keep [n_seqs] expected")
+    _ints(dev, counts, keep, n_keep)
+    with _on(dev):
+        view = table._view(layers, bt.shape)
+        if out is None:
+            out = torch.empty(bt.shape[0], dtype=_INT32, device=dev)
+        _ints(dev, out)
+        if out.numel() != bt.shape[0]:
+            raise ValueError("one new length per row")
+        _check("tq_pages_keep", lib().tq_pages_keep(
+            view, bt.shape[0], bt.shape[1], counts.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr(),
+            out.data_ptr(), layers.views, len(layers.views), *layers.args, _raw_stream(dev)))
+    return out
 
 
 def tq_device_status(reset: bool = False) -> int:

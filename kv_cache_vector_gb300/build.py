@@ -23,13 +23,13 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 # (source, specialisation macros TQ_UNIT_<name>)
 CODEC_DIMS = (8, 16, 32, 64, 128, 256)
 ATTN_DIMS = (32, 64, 128, 256)
-UNITS = ([("tq_api.cpp", {}), ("tq_launch.cu", {}), ("tq_noalloc.cu", {}), ("tq_pages.cu", {})]
+UNITS = ([("tq_api.cpp", {}), ("tq_launch.cu", {}), ("tq_noalloc.cu", {}), ("tq_pages.cu", {}), ("tq_steps.cu", {})]
          + [("tq_codec.cu", {"D": d}) for d in CODEC_DIMS]
          + [("tq_attn.cu", {"D": 128, "KB": kb}) for kb in (2, 3, 4)]
          + [("tq_attn_generic.cu", {"D": d, "KB": kb}) for d in ATTN_DIMS for kb in (2, 3, 4)]
          + [("tq_prefill.cu", {"KB": kb}) for kb in (2, 3, 4)]
          + [("tq_qjl.cu", {"D": d}) for d in (32, 64, 128)]
-         + [("tq_prefill_paged.cu", {"D": d}) for d in ATTN_DIMS])
+         + [("tq_prefill_paged.cu", {"D": d, "MODE": m}) for d in ATTN_DIMS for m in (0, 1, 2)])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

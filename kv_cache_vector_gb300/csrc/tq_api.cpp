@@ -1093,6 +1093,130 @@ tq_status tq_pages_compact(tq_page_table in, tq_page_table out, int32_t* moved_t
                       k_bits, v_bits, info, workspace, workspace_bytes, stream);
 }
 
+// ------------------------------------------------------------ a step's tokens
+
+tq_status tq_pages_slots(tq_page_table table, int n_seqs, int max_pages, int64_t n_pages, int page_size,
+                         const int32_t* counts, const int32_t* parents, int mask_words, int64_t n_tokens,
+                         int32_t* cu_q, int32_t* positions, int64_t* slots, uint32_t* mask, tq_stream_t stream) {
+    if (n_seqs < 1 || max_pages < 1 || n_pages < 1 || n_pages > kMaxPages || n_tokens < 0 || (parents && mask_words < 1))
+        return TQ_ERR_INVALID_ARG;
+    const int shift = page_shift_of(page_size);
+    if (shift < 0 || ((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows ||
+        n_tokens > INT32_MAX || (parents && mask_words > TQ_TREE_MAX_WORDS))
+        return TQ_ERR_UNSUPPORTED;
+    if (!table.block_table || !table.lens || !counts || !cu_q || (n_tokens > 0 && (!positions || !slots)) ||
+        (n_tokens > 0 && parents && !mask))
+        return TQ_ERR_INVALID_ARG;
+    if (!aligned4(table.block_table) || !aligned4(table.lens) || !aligned4(counts) || !aligned4(parents) ||
+        !aligned4(cu_q) || !aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned4(mask))
+        return TQ_ERR_ALIGNMENT;
+    auto span = [](const void* p, uint64_t bytes) { return Span{p && bytes ? reinterpret_cast<uintptr_t>(p) : 0, p ? bytes : 0}; };
+    const uint64_t T = (uint64_t)n_tokens;
+    const Span rd[4] = {span(table.block_table, 4 * (uint64_t)n_seqs * max_pages), span(table.lens, 4 * (uint64_t)n_seqs),
+                        span(counts, 4 * (uint64_t)n_seqs), span(parents, 4 * T)};
+    const Span wr[4] = {span(cu_q, 4 * (uint64_t)(n_seqs + 1)), span(positions, 4 * T), span(slots, 8 * T),
+                        span(parents ? mask : nullptr, 4 * T * mask_words)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap(wr[i], rd[j])) return TQ_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(wr[i], wr[j])) return TQ_ERR_INVALID_ARG;
+    }
+    if (!device_accessible(table.block_table) || !device_accessible(table.lens) || !device_accessible(counts) ||
+        !device_accessible(cu_q) || (T && (!device_accessible(positions) || !device_accessible(slots))) ||
+        (parents && (!device_accessible(parents) || (T && !device_accessible(mask)))))
+        return TQ_ERR_INVALID_ARG;
+    tq::StepSlotsCall c = {};
+    c.table = table;
+    c.counts = counts;
+    c.parents = parents;
+    c.cu_q = cu_q;
+    c.positions = positions;
+    c.slots = slots;
+    c.mask = mask;
+    c.n_tokens = n_tokens;
+    c.n_pages = n_pages;
+    c.n_seqs = n_seqs;
+    c.max_pages = max_pages;
+    c.page_shift = shift;
+    c.words = mask_words;
+    const cudaError_t e = tq::launch_slots(c, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
+tq_status tq_append_slots(const tq_plan* plan, int k_bits, int v_bits, const void* k_new, int64_t k_stride,
+                          const void* v_new, int64_t v_stride, tq_dtype dtype, int64_t n_tokens, int Hkv,
+                          tq_paged_cache cache, const int64_t* slots, tq_stream_t stream) {
+    if (!plan || n_tokens < 0 || Hkv <= 0 || cache.n_pages < 1) return TQ_ERR_INVALID_ARG;
+    if (!valid_bits(k_bits) || !valid_bits(v_bits) || !valid_dtype(dtype)) return TQ_ERR_UNSUPPORTED;
+    const tq::Plan* P = reinterpret_cast<const tq::Plan*>(plan);
+    const int shift = page_shift_of(cache.page_size);
+    if (P->d < 32 || shift < 0 || n_tokens > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return TQ_OK;
+    if (!k_new || !v_new || !slots || !paged_pointers_ok(cache)) return TQ_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)Hkv * P->d, size = dtype == TQ_BF16 ? 2 : 4;
+    if (n_tokens > 1 && (k_stride < row || v_stride < row)) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || (n_tokens > 1 && (k_stride * size % 16 || v_stride * size % 16)) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u) || !paged_aligned(cache))
+        return TQ_ERR_ALIGNMENT;
+    if (!device_accessible(k_new) || !device_accessible(v_new) || !device_accessible(slots) || !paged_accessible(cache))
+        return TQ_ERR_INVALID_ARG;
+    tq::RowParams PK, PV;
+    fill_row_params(*P, k_bits, PK);
+    fill_row_params(*P, v_bits, PV);
+    const tq::SlotRows r{k_new, v_new, k_stride, v_stride, slots, n_tokens, cache.n_pages, Hkv, shift};
+    const tq_cache_view view = paged_as_view(cache);
+    const cudaError_t e = dispatch_d(P->d, [&](auto D) {
+        return tq::launch_append_slots_d<decltype(D)::value>(k_bits, v_bits, dtype, r, view, PK, PV,
+                                                             reinterpret_cast<cudaStream_t>(stream));
+    });
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
+tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const int32_t* counts, const int32_t* keep,
+                        int max_keep, const int32_t* n_keep, int32_t* new_lens, const tq_paged_cache* layers,
+                        int n_layers, int Hkv, int d, int k_bits, int v_bits, tq_stream_t stream) {
+    if (n_seqs < 1 || max_pages < 1 || max_keep < 1) return TQ_ERR_INVALID_ARG;
+    const tq_status st = check_layers(layers, n_layers, Hkv, d, k_bits, v_bits);
+    if (st != TQ_OK) return st;
+    const int shift = page_shift_of(layers[0].page_size);
+    if (((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows || max_keep > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+    if (!table.block_table || !table.lens || !table.refs || !counts || !keep || !n_keep || !new_lens)
+        return TQ_ERR_INVALID_ARG;
+    if (!aligned4(table.block_table) || !aligned4(table.lens) || !aligned4(table.refs) || !aligned4(counts) ||
+        !aligned4(keep) || !aligned4(n_keep) || !aligned4(new_lens))
+        return TQ_ERR_ALIGNMENT;
+    auto span = [](const void* p, uint64_t n) { return Span{reinterpret_cast<uintptr_t>(p), 4 * n}; };
+    const uint64_t n = (uint64_t)n_seqs;
+    const Span wr = span(new_lens, n);
+    for (const Span& rd : {span(table.block_table, n * max_pages), span(table.lens, n),
+                           span(table.refs, (uint64_t)layers[0].n_pages), span(counts, n), span(keep, n * max_keep),
+                           span(n_keep, n)})
+        if (overlap(wr, rd)) return TQ_ERR_INVALID_ARG;
+    if (!device_accessible(table.block_table) || !device_accessible(table.lens) || !device_accessible(table.refs) ||
+        !device_accessible(counts) || !device_accessible(keep) || !device_accessible(n_keep) ||
+        !device_accessible(new_lens) || !layers_accessible(layers, n_layers))
+        return TQ_ERR_INVALID_ARG;
+    tq::StepKeepCall c = {};
+    c.table = table;
+    c.counts = counts;
+    c.keep = keep;
+    c.n_keep = n_keep;
+    c.new_lens = new_lens;
+    c.n_seqs = n_seqs;
+    c.max_pages = max_pages;
+    c.max_keep = max_keep;
+    c.page_shift = shift;
+    c.layers = layers;
+    c.n_layers = n_layers;
+    c.Hkv = Hkv;
+    c.d = d;
+    c.k_bits = k_bits;
+    c.v_bits = v_bits;
+    const cudaError_t e = tq::launch_keep(c, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
 size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d) {
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 32 && d != 64 && d != 128 && d != 256)) return 0;
     return tq::prefill_paged_ws_bytes(d, tq::num_sms());
@@ -1116,13 +1240,24 @@ void level_bytes(const tq::Plan& P, int bits, uint32_t* w) {
 }
 }  // namespace
 
-tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
-                                tq_paged_cache cache, const int32_t* block_table, int max_pages,
-                                const int32_t* cu_q, const int32_t* ctx_lens, int window, int k_bits, int v_bits,
-                                float scale, void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                                tq_stream_t stream) {
+namespace {
+// What the query rows attend to: window and sinks, or a tree's mask.
+struct Seen {
+    int mode, window, sinks, words;
+    const uint32_t* mask;
+};
+
+// Attention of several query tokens per sequence over the paged cache: the
+// checks and the launch that its public calls share.
+tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
+                            const tq_paged_cache& cache, const int32_t* block_table, int max_pages,
+                            const int32_t* cu_q, const int32_t* ctx_lens, Seen seen, int k_bits, int v_bits,
+                            float scale, void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                            tq_stream_t stream) {
+    const int window = seen.window;
+    const bool tree = seen.mode == tq::kPpTree;
     if (!plan || B < 0 || n_q < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_pages < 1 || cache.n_pages < 1 ||
-        window < 0 || !std::isfinite(scale))
+        window < 0 || seen.sinks < 0 || (tree && seen.words < 1) || !std::isfinite(scale))
         return TQ_ERR_INVALID_ARG;
     const tq::Plan* P = reinterpret_cast<const tq::Plan*>(plan);
     const int shift = page_shift_of(cache.page_size);
@@ -1131,12 +1266,13 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
         return TQ_ERR_UNSUPPORTED;
     // positions, rows of a KV head and page ids are 32-bit numbers
     if (((int64_t)max_pages << shift) > (int64_t(1) << 30) || n_q > INT32_MAX / (Hq / Hkv) - 256 ||
-        cache.n_pages > INT32_MAX || B > (1 << 20))
+        cache.n_pages > INT32_MAX || B > (1 << 20) || seen.words > TQ_TREE_MAX_WORDS)
         return TQ_ERR_UNSUPPORTED;
     if (B == 0 || n_q == 0) return TQ_OK;
-    if (!q || !out || !block_table || !cu_q || !ctx_lens || !paged_pointers_ok(cache)) return TQ_ERR_INVALID_ARG;
+    if (!q || !out || !block_table || !cu_q || !ctx_lens || !paged_pointers_ok(cache) || (tree && !seen.mask))
+        return TQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned4(block_table) || !aligned4(cu_q) || !aligned4(ctx_lens) ||
-        !paged_aligned(cache) || !aligned16(cache.k_norm) || !aligned16(cache.v_norm))
+        !paged_aligned(cache) || !aligned16(cache.k_norm) || !aligned16(cache.v_norm) || !aligned4(seen.mask))
         return TQ_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < tq::prefill_paged_ws_bytes(P->d, tq::num_sms())) return TQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TQ_ERR_ALIGNMENT;
@@ -1144,10 +1280,12 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
     const Span rd = {reinterpret_cast<uintptr_t>(q), 2 * n_el};
     const Span wr = {reinterpret_cast<uintptr_t>(out), n_el * (out_dtype == TQ_BF16 ? 2 : 4)};
     const Span ws = {reinterpret_cast<uintptr_t>(workspace), tq::prefill_paged_ws_bytes(P->d, tq::num_sms())};
-    if (overlap(rd, wr) || overlap(rd, ws) || overlap(wr, ws)) return TQ_ERR_INVALID_ARG;
+    const Span bits = {reinterpret_cast<uintptr_t>(seen.mask), 4 * (uint64_t)n_q * seen.words};
+    if (overlap(rd, wr) || overlap(rd, ws) || overlap(wr, ws) || overlap(bits, wr) || overlap(bits, ws))
+        return TQ_ERR_INVALID_ARG;
     if (!device_accessible(q) || !device_accessible(out) || !device_accessible(block_table) ||
         !device_accessible(cu_q) || !device_accessible(ctx_lens) || !device_accessible(workspace) ||
-        !paged_accessible(cache))
+        !paged_accessible(cache) || (tree && !device_accessible(seen.mask)))
         return TQ_ERR_INVALID_ARG;
     tq::PagedPrefillCall c = {};
     for (int i = 0; i < P->d; ++i) {
@@ -1174,16 +1312,67 @@ tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q,
     c.max_pages = max_pages;
     c.page_shift = shift;
     // a window past every length is none: below 2^30 a position minus it stays in 32 bits
-    c.window = window >= ((int64_t)max_pages << shift) ? 0 : window;
+    const int64_t cap = (int64_t)max_pages << shift;
+    c.window = window >= cap ? 0 : window;
+    c.sinks = (int)(seen.sinks < cap ? seen.sinks : cap);
+    c.mask = seen.mask;
+    c.mask_words = seen.words;
+    // without a window (or without sinks) there is nothing that the sinks add
+    const int mode = seen.mode == tq::kPpSinks && (c.window == 0 || c.sinks == 0) ? (int)tq::kPpCausal : seen.mode;
     c.k_bits = k_bits;
     c.v_bits = v_bits;
     c.out_bf16 = out_dtype == TQ_BF16;
     level_bytes(*P, k_bits, c.k_levels);
     level_bytes(*P, v_bits, c.v_levels);
     const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
-        return tq::launch_prefill_paged<decltype(D)::value>(c, reinterpret_cast<cudaStream_t>(stream));
+        constexpr int d = decltype(D)::value;
+        auto st = reinterpret_cast<cudaStream_t>(stream);
+        switch (mode) {
+            case tq::kPpTree: return tq::launch_prefill_paged<d, tq::kPpTree>(c, st);
+            case tq::kPpSinks: return tq::launch_prefill_paged<d, tq::kPpSinks>(c, st);
+            default: return tq::launch_prefill_paged<d, tq::kPpCausal>(c, st);
+        }
     });
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+}  // namespace
+
+tq_status tq_attn_prefill_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
+                                tq_paged_cache cache, const int32_t* block_table, int max_pages,
+                                const int32_t* cu_q, const int32_t* ctx_lens, int window, int k_bits, int v_bits,
+                                float scale, void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                tq_stream_t stream) {
+    return attn_tokens_paged(plan, q, n_q, B, Hq, Hkv, cache, block_table, max_pages, cu_q, ctx_lens,
+                             {tq::kPpCausal, window, 0, 0, nullptr}, k_bits, v_bits, scale, out, out_dtype, workspace,
+                             workspace_bytes, stream);
+}
+
+size_t tq_attn_sinks_paged_workspace_bytes(int Hq, int Hkv, int d) {
+    return tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d);
+}
+
+tq_status tq_attn_sinks_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
+                              tq_paged_cache cache, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                              const int32_t* ctx_lens, int window, int sinks, int k_bits, int v_bits, float scale,
+                              void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                              tq_stream_t stream) {
+    return attn_tokens_paged(plan, q, n_q, B, Hq, Hkv, cache, block_table, max_pages, cu_q, ctx_lens,
+                             {tq::kPpSinks, window, sinks, 0, nullptr}, k_bits, v_bits, scale, out, out_dtype,
+                             workspace, workspace_bytes, stream);
+}
+
+size_t tq_attn_tree_paged_workspace_bytes(int Hq, int Hkv, int d) {
+    return tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d);
+}
+
+tq_status tq_attn_tree_paged(const tq_plan* plan, const void* q, int64_t n_q, int B, int Hq, int Hkv,
+                             tq_paged_cache cache, const int32_t* block_table, int max_pages, const int32_t* cu_q,
+                             const int32_t* ctx_lens, const uint32_t* mask, int mask_words, int k_bits, int v_bits,
+                             float scale, void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                             tq_stream_t stream) {
+    return attn_tokens_paged(plan, q, n_q, B, Hq, Hkv, cache, block_table, max_pages, cu_q, ctx_lens,
+                             {tq::kPpTree, 0, 0, mask_words, mask}, k_bits, v_bits, scale, out, out_dtype, workspace,
+                             workspace_bytes, stream);
 }
 
 size_t tq_attn_prefill_workspace_bytes(int B, int T, int Hq, int Hkv, int64_t cap, int d) {

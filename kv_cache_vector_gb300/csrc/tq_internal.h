@@ -374,11 +374,16 @@ struct PagedPrefillCall {
     void* workspace;
     int64_t n_q;
     int B, Hq, Hkv, max_pages, page_shift, window, k_bits, v_bits, out_bf16;
+    int sinks;             // kPpSinks
+    const uint32_t* mask;  // kPpTree: [n_q][mask_words]
+    int mask_words;
     // the levels as fp16 bytes: high bytes of eight levels in words 0 and 1,
     // their low bytes in words 4 and 5 (4 bits: the eight positive ones)
     uint32_t k_levels[8], v_levels[8];
 };
-template <int D>
+// What a query row attends to (tq_paged_parts.cuh).
+enum { kPpCausal = 0, kPpSinks = 1, kPpTree = 2 };
+template <int D, int MODE>
 cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s);
 
 // Paged append of one token per sequence, d >= 32 (tq_codec.cu).
@@ -406,6 +411,46 @@ struct PagesCall {
 };
 size_t pages_workspace_bytes(int n_seqs, int64_t n_pages);
 cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s);
+
+// Append of rows at given slots, d >= 32 (tq_codec.cu): token t's row of KV head
+// h is at k_new + t * k_stride + h * d elements.
+struct SlotRows {
+    const void* k_new;
+    const void* v_new;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+    int64_t n_tokens, n_pages;
+    int Hkv, page_shift;
+};
+template <int D>
+cudaError_t launch_append_slots_d(int k_bits, int v_bits, tq_dtype dt, const SlotRows& r, const tq_cache_view& pages,
+                                  const RowParams& PK, const RowParams& PV, cudaStream_t s);
+
+// A step's slot map and its kept tokens (tq_steps.cu); arguments checked by the
+// caller.
+struct StepSlotsCall {
+    tq_page_table table;
+    const int32_t* counts;
+    const int32_t* parents;
+    int32_t* cu_q;
+    int32_t* positions;
+    int64_t* slots;
+    uint32_t* mask;
+    int64_t n_tokens, n_pages;
+    int n_seqs, max_pages, page_shift, words;
+};
+cudaError_t launch_slots(const StepSlotsCall& c, cudaStream_t s);
+struct StepKeepCall {
+    tq_page_table table;
+    const int32_t* counts;
+    const int32_t* keep;
+    const int32_t* n_keep;
+    int32_t* new_lens;
+    int n_seqs, max_pages, max_keep, page_shift;
+    const tq_paged_cache* layers;
+    int n_layers, Hkv, d, k_bits, v_bits;
+};
+cudaError_t launch_keep(const StepKeepCall& c, cudaStream_t s);
 
 // Shared launch helpers (tq_launch.cpp).
 int num_sms();

@@ -3,7 +3,8 @@
 //
 // Sequence b has n_b query tokens (rows cu_q[b] .. cu_q[b + 1] - 1 of q), the
 // last n_b of its ctx_b positions; token t sits at p = ctx_b - n_b + t and
-// attends over positions max(0, p - window + 1) .. p:
+// attends over positions max(0, p - window + 1) .. p (or, by MODE, over the
+// sinks too, or as a node of a tree: tq_paged_parts.cuh):
 //   out = R^-1 ( sum_j p_j n^v_j c[v_j] ),  p = softmax_j( scale n^k_j <R q, c[k_j]> )
 // with R the codec's rotation, c the codebook's levels and n the rows' norms.
 //
@@ -79,22 +80,16 @@
 #include <climits>
 #include <type_traits>
 
-#include "tq_async.cuh"
-#include "tq_device.cuh"
+#include "tq_paged_parts.cuh"
 #include "tq_tmem.cuh"
 #include "tq_umma.cuh"
 
-#if !defined(TQ_UNIT_D)
-#error "compile once per head dimension with -DTQ_UNIT_D=<d>"
+#if !defined(TQ_UNIT_D) || !defined(TQ_UNIT_MODE)
+#error "compile once per head dimension and mode with -DTQ_UNIT_D=<d> -DTQ_UNIT_MODE=<mode>"
 #endif
 
 namespace tq {
 namespace dev {
-
-constexpr int kPpStatusRange = 71;  // cu_q or ctx_lens outside their ranges
-constexpr int kPpStatusPage = 72;   // a page id outside [0, n_pages)
-constexpr int kPpStatusWait = 73;   // a wait gave up
-constexpr int kPpStatusAlign = 74;  // shared memory not 1024-byte aligned
 
 // Sizes for head dimension D.
 template <int D>
@@ -136,191 +131,6 @@ struct PpGeo {
     static constexpr uint32_t kSmem = (kMisc + 8 + 127) / 128 * 128;
     static constexpr uint32_t kTmemS = 0, kTmemO = 256;  // buffer b at kN b; output g at 128 g further
 };
-
-struct PpArgs {
-    const __nv_bfloat16* q;
-    void* out;
-    const int32_t* cu;
-    const int32_t* ctx;
-    const int32_t* bt;
-    tq_paged_cache c;
-    float* part;   // [shares][2] parts
-    int32_t* meta;  // [shares][kPpMeta]
-    int64_t n_q;
-    int B, Hq, Hkv, max_pages, shift, window, k_bits, v_bits, out_bf16;
-    uint32_t khi[4], klo[4], vhi[4], vlo[4];  // level bytes (see expand)
-};
-// what a share left: bit 0 a part of the item it starts in, bit 1 one of the
-// item it owns (which starts in this share and ends in the share kMetaLast;
-// -1: none), that item's first row of q, KV head, rows.  kShareFailed: a wait
-// gave up in the share, and its parts may be missing
-enum { kMetaHas = 0, kMetaLast, kMetaQ0, kMetaH, kMetaRow0, kMetaRows, kPpMeta = 8 };
-constexpr int kShareFailed = 4;
-
-// Where a share starts or goes on: sequence, row tile, KV head, and the units
-// (or, where the share is one part of an item, the parts) of the item that
-// belong to earlier shares.
-struct PpCursor {
-    int b, i, h;
-    int64_t off;
-    int64_t left;  // units of this share from here on
-    int n, ctx, q0;  // the sequence's lengths and first row of q
-    int parts;       // > 0: the share is part `off` of so many of one item
-};
-
-// Weights and ranges of sequence b's items.  A unit line position is only an
-// estimate of cost: any consistent weight gives a correct cut.
-template <int D>
-struct PpSeq {
-    using Z = PpGeo<D>;
-    int n, ctx, q0, tiles = 0, rows;
-    int64_t base, cap, kstar, over;
-    int G;
-
-    __device__ void load(const PpArgs& A, int b, int* status) {
-        const int64_t c0 = A.cu[b], c1 = A.cu[b + 1];
-        const int len = A.ctx[b];
-        if (c0 < 0 || c1 < c0 || c1 > A.n_q || len < 0 || len > ((int64_t)A.max_pages << A.shift) ||
-            (c1 - c0) * (A.Hq / A.Hkv) > INT32_MAX) {
-            if (status) report_timeout(status, kPpStatusRange);
-            set(A, 0, 0, 0);
-        } else {
-            set(A, (int)(c1 - c0), len, (int)c0);
-        }
-    }
-    __device__ void set(const PpArgs& A, int tokens, int len, int first) {
-        n = tokens;
-        ctx = len;
-        q0 = first;
-        G = A.Hq / A.Hkv;
-        rows = n * G;
-        tiles = (rows + Z::kRows - 1) / Z::kRows;
-        base = ctx > n ? (int64_t)(ctx - n) * G : 0;
-        cap = A.window > 0 ? (int64_t)A.window * G + Z::kRows : INT64_MAX;
-        // tiles before the window's cap binds: base + (k + 1) kRows < cap
-        kstar = cap == INT64_MAX ? INT32_MAX : (cap - base - 1) / Z::kRows;
-        if (cap - base - 1 < 0) kstar = 0;
-        over = (int64_t)Z::kCostItem * Z::kN * G;
-    }
-    __device__ int factor(int i) const {
-        return rows - (int64_t)i * Z::kRows > 128 ? Z::kCostPair : Z::kCostSplit;
-    }
-    __device__ int64_t weight(int i) const { return work(i) + over; }
-    __device__ int64_t work(int i) const {  // without the item's own cost
-        const int64_t e = base + min((int64_t)(i + 1) * Z::kRows, (int64_t)rows);
-        return factor(i) * min(e, cap);
-    }
-    // sum of the weights of tiles 0 .. i - 1
-    __device__ int64_t before(int i) const {
-        if (i <= 0) return 0;
-        if (i == tiles) return before(i - 1) + weight(i - 1);
-        const int64_t m = min((int64_t)i, kstar);
-        int64_t s = m * base + (int64_t)Z::kRows * (m * (m + 1) / 2);
-        if (i > m) s += (i - m) * cap;
-        return Z::kCostPair * s + i * over;
-    }
-};
-
-// One part of an item: blocks [blk0, blk1) of the item's nblk, its first
-// position and the share's bookkeeping.
-struct PpPart {
-    int b, i, h;
-    int row0, rows;      // first row within (sequence, KV head); valid rows
-    int lo_blk;          // first block of the item
-    int blk0, blk1, nblk;
-    int kv_lo, kv_end;   // the positions that some row attends to
-    int pair;            // the two streams take two row tiles
-    bool head, whole;    // part starts the item; covers it
-};
-
-// The block at which a cut `off` units into an item of w units falls.  The
-// item's own cost lies in front of its blocks: a share that starts inside an
-// item pays it once more, nearly every share does, and so the shares stay
-// equal.  Any rounding will do that never decreases and is the same for every
-// CTA.
-__device__ __forceinline__ int pp_cut(int nblk, int64_t off, int64_t w, int64_t over) {
-    return off >= w ? nblk
-                    : off <= over ? 0 : min(nblk, (int)((float)nblk * __fdividef((float)(off - over), (float)(w - over))));
-}
-
-// Blocks of row tile i, the first of them, and its first position and their end.
-template <int D>
-__device__ __forceinline__ int pp_blocks(const PpArgs& A, const PpSeq<D>& q, int i, int* lo_blk = nullptr,
-                                         int* kv_lo = nullptr, int* kv_end = nullptr) {
-    using Z = PpGeo<D>;
-    const int row0 = i * Z::kRows, rows = min(Z::kRows, q.rows - row0);
-    const int first_pos = q.ctx - q.n + row0 / q.G;
-    const int end = max(0, q.ctx - q.n + (row0 + rows - 1) / q.G + 1);
-    const int at = A.window > 0 ? max(0, first_pos - A.window + 1) : 0, lo = at / Z::kN;
-    if (lo_blk) *lo_blk = lo;
-    if (kv_lo) *kv_lo = at;
-    if (kv_end) *kv_end = end;
-    return max(0, (end + Z::kN - 1) / Z::kN - lo);
-}
-
-// Rows and blocks of item p.b, p.i, p.h.
-template <int D>
-__device__ __forceinline__ void pp_rows(const PpArgs& A, const PpSeq<D>& q, PpPart& p) {
-    using Z = PpGeo<D>;
-    p.row0 = p.i * Z::kRows;
-    p.rows = min(Z::kRows, q.rows - p.row0);
-    p.pair = Z::kStreams == 2 && p.rows > 128;
-    p.nblk = pp_blocks<D>(A, q, p.i, &p.lo_blk, &p.kv_lo, &p.kv_end);
-}
-
-// The share's next part with work in it; advances the cursor.  False at the
-// end of the share.  Items without blocks (no position to attend to) come as
-// a whole part with blk0 == blk1, to the share that holds their start.
-template <int D>
-__device__ bool pp_next(const PpArgs& A, PpCursor& c, PpSeq<D>& q, PpPart& p) {
-    using Z = PpGeo<D>;
-    while (c.left > 0) {
-        while (c.i >= q.tiles) {  // next sequence with rows
-            if (++c.b >= A.B) {
-                c.left = 0;
-                return false;
-            }
-            q.load(A, c.b, nullptr);
-            c.i = 0;
-            c.h = 0;
-        }
-        const int64_t w = q.weight(c.i);
-        const int64_t end = min(w, c.off + c.left);
-        p.b = c.b;
-        p.i = c.i;
-        p.h = c.h;
-        pp_rows<D>(A, q, p);
-        p.blk0 = pp_cut(p.nblk, c.off, w, q.over);
-        p.blk1 = pp_cut(p.nblk, end, w, q.over);
-        p.head = c.off == 0;
-        p.whole = p.nblk == 0 ? p.head : (p.blk0 == 0 && p.blk1 == p.nblk);
-        c.left -= end - c.off;
-        c.off = end;
-        if (c.off >= w) {  // on to the next item
-            c.off = 0;
-            if (++c.h >= A.Hkv) {
-                c.h = 0;
-                ++c.i;
-            }
-        }
-        if (p.whole || p.blk1 > p.blk0) return true;
-    }
-    return false;
-}
-
-// A part as the copy warp hands it to the others, through shared memory.
-struct PpJob {
-    int nb;        // blocks, -1: no more parts
-    int flags;     // kJob*
-    int q0;        // the sequence's first row of q
-    int h;         // KV head
-    int row0, rows;  // first row within (sequence, KV head); valid rows
-    int blk;       // first block
-    int kv_lo, kv_end;  // positions before the one and from the other on are not read
-    int pos0;      // position of the sequence's token 0
-    int tok0, rest;  // row0 / G and row0 % G
-};
-enum { kJobPair = 1, kJobWhole = 2, kJobHead = 4 };
 
 // Chunk c (8 dims, 16 bytes) of row r of a query tile.
 __device__ __forceinline__ unsigned char* pp_place(unsigned char* tile, int r, int c) {
@@ -625,25 +435,25 @@ __device__ __forceinline__ void pp_across(uint32_t t, uint32_t (&y)[PARTS][16]) 
             }
 }
 
-// Scores outside columns [c0, c1) of 32 become -inf.
-__device__ __forceinline__ void pp_mask(uint32_t (&s)[32], int c0, int c1) {
-    const uint32_t on = (c1 >= 32 ? 0xFFFFFFFFu : c1 <= 0 ? 0u : (1u << c1) - 1u) &
-                        (c0 <= 0 ? 0xFFFFFFFFu : c0 >= 32 ? 0u : ~((1u << c0) - 1u));
+// Scores whose bit is not set become -inf.
+__device__ __forceinline__ void pp_mask(uint32_t (&s)[32], uint32_t on) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) s[k] = (on >> k) & 1u ? s[k] : 0xFF800000u;
 }
 
 // A wide block's scores, 16 columns from column c on, times their own factors;
-// columns outside [c0, c1) become -inf.
-__device__ __forceinline__ void pp_wide16(uint32_t t_s, const unsigned char* cols, float cq, int c, int c0, int c1,
-                                          float (&x)[16]) {
+// columns that are not the row's become -inf.
+template <int MODE>
+__device__ __forceinline__ void pp_wide16(uint32_t t_s, const unsigned char* cols, float cq, int c,
+                                          const PpVis<MODE>& vis, float (&x)[16]) {
+    const uint32_t on = vis.word(c);
     uint32_t s[16];
     tmem_ld16(t_s + c, s);
     tmem_wait_ld();
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const int e = *reinterpret_cast<const volatile int8_t*>(cols + 2 * (c + k));
-        x[k] = c + k < c0 || c + k >= c1 ? -INFINITY : __uint_as_float(s[k]) * (cq * pp_pow2(e));
+        x[k] = (on >> k) & 1u ? __uint_as_float(s[k]) * (cq * pp_pow2(e)) : -INFINITY;
     }
 }
 // A wide block becomes one without powers of two: its scores times their factors
@@ -651,13 +461,13 @@ __device__ __forceinline__ void pp_wide16(uint32_t t_s, const unsigned char* col
 // and the block's maximum score, and the row's sum of 2^(s - that).  (A call by
 // itself, with values only: inlined in the step it took registers and instruction
 // cache from all steps, 1.37 -> 1.63 ms for the long chunks.)
-template <int N>
-__device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, float cq, int c0, int c1, float m) {
+template <int N, int MODE>
+__device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, float cq, PpVis<MODE> vis, float m) {
     float sum = 0.f;
 #pragma unroll 1
     for (int c = 0; c < N; c += 16) {
         float x[16];
-        pp_wide16(t_s, cols, cq, c, c0, c1, x);
+        pp_wide16(t_s, cols, cq, c, vis, x);
 #pragma unroll
         for (int k = 0; k < 16; ++k) m = fmaxf(m, x[k]);
     }
@@ -666,7 +476,7 @@ __device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, 
     for (int c = 0; c < N; c += 16) {
         float x[16];
         uint32_t w[16];
-        pp_wide16(t_s, cols, cq, c, c0, c1, x);
+        pp_wide16(t_s, cols, cq, c, vis, x);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             sum += pp_exp2(x[k] - mr);
@@ -697,11 +507,11 @@ __device__ __forceinline__ int pp_exponent(uint32_t m) { return min(100, max(-10
 // The factors of a wide block (norms kn and, behind them, vn), and its
 // positions' powers of two.
 template <int N>
-__device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint32_t segs, int from, int lim,
-                                           int seg_sh) {
+__device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint32_t segs, int from, int snk,
+                                           int lim, int seg_sh) {
 #pragma unroll 1
     for (int r = threadIdx.x & 31; r < N; r += 32) {
-        const bool in = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+        const bool in = (r >= from || r < snk) && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
         const float k = in ? kn[r] : 0.f, v = in ? kn[N + r] : 0.f;
         const int ek = pp_exponent(pp_finite(k)), ev = pp_exponent(pp_finite(v));
         kn[r] = fmaf(v, 0.f, k * pp_pow2(-ek));  // NaN if either norm is not finite
@@ -712,7 +522,7 @@ __device__ __noinline__ void pp_wide_norms(float* kn, unsigned char* cols, uint3
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(PpGeo<D>::kThreads, 1)
 k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefillConsts P, int* status) {
     using Z = PpGeo<D>;
@@ -789,7 +599,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     {
         const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
         const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
-        PpSeq<D> q;
+        PpSeq<Z, MODE> q;
         long long mine = 0;
         int items = 0;
         float most = 0.f;  // the largest item's work
@@ -942,7 +752,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                                                                                              : (const void*)A.c.v_norm);
         const uint32_t at = a == 0 ? 0u : a == 1 ? N * D / 2 : a == 2 ? N * D : N * D + 4 * N;
         PpCursor cur = *start;
-        PpSeq<D> seq;
+        PpSeq<Z, MODE> seq;
         if (cur.left > 0 || cur.parts > 0) seq.set(A, cur.n, cur.ctx, cur.q0);
         uint32_t tc = 0;
         int has = 0;  // parts left in the workspace
@@ -952,7 +762,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             bool more;
             if (cur.parts > 0) {  // the one part of this share
                 u.b = cur.b, u.i = cur.i, u.h = cur.h;
-                pp_rows<D>(A, seq, u);
+                pp_rows(A, seq, u);
                 const uint32_t nb = u.nblk, at = (uint32_t)cur.off, of = cur.parts;  // nb of < 2^32
                 u.blk0 = nb * at / of;
                 u.blk1 = nb * (at + 1) / of;
@@ -960,7 +770,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 u.whole = u.nblk == 0 ? u.head : (u.blk0 == 0 && u.blk1 == u.nblk);
                 more = job == 0 && (u.whole || u.blk1 > u.blk0);
             } else {
-                more = pp_next<D>(A, cur, seq, u);
+                more = pp_next(A, cur, seq, u);
             }
             if (job >= 2) ok = pp_wait(&job_free[job & 1], ((job >> 1) - 1) & 1, abort_f, status);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -988,16 +798,18 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             if (!more) break;
             if (!u.whole) has |= u.head ? 2 : 1;
             // this lane's segment of block j: its page, or -1; looked up a block ahead
+            auto block_at = [&](int j) { return pp_block_at<Z, MODE>(A, u.kv_lo, u.kv_end, u.lo_blk + j); };
             auto page_of = [&](int j) {
-                const int pos = (u.lo_blk + j) * N + s * seg;
-                return s < nseg && j < u.blk1 && pos < u.kv_end && pos + seg > u.kv_lo
+                const int pos = block_at(j) * N + s * seg;
+                return s < nseg && j < u.blk1 && pos < u.kv_end &&
+                               (pos + seg > u.kv_lo || (MODE == kPpSinks && pos < A.sinks))
                            ? A.bt[(int64_t)u.b * A.max_pages + (pos >> A.shift)]
                            : INT_MIN;
             };
             int next_page = page_of(u.blk0);
             for (int j = u.blk0; j < u.blk1; ++j, ++tc) {
                 const int st = tc % NS;
-                const int pos = (u.lo_blk + j) * N + s * seg;
+                const int pos = block_at(j) * N + s * seg;
                 const int page = next_page;
                 next_page = page_of(j + 1);
                 bool have = page != INT_MIN;
@@ -1029,14 +841,14 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             bool owner;
             if (cur.parts > 0) {
                 // (an item of one block is some share's whole)
-                owner = ok && cur.off == 0 && cur.parts > 1 && pp_blocks<D>(A, seq, cur.i) > 1;
+                owner = ok && cur.off == 0 && cur.parts > 1 && pp_blocks(A, seq, cur.i) > 1;
                 last += cur.parts - 1;
             } else {
                 owner = ok && cur.off > 0 &&
                         !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
                 if (owner) {
                     const int64_t w = seq.weight(cur.i), per = *share;
-                    const int nblk = pp_blocks<D>(A, seq, cur.i);
+                    const int nblk = pp_blocks(A, seq, cur.i);
                     // no join where one share has all of the item's blocks
                     owner = nblk > 0 && pp_cut(nblk, cur.off, w, seq.over) < nblk;
                     for (int64_t x = cur.off; x < w && pp_cut(nblk, x, w, seq.over) == 0; x += per)
@@ -1153,7 +965,9 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 ok = __all_sync(0xFFFFFFFFu, pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status));
                 if (!ok) break;
                 const uint32_t segs = reinterpret_cast<volatile uint32_t*>(sm + Z::kSegs)[st];
-                const int t0 = (p.blk + j) * N, from = p.kv_lo - t0, lim = p.kv_end - t0;  // the block's positions that count
+                const int t0 = pp_block_at<Z, MODE>(A, p.kv_lo, p.kv_end, p.blk + j) * N;
+                const int from = p.kv_lo - t0, lim = p.kv_end - t0;  // the block's positions that count
+                const int snk = MODE == kPpSinks ? A.sinks - t0 : 0;  // and the sinks among those in front
                 const int seg_sh = min(A.shift, N == 64 ? 6 : 7);
                 float kn[N / 32], vn[N / 32];
                 bool in[N / 32];
@@ -1162,7 +976,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
 #pragma unroll
                 for (int k = 0; k < N / 32; ++k) {
                     const int r = 32 * k + lane;
-                    in[k] = r >= from && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
+                    in[k] = (r >= from || r < snk) && r < lim && ((segs >> (4 * (r >> seg_sh))) & 1u);
                     kn[k] = in[k] ? knp[r] : 0.f;
                     vn[k] = in[k] ? vnp[r] : 0.f;
                     const uint32_t x = pp_finite(kn[k]), y = pp_finite(vn[k]);
@@ -1193,7 +1007,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     if (wides) ok = __all_sync(0xFFFFFFFFu, pp_wait(cols_free, (wides - 1) & 1, abort_f, status));
                     if (!ok) break;
                     ++wides;
-                    pp_wide_norms<N>(knp, sm + Z::kCols, segs, from, lim, seg_sh);
+                    pp_wide_norms<N>(knp, sm + Z::kCols, segs, from, snk, lim, seg_sh);
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -1306,6 +1120,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
             // a warp without rows only keeps the barriers' count
             const bool rows_here = __any_sync(0xFFFFFFFFu, rvalid);
             const int lo = A.window > 0 ? max(0, pos - A.window + 1) : 0;
+            const uint32_t* mask_row = MODE == kPpTree && rvalid ? A.mask + ((int64_t)p.q0 + tok) * A.words : nullptr;
             // ---- queries: each thread rotates its row in registers and tensor
             // memory (the output columns, free until the item's first product), 64
             // dims at a time, and rounds it to fp16 under a power of two.  A warp
@@ -1421,15 +1236,29 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     }
                     tc_fence_after();
                     const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
-                    const int t0 = (p.blk + j) * N;
-                    // columns [c0, c1) of the block are this row's
-                    const int c1 = min(N, pos + 1 - t0), c0 = max(0, lo - t0);
-                    const bool full = __all_sync(0xFFFFFFFFu, !rvalid || (c1 == N && c0 == 0));
+                    const int t0 = pp_block_at<Z, MODE>(A, p.kv_lo, p.kv_end, p.blk + j) * N;
+                    PpVis<MODE> vis;  // the columns of the block that are this row's
+                    bool all = true;
+                    if constexpr (MODE == kPpTree) {
+                        vis.row = mask_row;
+                        vis.words = rvalid ? A.words : 0;
+                        vis.node0 = p.pos0 - t0;
+                        vis.end = rvalid ? p.kv_end - t0 : 0;
+                        all = vis.node0 >= N;
+                    } else {
+                        vis.c1 = min(N, pos + 1 - t0), vis.c0 = max(0, lo - t0);
+                        if constexpr (MODE == kPpSinks) {
+                            vis.cs = min(vis.c1, A.sinks - t0);
+                            if (vis.cs >= vis.c0) vis.c0 = 0;
+                        }
+                        all = vis.c1 == N && vis.c0 == 0;
+                    }
+                    const bool full = __all_sync(0xFFFFFFFFu, !rvalid || all);
                     // not 0, which a masked score of -inf would make NaN: tiny queries over tiny norms
                     float cs = fmaxf(cq * meta.x, FLT_MIN), ev = meta.y;
                     float2 w2;  // a wide block's
                     if (kWide) {
-                        w2 = pp_wide<N>(t_s, sm + Z::kCols, cq, c0, c1, m);
+                        w2 = pp_wide<N>(t_s, sm + Z::kCols, cq, vis, m);
                         cs = 1.f, ev = 0.f;
                         __syncwarp();
                         if (lane <= (split ? 1 : 0)) mbar_arrive(cols_free);
@@ -1444,7 +1273,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                             uint32_t s[32];
                             tmem_ld32(t_s + c, s);
                             tmem_wait_ld();
-                            pp_mask(s, c0 - c, c1 - c);
+                            pp_mask(s, vis.word(c));
                             mx = fmaxf(mx, pp_max32(s));
                         }
                     }
@@ -1479,7 +1308,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                         uint32_t s[32];
                         tmem_ld32(t_s + c, s);
                         tmem_wait_ld();
-                        if (!full) pp_mask(s, c0 - c, c1 - c);
+                        if (!full) pp_mask(s, vis.word(c));
                         uint32_t w[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -1752,7 +1581,7 @@ k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ P
 
 }  // namespace dev
 
-template <int D>
+template <int D, int MODE>
 cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     const PagedPrefillConsts& P = c.consts;
     using namespace dev;
@@ -1775,6 +1604,9 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     A.k_bits = c.k_bits;
     A.v_bits = c.v_bits;
     A.out_bf16 = c.out_bf16;
+    A.sinks = c.sinks;
+    A.mask = c.mask;
+    A.words = c.mask_words;
     for (int i = 0; i < 4; ++i) {
         A.khi[i] = c.k_levels[i];
         A.klo[i] = c.k_levels[4 + i];
@@ -1789,11 +1621,11 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(k_prefill_paged<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Z::kSmem);
+        e = cudaFuncSetAttribute(k_prefill_paged<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Z::kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
-    e = launch_pdl(k_prefill_paged<D>, dim3(shares), dim3(Z::kThreads), Z::kSmem, s, A, P, status_word());
+    e = launch_pdl(k_prefill_paged<D, MODE>, dim3(shares), dim3(Z::kThreads), Z::kSmem, s, A, P, status_word());
     if (e != cudaSuccess) return e;
     // groups of 32 rows that an item can have
     const int64_t rows = c.n_q * (c.Hq / c.Hkv);
@@ -1807,6 +1639,6 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     return launch_pdl(k_prefill_paged_join<D, 2>, dim3(shares, groups), dim3(256), 0, s, A, P);
 }
 
-template cudaError_t launch_prefill_paged<TQ_UNIT_D>(const PagedPrefillCall&, cudaStream_t);
+template cudaError_t launch_prefill_paged<TQ_UNIT_D, TQ_UNIT_MODE>(const PagedPrefillCall&, cudaStream_t);
 
 }  // namespace tq
