@@ -29,7 +29,8 @@ UNITS = ([("tq_api.cpp", {}), ("tq_launch.cu", {}), ("tq_noalloc.cu", {}), ("tq_
          + [("tq_attn_generic.cu", {"D": d, "KB": kb}) for d in ATTN_DIMS for kb in (2, 3, 4)]
          + [("tq_prefill.cu", {"KB": kb}) for kb in (2, 3, 4)]
          + [("tq_qjl.cu", {"D": d}) for d in (32, 64, 128)]
-         + [("tq_prefill_paged.cu", {"D": d, "MODE": m}) for d in ATTN_DIMS for m in (0, 1, 2)])
+         + [("tq_prefill_paged.cu", {"D": d, "MODE": m}) for d in ATTN_DIMS for m in (0, 1, 2)]
+         + [("tq_attn_few.cu", {"D": d, "MODE": m}) for d in ATTN_DIMS for m in (1, 2)])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

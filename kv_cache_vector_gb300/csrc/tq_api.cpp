@@ -1166,7 +1166,7 @@ tq_status tq_append_slots(const tq_plan* plan, int k_bits, int v_bits, const voi
     fill_row_params(*P, v_bits, PV);
     const tq::SlotRows r{k_new, v_new, k_stride, v_stride, slots, n_tokens, cache.n_pages, Hkv, shift};
     const tq_cache_view view = paged_as_view(cache);
-    const cudaError_t e = dispatch_d(P->d, [&](auto D) {
+    const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
         return tq::launch_append_slots_d<decltype(D)::value>(k_bits, v_bits, dtype, r, view, PK, PV,
                                                              reinterpret_cast<cudaStream_t>(stream));
     });
@@ -1226,6 +1226,11 @@ namespace {
 // The scale s under which the levels are kept in fp16: the plan's where it has
 // one (then every c * s is close to an fp16 value).
 double level_scale(const tq::Plan& P, int bits) { return P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0; }
+
+// Level c * s as fp16 (0 past the last).
+uint16_t level_half(const tq::Plan& P, int bits, int i) {
+    return i < 1 << bits ? __half_as_ushort(__float2half_rn((float)((double)P.c32[bits][i] * level_scale(P, bits)))) : 0;
+}
 
 // The levels c * s as fp16 bytes for the byte-permute lookups.
 void level_bytes(const tq::Plan& P, int bits, uint32_t* w) {
@@ -1324,12 +1329,19 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
     c.out_bf16 = out_dtype == TQ_BF16;
     level_bytes(*P, k_bits, c.k_levels);
     level_bytes(*P, v_bits, c.v_levels);
+    for (int i = 0; i < 16; ++i) {
+        c.k_cen[i] = level_half(*P, k_bits, i);
+        c.v_cen[i] = level_half(*P, v_bits, i);
+    }
+    const bool few = n_q * (Hq / Hkv) <= (int64_t)(P->d == 256 ? 8 : 16) * B;  // query rows per sequence and KV head
     const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
         constexpr int d = decltype(D)::value;
         auto st = reinterpret_cast<cudaStream_t>(stream);
         switch (mode) {
-            case tq::kPpTree: return tq::launch_prefill_paged<d, tq::kPpTree>(c, st);
-            case tq::kPpSinks: return tq::launch_prefill_paged<d, tq::kPpSinks>(c, st);
+            case tq::kPpTree:
+                return few ? tq::launch_attn_few<d, tq::kPpTree>(c, st) : tq::launch_prefill_paged<d, tq::kPpTree>(c, st);
+            case tq::kPpSinks:
+                return few ? tq::launch_attn_few<d, tq::kPpSinks>(c, st) : tq::launch_prefill_paged<d, tq::kPpSinks>(c, st);
             default: return tq::launch_prefill_paged<d, tq::kPpCausal>(c, st);
         }
     });

@@ -236,52 +236,6 @@ __global__ void __launch_bounds__(32 * kAppWarps) k_append_warp(const T* __restr
     }
 }
 
-// The append of a step's tokens at the slots that tq_pages_slots gives them: row
-// (t, h) goes to offset slots[t] % page_size of page slots[t] / page_size; a
-// negative slot has no token.  One warp per row, as k_append_warp.
-template <int D, typename T>
-__global__ void __launch_bounds__(32 * kAppWarps) k_append_slots(const SlotRows A, tq_cache_view cache, int k_bits,
-                                                                 int v_bits, const __grid_constant__ RowParams PK,
-                                                                 const __grid_constant__ RowParams PV, int* status) {
-    __shared__ uint32_t sg[D], sg2[D];
-    __shared__ uint8_t idxbuf[kAppWarps][D];
-    const bool is_v = blockIdx.y == 1;
-    const RowParams& P = is_v ? PV : PK;
-    for (int i = threadIdx.x; i < D; i += blockDim.x) {
-        sg[i] = sign_mask(P.sgnb, i);
-        sg2[i] = sign_mask(P.sgn2b, i);
-    }
-    __syncthreads();
-    griddep_wait();    // the new rows and slots, and readers of the cache, of the previous kernel
-    griddep_launch();  // the next kernel may set itself up; it waits for this grid
-    const int bits = is_v ? v_bits : k_bits;
-    const T* src = static_cast<const T*>(is_v ? A.v_new : A.k_new);
-    const int64_t stride = is_v ? A.v_stride : A.k_stride;
-    uint8_t* pk = is_v ? cache.v_packed : cache.k_packed;
-    float* nrm = is_v ? cache.v_norm : cache.k_norm;
-    const int rb = D * bits / 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* ib = idxbuf[warp];
-    const int64_t rows = A.n_tokens * A.Hkv;
-    for (int64_t r = (int64_t)blockIdx.x * kAppWarps + warp; r < rows; r += (int64_t)gridDim.x * kAppWarps) {
-        const int64_t t = r / A.Hkv;
-        const int h = (int)(r - t * A.Hkv);
-        const int64_t slot = A.slots[t];
-        if (slot < 0) continue;
-        const int64_t page = slot >> A.page_shift;
-        if (page >= A.n_pages) {
-            if (lane == 0) report_timeout(status, kAppStatusRange);
-            continue;
-        }
-        const float n = warp_encode_indices<D, T>(src + t * stride + (int64_t)h * D, lane, sg, P.two_sided ? sg2 : nullptr,
-                                                  P, (1 << bits) - 1, ib);
-        const int64_t drow = ((page * A.Hkv + h) << A.page_shift) + (slot & ((int64_t(1) << A.page_shift) - 1));
-        warp_pack_row<D>(ib, lane, bits, pk + drow * rb);
-        if (lane == 0) nrm[drow] = n;
-        __syncwarp();
-    }
-}
-
 // ------------------------------------------------------------------ decode
 
 template <int D, int BITS, typename TO>
@@ -1766,24 +1720,6 @@ cudaError_t launch_append_paged_d(int k_bits, int v_bits, tq_dtype dt, const voi
     }
 }
 
-template <int D>
-cudaError_t launch_append_slots_d(int k_bits, int v_bits, tq_dtype dt, const SlotRows& r, const tq_cache_view& pages,
-                                  const RowParams& PK, const RowParams& PV, cudaStream_t s) {
-    if constexpr (D >= 32) {
-        auto launch = [&](auto tag) {
-            auto fn = dev::k_append_slots<D, decltype(tag)>;
-            int64_t g = (r.n_tokens * r.Hkv + dev::kAppWarps - 1) / dev::kAppWarps;
-            const int64_t cap = (int64_t)num_sms() * blocks_per_sm((const void*)fn, 32 * dev::kAppWarps, 0);
-            if (g > cap) g = cap;
-            return dev::launch_pdl(fn, dim3((unsigned)g, 2), dim3(32 * dev::kAppWarps), 0, s, r, pages, k_bits, v_bits,
-                                   PK, PV, status_word());
-        };
-        return dt == TQ_BF16 ? launch(__nv_bfloat16{}) : launch(float{});
-    } else {
-        return cudaErrorInvalidValue;
-    }
-}
-
 #ifndef TQ_UNIT_D
 #error "compile once per head dimension with -DTQ_UNIT_D=<d>"
 #endif
@@ -1793,8 +1729,6 @@ template cudaError_t launch_decode_d<TQ_UNIT_D>(int, tq_dtype, const uint8_t*, c
                                                 void*, const RowParams&, cudaStream_t);
 template cudaError_t launch_append_paged_d<TQ_UNIT_D>(int, int, tq_dtype, const void*, const void*, int, int,
                                                       const tq_cache_view&, const PagedArgs&,
-                                                      const RowParams&, const RowParams&, cudaStream_t);
-template cudaError_t launch_append_slots_d<TQ_UNIT_D>(int, int, tq_dtype, const SlotRows&, const tq_cache_view&,
                                                       const RowParams&, const RowParams&, cudaStream_t);
 template cudaError_t launch_append_d<TQ_UNIT_D>(int, int, tq_dtype, const void*, const void*, int, int,
                                                 int64_t, const tq_cache_view&, int64_t,

@@ -380,11 +380,16 @@ struct PagedPrefillCall {
     // the levels as fp16 bytes: high bytes of eight levels in words 0 and 1,
     // their low bytes in words 4 and 5 (4 bits: the eight positive ones)
     uint32_t k_levels[8], v_levels[8];
+    uint16_t k_cen[16], v_cen[16];  // the levels as fp16 (tq_attn_few.cu)
 };
 // What a query row attends to (tq_paged_parts.cuh).
 enum { kPpCausal = 0, kPpSinks = 1, kPpTree = 2 };
 template <int D, int MODE>
 cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s);
+// The same for few query rows per sequence and KV head (tq_attn_few.cu), not
+// causal.
+template <int D, int MODE>
+cudaError_t launch_attn_few(const PagedPrefillCall& c, cudaStream_t s);
 
 // Paged append of one token per sequence, d >= 32 (tq_codec.cu).
 template <int D>
@@ -412,7 +417,7 @@ struct PagesCall {
 size_t pages_workspace_bytes(int n_seqs, int64_t n_pages);
 cudaError_t launch_pages(int op, const PagesCall& c, cudaStream_t s);
 
-// Append of rows at given slots, d >= 32 (tq_codec.cu): token t's row of KV head
+// Append of rows at given slots, d >= 32 (tq_steps.cu): token t's row of KV head
 // h is at k_new + t * k_stride + h * d elements.
 struct SlotRows {
     const void* k_new;

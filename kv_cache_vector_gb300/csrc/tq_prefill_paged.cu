@@ -81,8 +81,6 @@
 #include <type_traits>
 
 #include "tq_paged_parts.cuh"
-#include "tq_tmem.cuh"
-#include "tq_umma.cuh"
 
 #if !defined(TQ_UNIT_D) || !defined(TQ_UNIT_MODE)
 #error "compile once per head dimension and mode with -DTQ_UNIT_D=<d> -DTQ_UNIT_MODE=<mode>"
@@ -137,130 +135,7 @@ __device__ __forceinline__ unsigned char* pp_place(unsigned char* tile, int r, i
     return tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ float pp_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
-__device__ __forceinline__ float pp_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t e;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(e));
-    return e;
-}
-
-// The value of lane 0: known to the compiler to be the same in the whole warp.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-    return ((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v);
-}
-
-// A try_wait that may suspend the warp for up to 100 us.
-__device__ __forceinline__ bool pp_try_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(100000u)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait; gives up at once when the CTA's abort flag is set.
-__device__ __forceinline__ bool pp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_f, int* status) {
-    if (pp_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!pp_try_wait(bar, parity)) {
-        if (*abort_f) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-            *abort_f = 1;
-            report_timeout(status, kPpStatusWait);
-            return false;
-        }
-    }
-    return true;
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// The largest of 32 columns as fp32, NaN left out: the load's own reduction.
-__device__ __forceinline__ float tmem_max32(uint32_t taddr) {
-    uint32_t r[32];
-    float m;
-    asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=f"(m)
-        : "r"(taddr));
-    // completes the load; naming its registers keeps them the load's until then
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+f"(m)::"memory");
-    return m;
-}
-
-// Shared-memory descriptor of the V tile as an N-major B operand (N = dims):
-// 128-byte swizzle, 64-dim columns `lbo` bytes apart (leading offset), groups
-// of 8 positions 1024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFF);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-constexpr uint32_t kIdescBTransposed = 1u << 16;
-
 // ------------------------------------------------------------------ expansion
-
-// Byte permute whose selector nibbles are below 8 already (__byte_perm masks
-// them first).
-__device__ __forceinline__ uint32_t pp_prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-    return d;
-}
-// Bits of b where m is set, of a elsewhere.
-__device__ __forceinline__ uint32_t pp_select(uint32_t a, uint32_t b, uint32_t m) { return (a & ~m) | (b & m); }
-
-// Four fp16 levels from four 4-bit selectors (nibbles of sel's low half) and
-// the level bytes: two byte permutes pick the high and the low bytes, two
-// interleave them.  4-bit indices: hi/lo hold the 8 positive levels; x has a 1
-// in the nibble of every positive index, and the sign byte is permuted from
-// it.  Narrower indices: hi/lo hold all levels with their signs.
-template <int BITS>
-__device__ __forceinline__ void pp_levels4(uint32_t sel, uint32_t x, const uint32_t* hi, const uint32_t* lo,
-                                           uint32_t& p01, uint32_t& p23) {
-    uint32_t h = pp_prmt(hi[0], hi[1], sel);
-    const uint32_t l = pp_prmt(lo[0], lo[1], sel);
-    if constexpr (BITS == 4) h ^= pp_prmt(0x00000080u, 0u, x);
-    p01 = pp_prmt(l, h, 0x5140);
-    p23 = pp_prmt(l, h, 0x7362);
-}
 
 // 8 indices (fp16 pairs of their levels times the row's norm) to 16 bytes at
 // dst.  The norm comes as fp16 high part r; with LOW also its rest rl, so that
@@ -296,23 +171,6 @@ __device__ __forceinline__ void pp_expand8(uint32_t f, __half2 r, __half2 rl, co
         v[k] = *reinterpret_cast<const uint32_t*>(&y);
     }
     *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// Which pair of 16-byte chunks a row's thread starts with (an xor on the pair
-// number): a permutation per row under which a warp's reads of the staged
-// words fall into different banks, and each eight lanes' writes to the
-// swizzled tile too.
-template <int BITS, int D>
-__device__ __forceinline__ int pp_turn(int r) {
-    if constexpr (BITS == 4)
-        return D == 128 ? ((r >> 2) & 3) | ((r & 2) << 1)
-                        : D == 256 ? ((r >> 2) & 3) | ((r & 3) << 2) : D == 64 ? (r >> 2) & 3 : (r >> 3) & 1;
-    else if constexpr (BITS == 3)
-        return D == 128 ? ((r >> 3) & 3) << 1
-                        : D == 256 ? (((r >> 3) & 3) << 1) | ((r & 4) << 1) : D == 64 ? (r >> 4) & 1 : 0;
-    else
-        return D == 128 ? (r >> 2) & 7
-                        : D == 256 ? ((r >> 2) & 7) | ((r & 2) << 2) : D == 64 ? (r >> 3) & 3 : (r >> 4) & 1;
 }
 
 // This thread's share of one staged row, 16 indices per turn of a rolled loop.
@@ -364,11 +222,6 @@ __device__ __forceinline__ void pp_expand(int bits, const unsigned char* rows, f
     else pp_expand_row<2, D, TPR, LOW>(rows, rf, hi, lo, tile, half_bytes, row, sub);
 }
 
-__device__ __forceinline__ float pp_max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 // The largest of 32 values, NaN left out, in four chains.
 __device__ __forceinline__ float pp_max32(const uint32_t (&s)[32]) {
     float m[4];
@@ -487,14 +340,6 @@ __device__ __noinline__ float2 pp_wide(uint32_t t_s, const unsigned char* cols, 
     tmem_wait_st();
     return make_float2(m, sum);
 }
-// Sums of 2^(s - m) of two sets of positions put together (m -inf: an empty set,
-// its sum 0 or NaN).
-__device__ __forceinline__ void pp_join_sums(float& l, float& m, float l1, float m1) {
-    const float mx = fmaxf(m, m1), mr = mx == -INFINITY ? 0.f : mx;
-    l = l * pp_exp2(m - mr) + l1 * pp_exp2(m1 - mr);
-    m = mx;
-}
-
 // The finite norms' bits, 0 for the others; the power of two that goes with them:
 // norms below 2^(e + 14), and a range that keeps every factor of the kernel a
 // normal fp32.
@@ -595,123 +440,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     // From here on: what earlier kernels wrote.  No read-only loads (__ldg): they
     // may be taken ahead of the wait, as these values change within the grid's life.
     griddep_wait();
-    // ---- this CTA's share: the sequences' weights, scanned over the block
-    {
-        const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
-        const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
-        PpSeq<Z, MODE> q;
-        long long mine = 0;
-        int items = 0;
-        float most = 0.f;  // the largest item's work
-        for (int b = b0; b < b1; ++b) {
-            q.load(A, b, blockIdx.x == 0 ? status : nullptr);
-            mine += (long long)A.Hkv * q.before(q.tiles);
-            if (q.tiles) most = fmaxf(most, fmaxf((float)q.work(q.tiles - 1), (float)q.work(max(0, q.tiles - 2))));
-            items += (int)min((int64_t)1 << 10, (int64_t)A.Hkv * q.tiles);  // exact where it counts: below the CTAs
-        }
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) red[warp] = incl;
-        uint32_t* red2 = reinterpret_cast<uint32_t*>(red + Z::kWarps);
-        const uint32_t wi = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)items);
-        const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-        if (lane == 0) red2[2 * warp] = wi, red2[2 * warp + 1] = wm;
-        __syncthreads();
-        long long total = 0, before = 0;
-        uint32_t all = 0, top = 0;
-#pragma unroll
-        for (int w = 0; w < Z::kWarps; ++w) {
-            if (w < warp) before += red[w];
-            total += red[w];
-            all += red2[2 * w];
-            top = max(top, red2[2 * w + 1]);
-        }
-        before += incl - mine;
-        const float sum = (float)total, grid = (float)gridDim.x;
-        // a little over total / grid: the last CTA's share may be smaller
-        const long long per = (long long)(sum * (1.000001f / grid)) + 1;
-        if (tid == 0) *share = per;
-        // Shares along the line of all items cross from one item into the next, and
-        // then pay for two items' rotations and outputs.  With few items a share is
-        // a part of one item instead: an item gets (work / cut) + 1 shares, no more
-        // than there are CTAs in all.  Taken where the largest of them is no more
-        // than a share of the line: the drafts of 4 sequences over 400-2000
-        // positions took 24.7 us along the line, 20.8 us so.
-        float cut = 0.f;
-        if (each == 1 && all > 0 && all < gridDim.x) {
-            const float over = (float)Z::kCostItem * Z::kN * (A.Hq / A.Hkv);
-            const float c = fmaxf(1.f, __fdividef((sum - (float)all * over) * 1.000002f, grid - (float)all));
-            if (fminf(c, __uint_as_float(top)) * grid <= sum) cut = c;
-        }
-        if (cut > 0.f) {
-            auto parts = [&](int i) { return (int)__fdividef((float)q.work(i), cut) + 1; };
-            int sums = 0;
-            for (int i = 0; i < q.tiles; ++i) sums += A.Hkv * parts(i);
-            int ins = sums;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xFFFFFFFFu, ins, o);
-                if (lane >= o) ins += u;
-            }
-            __syncthreads();  // red2 is free
-            if (lane == 31) red2[warp] = ins;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) ins += red2[w];
-            int v = (int)blockIdx.x - (ins - sums);
-            if (v >= 0 && v < sums) {  // this thread's sequence holds this CTA's share
-                int i = 0, n;
-                for (;; ++i) {
-                    n = parts(i);
-                    if (v < A.Hkv * n) break;
-                    v -= A.Hkv * n;
-                }
-                start->b = b0;
-                start->i = i;
-                start->h = v / n;
-                start->off = v % n;
-                start->parts = n;
-                start->n = q.n;
-                start->ctx = q.ctx;
-                start->q0 = q.q0;
-            }
-        } else {
-        const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-        if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
-            long long v = u0 - before;
-            int b = b0;
-            if (each > 1)
-                for (;; ++b) {
-                    q.load(A, b, nullptr);
-                    const long long w = (long long)A.Hkv * q.before(q.tiles);
-                    if (v < w) break;
-                    v -= w;
-                }
-            int lo = 0, hi = q.tiles - 1;  // the last tile whose units start at or before v
-            while (lo < hi) {
-                const int m = (lo + hi + 1) / 2;
-                if ((long long)A.Hkv * q.before(m) <= v) lo = m;
-                else hi = m - 1;
-            }
-            v -= (long long)A.Hkv * q.before(lo);
-            const long long w = q.weight(lo);
-            start->b = b;
-            start->i = lo;
-            int h = (int)((float)v / (float)w);  // v / w, to within one
-            h -= (long long)h * w > v;
-            h += (long long)(h + 1) * w <= v;
-            start->h = h;
-            start->off = v - (long long)h * w;
-            start->left = u1 - u0;
-            start->n = q.n;
-            start->ctx = q.ctx;
-            start->q0 = q.q0;
-        }
-        }
-    }
+    pp_start<Z, MODE>(A, red, start, share, status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -759,39 +488,12 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
         bool ok = true;
         for (; ok; ++job) {
             PpPart u;
-            bool more;
-            if (cur.parts > 0) {  // the one part of this share
-                u.b = cur.b, u.i = cur.i, u.h = cur.h;
-                pp_rows(A, seq, u);
-                const uint32_t nb = u.nblk, at = (uint32_t)cur.off, of = cur.parts;  // nb of < 2^32
-                u.blk0 = nb * at / of;
-                u.blk1 = nb * (at + 1) / of;
-                u.head = cur.off == 0;
-                u.whole = u.nblk == 0 ? u.head : (u.blk0 == 0 && u.blk1 == u.nblk);
-                more = job == 0 && (u.whole || u.blk1 > u.blk0);
-            } else {
-                more = pp_next(A, cur, seq, u);
-            }
+            const bool more = pp_next_part(A, cur, seq, u, job == 0);
             if (job >= 2) ok = pp_wait(&job_free[job & 1], ((job >> 1) - 1) & 1, abort_f, status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (lane == 0) {
-                volatile PpJob* m = reinterpret_cast<volatile PpJob*>(sm + Z::kJobs) + (job & 1);
-                m->nb = more ? u.blk1 - u.blk0 : -1;
-                if (more) {
-                    m->flags = (u.pair ? kJobPair : 0) | (u.whole ? kJobWhole : 0) | (u.head ? kJobHead : 0);
-                    m->q0 = seq.q0;
-                    m->h = u.h;
-                    m->row0 = u.row0;
-                    m->rows = u.rows;
-                    m->blk = u.lo_blk + u.blk0;
-                    m->kv_lo = u.kv_lo;
-                    m->kv_end = u.kv_end;
-                    m->pos0 = seq.ctx - seq.n;
-                    const int tok0 = u.row0 / seq.G;
-                    m->tok0 = tok0;
-                    m->rest = u.row0 - tok0 * seq.G;
-                }
+                pp_write_job(reinterpret_cast<volatile PpJob*>(sm + Z::kJobs) + (job & 1), more, u, seq);
                 mbar_arrive(&job_full[job & 1]);
             }
             __syncwarp();
@@ -834,33 +536,7 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                               &stage_full[st]);
             }
         }
-        // which parts this share left, and the item it owns: the one that starts
-        // in this share and ends in a later one
-        if (lane == 0) {
-            int last = blockIdx.x;
-            bool owner;
-            if (cur.parts > 0) {
-                // (an item of one block is some share's whole)
-                owner = ok && cur.off == 0 && cur.parts > 1 && pp_blocks(A, seq, cur.i) > 1;
-                last += cur.parts - 1;
-            } else {
-                owner = ok && cur.off > 0 &&
-                        !(start->off > 0 && start->b == cur.b && start->i == cur.i && start->h == cur.h);
-                if (owner) {
-                    const int64_t w = seq.weight(cur.i), per = *share;
-                    const int nblk = pp_blocks(A, seq, cur.i);
-                    // no join where one share has all of the item's blocks
-                    owner = nblk > 0 && pp_cut(nblk, cur.off, w, seq.over) < nblk;
-                    for (int64_t x = cur.off; x < w && pp_cut(nblk, x, w, seq.over) == 0; x += per)
-                        if (pp_cut(nblk, min(w, x + per), w, seq.over) == nblk) owner = false;
-                    last += (int)((w - cur.off + per - 1) / per);
-                }
-            }
-            const int row0 = cur.i * Z::kRows;
-            int4* m = reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta);
-            m[0] = make_int4(has, owner ? last : -1, owner ? seq.q0 : 0, cur.h);
-            m[1] = make_int4(row0, owner ? min(Z::kRows, seq.rows - row0) : 0, 0, 0);
-        }
+        if (lane == 0) pp_report<Z, MODE>(A, *start, *share, cur, seq, ok, has);
         // the copies issued have landed before the CTA leaves (bounded)
         if (lane == 0 && tc > 0)
             for (uint32_t t = tc > (uint32_t)NS ? tc - NS : 0; t < tc; ++t) mbar_wait(&stage_full[t % NS], (t / NS) & 1);
@@ -1463,122 +1139,6 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
     }
 }
 
-// Block (share, y): rows 32 y .. + 31 of the item that the share owns, its
-// parts summed in the order of the shares, AT parts' loads in flight, divided
-// and rotated back.
-template <int D, int AT>
-__global__ void __launch_bounds__(256, D < 256 && AT == 2 ? 3 : 2)
-k_prefill_paged_join(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefillConsts P) {
-    using Z = PpGeo<D>;
-    constexpr int C = D / 32;  // 16-byte columns per thread, and elements per lane of a row
-    __shared__ float tile[32][D + 1];
-    griddep_wait();
-    const int sh = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int4* meta = reinterpret_cast<const int4*>(A.meta);
-    const int4 m0 = __ldcg(meta + 2 * sh), m1 = __ldcg(meta + 2 * sh + 1);
-    int near = 0;  // what the shares up to 31 further on left, looked up together with the item
-    if (sh + lane < (int)gridDim.x) near = __ldcg(A.meta + (sh + lane) * kPpMeta + kMetaHas);
-    const int last = m0.y, rows = m1.y;
-    if (last < 0 || 32 * (int)blockIdx.y >= rows) return;
-    const int G = A.Hq / A.Hkv;
-    const int lrow = 32 * blockIdx.y + lane;  // every warp: the same 32 rows
-    constexpr int64_t PF = PagedPrefillGeo<D>::kPartFloats;
-    const bool in = lrow < rows;
-    float M = -INFINITY, l = 0.f, m = -INFINITY;
-    float4 o[C];
-#pragma unroll
-    for (int k = 0; k < C; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = sh; c0 <= last; c0 += 32) {
-        const int cl = c0 + lane;
-        if (c0 > sh && cl <= last) near = __ldcg(A.meta + cl * kPpMeta + kMetaHas);
-        unsigned has = __ballot_sync(0xFFFFFFFFu, cl <= last && (near & (cl == sh ? 2 : 1)));
-        if (__any_sync(0xFFFFFFFFu, cl <= last && (near & kShareFailed))) return;  // every warp sees the same
-        while (has && in) {
-            // a few parts' loads in flight at once
-            float4 v[AT][C];
-            float Mc[AT], lc[AT], mc[AT];
-            unsigned left = has;
-#pragma unroll
-            for (int t = 0; t < AT; ++t) {
-                Mc[t] = -INFINITY, lc[t] = 0.f, mc[t] = -INFINITY;
-                if (left) {
-                    const int c = c0 + __ffs(left) - 1;
-                    left &= left - 1;
-                    const float* pt = A.part + ((int64_t)c * 2 + (c == sh)) * PF;
-                    const float* x = pt + D * Z::kRows + lrow;
-                    Mc[t] = __ldcg(x), lc[t] = __ldcg(x + Z::kRows), mc[t] = __ldcg(x + 2 * Z::kRows);
-#pragma unroll
-                    for (int k = 0; k < C; ++k)
-                        v[t][k] = __ldcg(reinterpret_cast<const float4*>(pt) + lrow + (warp + 8 * k) * Z::kRows);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < AT; ++t) {
-                if (!has) break;
-                has &= has - 1;
-                // both sides to the larger maximum; a side that attended to nothing
-                // has -inf, no output and the sum 0 (or NaN)
-                const float Mx = fmaxf(M, Mc[t]);
-                const float a = M == -INFINITY ? 0.f : pp_exp2(M - Mx), a1 = Mc[t] == -INFINITY ? 0.f : pp_exp2(Mc[t] - Mx);
-                pp_join_sums(l, m, lc[t], mc[t]);
-                M = Mx;
-#pragma unroll
-                for (int k = 0; k < C; ++k) {
-                    o[k].x = o[k].x * a + v[t][k].x * a1;
-                    o[k].y = o[k].y * a + v[t][k].y * a1;
-                    o[k].z = o[k].z * a + v[t][k].z * a1;
-                    o[k].w = o[k].w * a + v[t][k].w * a1;
-                }
-            }
-        }
-    }
-    const float inv = l == 0.f ? 0.f : pp_exp2(M - m) * P.out_mul * P.inv_sqrt_d / l;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-        const float v[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int j = 4 * (warp + 8 * k) + u;
-            tile[lane][j] = __uint_as_float(__float_as_uint(v[u] * inv) ^ (P.two_sided ? sign_mask(P.sgn2b, j) : 0u));
-        }
-    }
-    __syncthreads();
-    // rows rotated back, one per warp at a time: elements lane + 32 k, the
-    // transform's low five bits across lanes, the rest in registers
-    for (int r = warp; r < 32; r += 8) {
-        const int lr = 32 * blockIdx.y + r;
-        if (lr >= rows) break;
-        float e[C];
-#pragma unroll
-        for (int k = 0; k < C; ++k) e[k] = tile[r][lane + 32 * k];
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2)
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-                const float u = __shfl_xor_sync(0xFFFFFFFFu, e[k], m);
-                e[k] = lane & m ? u - e[k] : e[k] + u;
-            }
-#pragma unroll
-        for (int len = 1; len < C; len *= 2)
-#pragma unroll
-            for (int k = 0; k < C; ++k)
-                if (!(k & len)) {
-                    const float u = e[k], v = e[k + len];
-                    e[k] = u + v;
-                    e[k + len] = u - v;
-                }
-        const int grow = m1.x + lr, tok = grow / G, hd = grow - tok * G;
-        const int64_t at = (((int64_t)m0.z + tok) * A.Hq + (int64_t)m0.w * G + hd) * D;
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const int j = lane + 32 * k;
-            const float v = __uint_as_float(__float_as_uint(e[k]) ^ sign_mask(P.sgnb, j));
-            if (A.out_bf16) static_cast<__nv_bfloat16*>(A.out)[at + j] = __float2bfloat16_rn(v);
-            else static_cast<float*>(A.out)[at + j] = v;
-        }
-    }
-}
-
 }  // namespace dev
 
 template <int D, int MODE>
@@ -1587,35 +1147,8 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     using namespace dev;
     using Z = PpGeo<D>;
     static_assert(Z::kSmem <= 232448, "shared memory per CTA");
-    PpArgs A = {};
-    A.q = static_cast<const __nv_bfloat16*>(c.q);
-    A.out = c.out;
-    A.cu = c.cu_q;
-    A.ctx = c.ctx_lens;
-    A.bt = c.block_table;
-    A.c = c.cache;
-    A.n_q = c.n_q;
-    A.B = c.B;
-    A.Hq = c.Hq;
-    A.Hkv = c.Hkv;
-    A.max_pages = c.max_pages;
-    A.shift = c.page_shift;
-    A.window = c.window;
-    A.k_bits = c.k_bits;
-    A.v_bits = c.v_bits;
-    A.out_bf16 = c.out_bf16;
-    A.sinks = c.sinks;
-    A.mask = c.mask;
-    A.words = c.mask_words;
-    for (int i = 0; i < 4; ++i) {
-        A.khi[i] = c.k_levels[i];
-        A.klo[i] = c.k_levels[4 + i];
-        A.vhi[i] = c.v_levels[i];
-        A.vlo[i] = c.v_levels[4 + i];
-    }
     const int shares = num_sms();
-    A.part = static_cast<float*>(c.workspace);
-    A.meta = reinterpret_cast<int32_t*>(A.part + (size_t)shares * 2 * PagedPrefillGeo<D>::kPartFloats);
+    const PpArgs A = pp_args(c, shares, PagedPrefillGeo<D>::kPartFloats);
     static int attr_done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1635,8 +1168,8 @@ cudaError_t launch_prefill_paged(const PagedPrefillCall& c, cudaStream_t s) {
     // 21.1 -> 21.5 us, but 32 mixed sequences 222 -> 220, 2048 tokens after 4000 238
     // -> 235).
     if (D < 256 && rows < Z::kRows)
-        return launch_pdl(k_prefill_paged_join<D, D < 256 ? 4 : 2>, dim3(shares, groups), dim3(256), 0, s, A, P);
-    return launch_pdl(k_prefill_paged_join<D, 2>, dim3(shares, groups), dim3(256), 0, s, A, P);
+        return launch_pdl(k_prefill_paged_join<D, D < 256 ? 4 : 2, Z::kRows>, dim3(shares, groups), dim3(256), 0, s, A, P);
+    return launch_pdl(k_prefill_paged_join<D, 2, Z::kRows>, dim3(shares, groups), dim3(256), 0, s, A, P);
 }
 
 template cudaError_t launch_prefill_paged<TQ_UNIT_D, TQ_UNIT_MODE>(const PagedPrefillCall&, cudaStream_t);

@@ -1,8 +1,10 @@
-// tq_steps.cu -- a serving step's books beside the pages: where its new tokens
-// go (tq_pages_slots), and the drafted rows that are kept (tq_pages_keep).
+// tq_steps.cu -- a serving step's tokens: where the new ones go (tq_pages_slots),
+// their append (tq_append_slots), and the drafted ones that are kept
+// (tq_pages_keep).
 #include <climits>
 
 #include "tq_async.cuh"
+#include "tq_device.cuh"
 #include "tq_internal.h"
 
 namespace tq {
@@ -141,6 +143,58 @@ __global__ void __launch_bounds__(kSlThreads) k_pages_slots(const SlotsArgs A, i
     }
 }
 
+// -------------------------------------------------------------------- append
+//
+// A step's tokens at the slots that tq_pages_slots gives them: row
+// (t, h) goes to offset slots[t] % page_size of page slots[t] / page_size; a
+// negative slot has no token.  One warp per row, as the append of one token per
+// sequence.
+constexpr int kAsWarps = 4;
+constexpr int kAsStatusRange = 42;  // a slot past the pool's end (as the other appends)
+
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kAsWarps) k_append_slots(const SlotRows A, tq_cache_view cache, int k_bits,
+                                                                 int v_bits, const __grid_constant__ RowParams PK,
+                                                                 const __grid_constant__ RowParams PV, int* status) {
+    __shared__ uint32_t sg[D], sg2[D];
+    __shared__ uint8_t idxbuf[kAsWarps][D];
+    const bool is_v = blockIdx.y == 1;
+    const RowParams& P = is_v ? PV : PK;
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
+        sg[i] = sign_mask(P.sgnb, i);
+        sg2[i] = sign_mask(P.sgn2b, i);
+    }
+    __syncthreads();
+    griddep_wait();    // the new rows and slots, and readers of the cache, of the previous kernel
+    griddep_launch();  // the next kernel may set itself up; it waits for this grid
+    const int bits = is_v ? v_bits : k_bits;
+    const T* src = static_cast<const T*>(is_v ? A.v_new : A.k_new);
+    const int64_t stride = is_v ? A.v_stride : A.k_stride;
+    uint8_t* pk = is_v ? cache.v_packed : cache.k_packed;
+    float* nrm = is_v ? cache.v_norm : cache.k_norm;
+    const int rb = D * bits / 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ib = idxbuf[warp];
+    const int64_t rows = A.n_tokens * A.Hkv;
+    for (int64_t r = (int64_t)blockIdx.x * kAsWarps + warp; r < rows; r += (int64_t)gridDim.x * kAsWarps) {
+        const int64_t t = r / A.Hkv;
+        const int h = (int)(r - t * A.Hkv);
+        const int64_t slot = A.slots[t];
+        if (slot < 0) continue;
+        const int64_t page = slot >> A.page_shift;
+        if (page >= A.n_pages) {
+            if (lane == 0) report_timeout(status, kAsStatusRange);
+            continue;
+        }
+        const float n = warp_encode_indices<D, T>(src + t * stride + (int64_t)h * D, lane, sg, P.two_sided ? sg2 : nullptr,
+                                                  P, (1 << bits) - 1, ib);
+        const int64_t drow = ((page * A.Hkv + h) << A.page_shift) + (slot & ((int64_t(1) << A.page_shift) - 1));
+        warp_pack_row<D>(ib, lane, bits, pk + drow * rb);
+        if (lane == 0) nrm[drow] = n;
+        __syncwarp();
+    }
+}
+
 // ---------------------------------------------------------------- kept tokens
 //
 // Of row b's counts[b] last tokens those in keep[b] stay: token keep[b][i] moves
@@ -274,6 +328,28 @@ static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, const KeepA
 }
 
 }  // namespace dev
+
+template <int D>
+cudaError_t launch_append_slots_d(int k_bits, int v_bits, tq_dtype dt, const SlotRows& r, const tq_cache_view& pages,
+                                  const RowParams& PK, const RowParams& PV, cudaStream_t s) {
+    auto launch = [&](auto tag) {
+        auto fn = dev::k_append_slots<D, decltype(tag)>;
+        int64_t g = (r.n_tokens * r.Hkv + dev::kAsWarps - 1) / dev::kAsWarps;
+        const int64_t cap = (int64_t)num_sms() * blocks_per_sm((const void*)fn, 32 * dev::kAsWarps, 0);
+        if (g > cap) g = cap;
+        return dev::launch_pdl(fn, dim3((unsigned)g, 2), dim3(32 * dev::kAsWarps), 0, s, r, pages, k_bits, v_bits,
+                               PK, PV, status_word());
+    };
+    return dt == TQ_BF16 ? launch(__nv_bfloat16{}) : launch(float{});
+}
+template cudaError_t launch_append_slots_d<32>(int, int, tq_dtype, const SlotRows&, const tq_cache_view&, const RowParams&,
+                                               const RowParams&, cudaStream_t);
+template cudaError_t launch_append_slots_d<64>(int, int, tq_dtype, const SlotRows&, const tq_cache_view&, const RowParams&,
+                                               const RowParams&, cudaStream_t);
+template cudaError_t launch_append_slots_d<128>(int, int, tq_dtype, const SlotRows&, const tq_cache_view&,
+                                                const RowParams&, const RowParams&, cudaStream_t);
+template cudaError_t launch_append_slots_d<256>(int, int, tq_dtype, const SlotRows&, const tq_cache_view&,
+                                                const RowParams&, const RowParams&, cudaStream_t);
 
 cudaError_t launch_slots(const StepSlotsCall& c, cudaStream_t s) {
     using namespace dev;
