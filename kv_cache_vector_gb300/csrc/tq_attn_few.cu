@@ -13,9 +13,10 @@
 //   S^T[position, row] = K[position, :] . Q[row, :]
 //   O^T[dim, row]     += V[:, dim]^T . P^T[position, row]
 //
-// Every warp by itself takes chunks of 32 positions of the CTA's part (copied
-// to its own ring by bulk copies) and keeps a running maximum and output; the
-// warps are merged at the part's end.  Work is cut into shares, parts of items
+// Four warps at a time take a block of 128 positions of the CTA's part, 32 each,
+// from a ring of two blocks of their own (one bulk copy per array and page:
+// issuing one costs a warp some 100 cycles).  Every warp keeps a running maximum
+// and output; the warps are merged at the part's end.  Work is cut into shares, parts of items
 // are joined and lengths are read as in tq_prefill_paged.cu (tq_paged_parts.cuh).
 //
 // Numbers.  s = log2 score, in fp32 from the fp16 products.  Per row a running
@@ -44,9 +45,9 @@ constexpr int kFwStatusLayout = 76;  // dynamic shared memory starts above kFwLo
 // Shared memory by absolute shared-window address (the dynamic block starts at
 // or below kFwLow): the pair table 64 KiB aligned, so that a lookup's address is
 // one byte permute: row e (256 bytes) holds pair e, keys in bytes 0..127 and
-// values in 128..255, 4 bytes a lane.  The warps' rings lie below it and, where
+// values in 128..255, 4 bytes a lane.  The rings' blocks lie below it and, where
 // they do not all fit, above.
-constexpr uint32_t kFwLow = 2048, kFwTable = 65536, kFwHigh = 131072, kFwTop = 232448;
+constexpr uint32_t kFwLow = 2048, kFwTop = 232448;
 
 struct FwJob {
     int b, h, nb, flags, q0, row0, rows, blk, kv_lo, kv_end, pos0, tok0, rest;
@@ -59,36 +60,40 @@ struct FwGeo {
     static constexpr int kRows = 8 * NT;  // query rows of an item
     static constexpr int kStreams = 1;
     static constexpr int kCostPair = 1, kCostSplit = 1, kCostItem = 4;  // of a block and an item (pp_start)
-    // registers: the output takes D / 4 NT, the queries D / 8 NT (kept in
-    // registers up to two tiles of rows)
+    // registers: the output takes D / 4 NT, the queries D / 8 NT
     static constexpr int kWarps = D * NT >= 256 ? 8 : 12;
     static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kQuads = kWarps / 4;
     static constexpr int kStages = 2;
-    static constexpr uint32_t kStage = 32 * D + 256;  // 4-bit K and V rows, K and V norms
-    static constexpr uint32_t kWarpRing = kStages * kStage;
-    static constexpr int kLowWarps = (int)((kFwTable - kFwLow) / kWarpRing) < kWarps ? (int)((kFwTable - kFwLow) / kWarpRing) : kWarps;
-    static constexpr uint32_t kLowEnd = kFwLow + kLowWarps * kWarpRing;
-    static constexpr uint32_t kHighEnd = kFwHigh + (kWarps - kLowWarps) * kWarpRing;
-    // queries in the order of the B fragments, row factors, jobs, barriers, ...
+    static constexpr uint32_t kStage = kN * (D + 8);  // 4-bit K and V rows, K and V norms
+    static constexpr uint32_t kTable = D == 256 ? 131072 : 65536, kHigh = kTable + 65536;
+    static constexpr int kAll = kQuads * kStages, kFitLow = (int)((kTable - kFwLow) / kStage);
+    static constexpr int kLow = kFitLow < kAll ? kFitLow : kAll;  // blocks below the table
+    static constexpr uint32_t kLowEnd = kFwLow + kLow * kStage;
+    static constexpr uint32_t kHighEnd = kHigh + (kAll - kLow) * kStage;
+    // queries in the order of the B fragments, row factors, parts, barriers, ...
     static constexpr uint32_t kQBytes = kRows * D * 2;
-    static constexpr uint32_t kMiscBytes = kQBytes + 4 * kRows + kFwJobs * sizeof(FwJob) + 16 + 8 * kWarps * kStages + 16 * kWarps +
-                                           16 + 96 + 16;
-    static constexpr bool kMiscLow = kLowEnd + kMiscBytes <= kFwTable;
+    static constexpr uint32_t kMiscBytes =
+        kQBytes + 4 * kRows + kFwJobs * sizeof(FwJob) + 16 + (16 + 16) * kQuads * kStages + 16 * kWarps + 16 + 96 + 16;
+    static constexpr bool kMiscLow = kLowEnd + kMiscBytes <= kTable;
     static constexpr uint32_t kQ = kMiscLow ? kLowEnd : kHighEnd;
     static constexpr uint32_t kFac = kQ + kQBytes;
     static constexpr uint32_t kJobs = kFac + 4 * kRows;
     static constexpr uint32_t kBar = (kJobs + kFwJobs * sizeof(FwJob) + 15) / 16 * 16;
-    static constexpr uint32_t kRed = kBar + 8 * kWarps * kStages;
+    static constexpr uint32_t kRec = kBar + 16 * kQuads * kStages;  // [quads][stages] int4: position, part, segments
+    static constexpr uint32_t kRed = kRec + 16 * kQuads * kStages;
     static constexpr uint32_t kCur = (kRed + 16 * kWarps + 15) / 16 * 16;
-    static constexpr uint32_t kMisc = kCur + 96;  // jobs at hand, abort flag
+    static constexpr uint32_t kMisc = kCur + 96;  // parts at hand, abort flag
     static constexpr uint32_t kMiscEnd = kMisc + 16;
-    static constexpr uint32_t kMerge = kMiscLow ? kHighEnd : kMiscEnd;
-    // merge buffer: [warps][rows at a time] of D floats and m, M, l
+    // merge buffer, where more is left: [warps][rows at a time] of D floats and m, M, l
+    static constexpr bool kMergeLow = kMiscLow && kTable - kMiscEnd > kFwTop - kHighEnd;
+    static constexpr uint32_t kMerge = kMiscLow && !kMergeLow ? kHighEnd : kMiscEnd, kMergeTop = kMergeLow ? kTable : kFwTop;
     static constexpr uint32_t kMergeRow = 4 * (D + 4);
-    static constexpr int kFit = (int)((kFwTop - kMerge) / (kWarps * kMergeRow));
+    static constexpr int kFit = (int)((kMergeTop - kMerge) / (kWarps * kMergeRow));
     static constexpr int kMergeRows = kFit < kRows ? kFit : kRows;
-    static constexpr uint32_t kEnd = kMerge + kWarps * kMergeRows * kMergeRow;
-    static_assert(kMergeRows >= 1 && kEnd <= kFwTop && (!kMiscLow || kMiscEnd <= kFwTable) && kMerge % 16 == 0 && kQ % 16 == 0 &&
+    static constexpr uint32_t kMergeEnd = kMerge + kWarps * kMergeRows * kMergeRow;
+    static constexpr uint32_t kEnd = kMergeEnd > kHighEnd ? kMergeEnd : kHighEnd;
+    static_assert(kMergeRows >= 1 && kMergeEnd <= kMergeTop && kEnd <= kFwTop && kHighEnd <= kFwTop && (!kMiscLow || kMiscEnd <= kTable) && kMerge % 16 == 0 && kQ % 16 == 0 &&
                       kStage % 16 == 0,
                   "shared-memory plan");
 };
@@ -262,7 +267,10 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
     volatile int* abort_f = n_jobs + 1;
     FwJob* jobs = reinterpret_cast<FwJob*>(at(Z::kJobs));
     float* fac = reinterpret_cast<float*>(at(Z::kFac));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(at(Z::kBar)) + warp * S;
+    const int quad = warp >> 2, sub = warp & 3;
+    uint64_t* full = reinterpret_cast<uint64_t*>(at(Z::kBar)) + quad * S;  // [S] a block has landed
+    uint64_t* free_ = full + Z::kQuads * S;                                // [S] its four warps have read it
+    volatile int4* recs = reinterpret_cast<volatile int4*>(at(Z::kRec)) + quad * S;
 
     // ---- pair tables: row e holds the pair e mod 2^(2 bits)
     {
@@ -270,15 +278,13 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
         for (int e = warp; e < 256; e += W) {
             const uint32_t k = L.k[e & mk] | (uint32_t)L.k[(e >> A.k_bits) & mk] << 16;
             const uint32_t v = L.v[e & mv] | (uint32_t)L.v[(e >> A.v_bits) & mv] << 16;
-            *reinterpret_cast<uint32_t*>(at(kFwTable + 256u * e + 4u * lane)) = k;
-            *reinterpret_cast<uint32_t*>(at(kFwTable + 256u * e + 128u + 4u * lane)) = v;
+            *reinterpret_cast<uint32_t*>(at(Z::kTable + 256u * e + 4u * lane)) = k;
+            *reinterpret_cast<uint32_t*>(at(Z::kTable + 256u * e + 128u + 4u * lane)) = v;
         }
     }
-    if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(bars + s, 1);
-        mbar_fence_init();
-    }
     if (tid == 0) {
+        for (int i = 0; i < Z::kQuads * S; ++i) mbar_init(full + i, 1), mbar_init(free_ + i, 4);
+        mbar_fence_init();
         start->left = 0;
         start->parts = 0;
         *abort_f = 0;
@@ -290,22 +296,23 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
 
     const int g = lane >> 2, t = lane & 3;
     const int G = A.Hq / A.Hkv;
-    const uint32_t kslot = kFwTable + 4u * lane, vslot = kslot + 128u;
-    const uint32_t ring = warp < Z::kLowWarps ? kFwLow + warp * Z::kWarpRing : kFwHigh + (warp - Z::kLowWarps) * Z::kWarpRing;
-    // lanes 0 to 3 each copy one of a chunk's four arrays
+    const uint32_t kslot = Z::kTable + 4u * lane, vslot = kslot + 128u;
+    auto stage_at = [&](uint32_t st) {
+        const int i = quad * S + (int)st;
+        return i < Z::kLow ? kFwLow + i * Z::kStage : Z::kHigh + (i - Z::kLow) * Z::kStage;
+    };
     const uint32_t k_row = D * A.k_bits / 8, v_row = D * A.v_bits / 8;
+    // lane 4 s + a copies array a of segment s (min(page, 128) positions) of a block
+    const int seg = min(1 << A.shift, Z::kN), seg_at = (lane >> 2) * seg;
     const unsigned char* my_src = reinterpret_cast<const unsigned char*>(
-        lane == 0 ? (const void*)A.c.k_packed : lane == 1 ? (const void*)A.c.v_packed
-                                            : lane == 2 ? (const void*)A.c.k_norm : (const void*)A.c.v_norm);
-    const uint32_t my_row = lane == 0 ? k_row : lane == 1 ? v_row : 4u;
-    const uint32_t my_dst = ring + (lane == 0 ? 0 : lane == 1 ? 16 * D : lane == 2 ? 32 * D : 32 * D + 128);
+        (lane & 3) == 0 ? (const void*)A.c.k_packed : (lane & 3) == 1 ? (const void*)A.c.v_packed
+                                                  : (lane & 3) == 2 ? (const void*)A.c.k_norm : (const void*)A.c.v_norm);
+    const uint32_t my_row = (lane & 3) == 0 ? k_row : (lane & 3) == 1 ? v_row : 4u;
+    const uint32_t my_dst = ((lane & 3) == 0 ? 0 : (lane & 3) == 1 ? 64 * D : (lane & 3) == 2 ? 128 * D : 128 * D + 512) + seg_at * my_row;  // in the block
     const float q_sign = P.q_mul > 0.f ? 1.f : (P.q_mul < 0.f ? -1.f : 0.f);
     const float q_abs = P.q_mul == 0.f ? 1.f : fabsf(P.q_mul);
-    bool bad = false;   // a wait gave up: nothing is computed from then on
-    uint32_t issued = 0, taken = 0;  // stages of this warp's ring so far
-    // of the stages: the position of the chunk, or'd with 1 if it holds no rows (a
-    // page out of range), and its part
-    int st_pos[S], st_job[S];
+    bool bad = false;              // a wait gave up: nothing is computed from then on
+    uint32_t put = 0, taken = 0;   // blocks of the ring so far: copied (or on their way), and read by this warp
 
     PpCursor cur;  // of thread 0
     PpSeq<Z, MODE> seq;
@@ -338,53 +345,45 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
         const int nj = *n_jobs;
         if (nj == 0) break;
 
-        // The warp's chunks: numbers warp, warp + W, ... of a part's 4 nb, those
-        // left out that no row attends to.
-        int pj = -1, pc = 0, pn = 0;  // the next chunk to copy: its part, number, and the part's chunks
-        int p_b = 0, p_h = 0, p_blk = 0, p_lo = 0, p_end = 0, p_page = 0, p_pos = -1;
-        auto seek = [&]() {
-            p_pos = -1;
-            if (bad) return;
-            for (;;) {
-                for (; pc < pn; pc += W) {
-                    const int pos = pp_block_at<Z, MODE>(A, p_lo, p_end, p_blk + (pc >> 2)) * Z::kN + 32 * (pc & 3);
-                    if (pos < p_end && (pos + 32 > p_lo || (MODE == kPpSinks && pos < A.sinks))) {
-                        p_pos = pos;
-                        p_page = A.bt[(int64_t)p_b * A.max_pages + (pos >> A.shift)];
-                        pc += W;
-                        return;
-                    }
-                }
-                if (++pj >= nj) return;
-                const FwJob& x = jobs[pj];
-                pc = warp, pn = 4 * x.nb;
-                p_b = x.b, p_h = x.h, p_blk = x.blk, p_lo = x.kv_lo, p_end = x.kv_end;
+        // The quad's blocks: numbers quad, quad + kQuads, ... of every part's, and then
+        // a record without one.  Its warps bring them in turn, S ahead.
+        int pj = -1, pc = 0, pn = 0;  // of the next block: its part, number, and the part's blocks
+        auto bring = [&]() {
+            if (pj >= nj || bad) return;
+            while (pc >= pn) {
+                if (++pj >= nj) break;
+                pc = quad, pn = jobs[pj].nb;
             }
-        };
-        auto issue = [&]() {
-            if (p_pos < 0) return;
-            const int st = issued % S;
-            const bool ok = p_page >= 0 && p_page < A.c.n_pages;
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                if (st == i) st_pos[i] = p_pos | (ok ? 0 : 1), st_job[i] = pj;
-            if (ok) {
-                if (lane == 0) mbar_arrive_expect_tx(bars + st, 32 * (k_row + v_row) + 256);
-                if (lane < 4) {
-                    const int64_t row = (((int64_t)p_page * A.Hkv + p_h) << A.shift) + (p_pos & ((1 << A.shift) - 1));
+            const uint32_t st = put % S;
+            if ((put & 3) == (uint32_t)sub) {
+                const FwJob& x = jobs[min(pj, nj - 1)];
+                const int t0 = pp_block_at<Z, MODE>(A, x.kv_lo, x.kv_end, x.blk + pc) * Z::kN, pos = t0 + seg_at;
+                int page = INT_MIN;
+                if (pj < nj && seg_at < Z::kN && pos < x.kv_end && (pos + seg > x.kv_lo || (MODE == kPpSinks && pos < A.sinks)))
+                    page = A.bt[(int64_t)x.b * A.max_pages + (pos >> A.shift)];
+                const bool have = page >= 0 && page < A.c.n_pages;
+                if (page != INT_MIN && !have) report_timeout(status, kPpStatusPage);
+                const uint32_t mask = __ballot_sync(kAll, have && (lane & 3) == 0);
+                // (a wait that gives up is noticed at the block's own)
+                if (put >= (uint32_t)S) pp_wait(free_ + st, (put / S - 1) & 1, abort_f, status);
+                __syncwarp();
+                if (lane == 0) {
+                    recs[st].x = t0;
+                    recs[st].y = pj;
+                    recs[st].z = (int)mask;
+                    mbar_arrive_expect_tx(full + st, __popc(mask) * seg * (k_row + v_row + 8));
+                }
+                __syncwarp();
+                if (have && *abort_f == 0) {
+                    const int64_t row = (((int64_t)page * A.Hkv + x.h) << A.shift) + (pos & ((1 << A.shift) - 1));
                     fence_async_smem();  // earlier reads of this stage come first
-                    bulk_load(my_dst + st * Z::kStage, my_src + row * my_row, 32 * my_row, bars + st);
+                    bulk_load(stage_at(st) + my_dst, my_src + row * my_row, seg * my_row, full + st);
                 }
-            } else if (lane == 0) {
-                report_timeout(status, kPpStatusPage);
-                mbar_arrive(bars + st);
             }
-            ++issued;
+            ++put;
+            pc += Z::kQuads;
         };
-        for (int i = 0; i < S; ++i) {
-            seek();
-            issue();
-        }
+        for (int i = 0; i < S; ++i) bring();
 
         for (int j = 0; j < nj; ++j) {
             const FwJob x = jobs[j];
@@ -480,49 +479,35 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 }
             }
 
+            bool zero = false;  // a row of the lane's has attended to V norms of 0 alone: its factor is 0
             const int first_p = x.pos0 + x.tok0, last_p = x.pos0 + (x.row0 + x.rows - 1) / G;  // the rows' positions
             for (;;) {
-                const int st = taken % S;
-                int pos = 0, of = -1;
-#pragma unroll
-                for (int i = 0; i < S; ++i)
-                    if (st == i) pos = st_pos[i], of = st_job[i];
-                if (bad || taken == issued || of != j) break;
-                seek();  // the next chunk's page id loads while this one is worked on
-                if (!__all_sync(kAll, mbar_wait(bars + st, (taken / S) & 1))) {
-                    if (lane == 0) {
-                        report_timeout(status, kPpStatusWait);
-                        *abort_f = 1;
-                    }
-                    bad = true;  // taken stays at the stage that gave up
+                const uint32_t st = taken % S;
+                if (bad) break;
+                if (!__all_sync(kAll, pp_wait(full + st, (taken / S) & 1, abort_f, status))) {
+                    bad = true;
                     break;
                 }
-                const uint32_t sb = ring + st * Z::kStage;
+                const int pos = recs[st].x + 32 * sub;
+                if (recs[st].y != j) break;  // of a later part, or the end: it stays
+                const uint32_t segs = (uint32_t)recs[st].z;
+                const uint32_t sb = stage_at(st), s_k = sb + sub * 32 * k_row, s_v = sb + 64 * D + sub * 32 * v_row,
+                               s_n = sb + 128 * D + sub * 128;
+                if (pos < x.kv_end && (pos + 32 > x.kv_lo || (MODE == kPpSinks && pos < A.sinks))) {
                 float acc[2][NT][4];
-                if (A.k_bits == 4) fw_scores<D, NT, 4, QREG>(sb, kslot, qf, qs, g, t, acc);
-                else if (A.k_bits == 3) fw_scores<D, NT, 3, QREG>(sb, kslot, qf, qs, g, t, acc);
-                else fw_scores<D, NT, 2, QREG>(sb, kslot, qf, qs, g, t, acc);
+                if (A.k_bits == 4) fw_scores<D, NT, 4, QREG>(s_k, kslot, qf, qs, g, t, acc);
+                else if (A.k_bits == 3) fw_scores<D, NT, 3, QREG>(s_k, kslot, qf, qs, g, t, acc);
+                else fw_scores<D, NT, 2, QREG>(s_k, kslot, qf, qs, g, t, acc);
                 // this lane's positions: 16 u + 8 h + fw_at(g)
-                float kn[2][2], vn[2][2], odd = 0.f;
-                const uint32_t sn = sb + 32 * D + 4 * fw_at(g);
+                float kn[2][2], vn[2][2];
+                {
+                    const uint32_t sn = s_n + 4 * fw_at(g);
+                    const bool none = !((segs >> (4 * (32 * sub / seg))) & 1u);  // the page is out of range: rows of norm 0
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        kn[u][h] = __uint_as_float(fw_word(sn + 64 * u + 32 * h));
-                        vn[u][h] = __uint_as_float(fw_word(sn + 128 + 64 * u + 32 * h));
-                        odd = fmaf(kn[u][h], 0.f, fmaf(vn[u][h], 0.f, odd));
+                    for (int i = 0; i < 4; ++i) {
+                        kn[i >> 1][i & 1] = none ? 0.f : __uint_as_float(fw_word(sn + 32 * i));
+                        vn[i >> 1][i & 1] = none ? 0.f : __uint_as_float(fw_word(sn + 512 + 32 * i));
                     }
-                if (__any_sync(kAll, odd != 0.f || (pos & 1))) {  // norms that are not finite, or none at all
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (pos & 1) kn[u][h] = vn[u][h] = 0.f;
-                            if (!(fabsf(kn[u][h]) <= FLT_MAX && fabsf(vn[u][h]) <= FLT_MAX))
-                                kn[u][h] = __uint_as_float(0x7FFFFFFFu), vn[u][h] = 0.f;
-                        }
-                    pos &= ~1;
                 }
                 bool all;  // every row attends to every position
                 if (MODE == kPpTree) all = pos + 32 <= x.pos0;
@@ -557,103 +542,88 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                             if (i == k) on[k >> 1][k & 1] = w;
                     }
                 }
-                // log2 scores less the running maximum; -inf where not attended
-                float xs[2][NT][4], top;
-                auto scores = [&]() {
-                    top = -INFINITY;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    xs[u][nt][2 * h + k] = fmaf(acc[u][nt][2 * h + k] * kn[u][h], cq[nt][k], nm[nt][k]);
-                                    if (!all) xs[u][nt][2 * h + k] = (on[u][h] >> (2 * nt + k)) & 1u ? xs[u][nt][2 * h + k] : -INFINITY;
-                                }
-                                top = pp_max3(top, xs[u][nt][2 * h], xs[u][nt][2 * h + 1]);
-                            }
-                };
-                float lv[2][2];
+                // ---- probabilities, as B fragments.  Turn 0 takes the maxima as they are; if a
+                // score is 8 above m, a P above 2^15, or a norm not finite, they move and
+                // turn 1 follows, and where the factor of P leaves fp32 turn 2, by exponents
+                float p[2][NT][4], lv[2][2];
                 uint32_t pb[2][NT][2];
-                scores();
-                bool move = __any_sync(kAll, top > 8.f);
-                // (a second turn where P would leave its range: M moves, and P comes by exponents)
 #pragma unroll 1
                 for (int turn = 0;; ++turn) {
-                    if (move) {
+                    float top = -INFINITY, ymax = 0.f, odd = 0.f;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) lv[u][h] = __log2f(fabsf(vn[u][h]));
+                        for (int h = 0; h < 2; ++h) {
+                            odd = fmaf(kn[u][h], 0.f, fmaf(vn[u][h], 0.f, odd));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float x[2], y[2];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float a = -INFINITY, b = -INFINITY;  // the most score, and with the V norm (NaN left out)
+                                for (int k = 0; k < 2; ++k) {
+                                    x[k] = fmaf(acc[u][nt][2 * h + k] * kn[u][h], cq[nt][k], nm[nt][k]);
+                                    if (!all) x[k] = (on[u][h] >> (2 * nt + k)) & 1u ? x[k] : -INFINITY;
+                                }
+                                top = pp_max3(top, x[0], x[1]);
 #pragma unroll
-                                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        float v = acc[u][nt][2 * h + k] * kn[u][h] * cq[nt][k];
-                                        if (!all) v = (on[u][h] >> (2 * nt + k)) & 1u ? v : -INFINITY;
-                                        a = fmaxf(a, v);
-                                        b = fmaxf(b, v + lv[u][h]);
+                                for (int k = 0; k < 2; ++k) {
+                                    const float e = pp_exp2(x[k]), w = vn[u][h] * cc[nt][k];
+                                    p[u][nt][2 * h + k] = e;
+                                    y[k] = e * w;
+                                    ymax = pp_max3(ymax, fabsf(y[k]), fabsf(w) * 1e-33f);
+                                    if (turn == 2) {  // (no M: no V norm but 0)
+                                        const float d = M[nt][k] == -INFINITY ? 0.f : -nm[nt][k] - M[nt][k];
+                                        y[k] = copysignf(pp_exp2(x[k] + (lv[u][h] + d)), vn[u][h]);
                                     }
-#pragma unroll
-                                for (int o = 4; o < 32; o *= 2) {
-                                    a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
-                                    b = fmaxf(b, __shfl_xor_sync(kAll, b, o));
                                 }
-                                if (nm[nt][k] == -INFINITY) continue;  // past the item's rows
-                                const float m0 = -nm[nt][k], M0 = M[nt][k], m1 = fmaxf(m0, a);
-                                const float M1 = b > M0 + 15.f || (M0 == -INFINITY && b > -INFINITY) ? b - 7.f : M0;
-                                const float fl = m0 == m1 ? 1.f : pp_exp2(m0 - m1), fo = M0 == M1 ? 1.f : pp_exp2(M0 - M1);
-                                nm[nt][k] = -m1;
-                                M[nt][k] = M1;
-                                l[nt][k] *= fl;
-#pragma unroll
-                                for (int mt = 0; mt < KK; ++mt) {
-                                    O[nt][mt][k] *= fo;
-                                    O[nt][mt][2 + k] *= fo;
-                                }
-                                cc[nt][k] = m1 == -INFINITY || M1 == -INFINITY ? 0.f : pp_exp2(m1 - M1);
-                            }
-                        scores();
-                    }
-                    // probabilities, as B fragments
-                    float ymax = 0.f, wmax = 0.f;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float p0 = pp_exp2(xs[u][nt][2 * h]), p1 = pp_exp2(xs[u][nt][2 * h + 1]);
-                                const float w0 = vn[u][h] * cc[nt][0], w1 = vn[u][h] * cc[nt][1];
-                                float y0 = p0 * w0, y1 = p1 * w1;
-                                if (turn) {  // the factor may leave fp32 (no M: no V norm but 0)
-                                    const float d0 = M[nt][0] == -INFINITY ? 0.f : -nm[nt][0] - M[nt][0];
-                                    const float d1 = M[nt][1] == -INFINITY ? 0.f : -nm[nt][1] - M[nt][1];
-                                    y0 = copysignf(pp_exp2(xs[u][nt][2 * h] + (lv[u][h] + d0)), vn[u][h]);
-                                    y1 = copysignf(pp_exp2(xs[u][nt][2 * h + 1] + (lv[u][h] + d1)), vn[u][h]);
-                                } else {
-                                    ymax = pp_max3(ymax, fabsf(y0), fabsf(y1));
-                                    wmax = pp_max3(wmax, fabsf(w0), fabsf(w1));
-                                }
-                                const __half2 hh = __floats2half2_rn(y0, y1);
+                                const __half2 hh = __floats2half2_rn(y[0], y[1]);
                                 pb[u][nt][h] = *reinterpret_cast<const uint32_t*>(&hh);
                             }
-                    if (turn) break;
-                    // (V norms beside a row that had none but 0 so far: its factor is 0)
-                    bool none = false;
+                        }
+                    if (turn == 2 || !__any_sync(kAll, top > 8.f || ymax > 32768.f || odd != 0.f || zero)) break;
+                    if (turn == 1) continue;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(fabsf(kn[u][h]) <= FLT_MAX && fabsf(vn[u][h]) <= FLT_MAX))
+                                kn[u][h] = __uint_as_float(0x7FFFFFFFu), vn[u][h] = 0.f;
+                            lv[u][h] = __log2f(fabsf(vn[u][h]));
+                        }
+                    zero = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) none = none || (M[nt][k] == -INFINITY && fabsf(nm[nt][k]) <= FLT_MAX);
-                    if (!__any_sync(kAll, ymax > 32768.f || wmax > 1e37f || none)) break;
-                    move = true;
+                        for (int k = 0; k < 2; ++k) {
+                            float a = -INFINITY, b = -INFINITY;  // the most score, and with the V norm (NaN left out)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float v = acc[u][nt][2 * h + k] * kn[u][h] * cq[nt][k];
+                                    if (!all) v = (on[u][h] >> (2 * nt + k)) & 1u ? v : -INFINITY;
+                                    a = fmaxf(a, v);
+                                    b = fmaxf(b, v + lv[u][h]);
+                                }
+#pragma unroll
+                            for (int o = 4; o < 32; o *= 2) {
+                                a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+                                b = fmaxf(b, __shfl_xor_sync(kAll, b, o));
+                            }
+                            if (nm[nt][k] == -INFINITY) continue;  // past the item's rows
+                            const float m0 = -nm[nt][k], M0 = M[nt][k], m1 = fmaxf(m0, a);
+                            const float M1 = b > M0 + 15.f || (M0 == -INFINITY && b > -INFINITY) ? b - 7.f : M0;
+                            const float fl = m0 == m1 ? 1.f : pp_exp2(m0 - m1), fo = M0 == M1 ? 1.f : pp_exp2(M0 - M1);
+                            nm[nt][k] = -m1;
+                            M[nt][k] = M1;
+                            l[nt][k] *= fl;
+#pragma unroll
+                            for (int mt = 0; mt < KK; ++mt) {
+                                O[nt][mt][k] *= fo;
+                                O[nt][mt][2 + k] *= fo;
+                            }
+                            cc[nt][k] = m1 == -INFINITY || M1 == -INFINITY ? 0.f : pp_exp2(m1 - M1);
+                            zero = zero || (M1 == -INFINITY && m1 > -INFINITY);
+                        }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -661,17 +631,18 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            l[nt][0] += pp_exp2(xs[u][nt][2 * h]);
-                            l[nt][1] += pp_exp2(xs[u][nt][2 * h + 1]);
+                            l[nt][0] += p[u][nt][2 * h];
+                            l[nt][1] += p[u][nt][2 * h + 1];
                             pb[u][nt][h] = fw_transpose(pb[u][nt][h]);
                         }
-                const uint32_t sv = sb + 16 * D;
-                if (A.v_bits == 4) fw_output<D, NT, 4>(sv, vslot, pb, g, t, O);
-                else if (A.v_bits == 3) fw_output<D, NT, 3>(sv, vslot, pb, g, t, O);
-                else fw_output<D, NT, 2>(sv, vslot, pb, g, t, O);
+                if (A.v_bits == 4) fw_output<D, NT, 4>(s_v, vslot, pb, g, t, O);
+                else if (A.v_bits == 3) fw_output<D, NT, 3>(s_v, vslot, pb, g, t, O);
+                else fw_output<D, NT, 2>(s_v, vslot, pb, g, t, O);
+                }
                 __syncwarp();
-                issue();
+                if (lane == 0) mbar_arrive(free_ + st);
                 ++taken;
+                bring();
             }
 
             // ---- the warps' rows put together
@@ -766,11 +737,20 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 __syncthreads();
             }
         }
+        if (!bad) {  // the record at the end
+            if (__all_sync(kAll, pp_wait(full + taken % S, (taken / S) & 1, abort_f, status))) {
+                if (lane == 0) mbar_arrive(free_ + taken % S);
+                ++taken;
+            } else {
+                bad = true;
+            }
+        }
         __syncthreads();  // the jobs have been read
     }
     if (tid == 0) pp_report<Z, MODE>(A, *start, *share, cur, seq, true, has);
-    // copies in flight land before the CTA leaves (bounded; none unless a wait gave up)
-    for (; taken < issued; ++taken) mbar_wait(bars + taken % S, (taken / S) & 1);
+    // after a wait that gave up: the copies in flight land before the CTA leaves (bounded)
+    if (bad)
+        for (uint32_t i = put > (uint32_t)S ? put - S : 0; i < put; ++i) mbar_wait(full + i % S, (i / S) & 1);
     griddep_launch();
     __syncthreads();
     if (tid == 0 && *abort_f) *reinterpret_cast<int4*>(A.meta + (int64_t)blockIdx.x * kPpMeta) = make_int4(kShareFailed, -1, 0, 0);
