@@ -8,6 +8,7 @@ kernels.  There is no fallback: if ``libtq.so`` is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from contextlib import nullcontext
 from dataclasses import dataclass
@@ -727,19 +728,20 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
             _raw_stream(dst.device)))
 
 
-_FRESH: dict = {}  # per device, stream and length: int32 tensors that no call has had yet
+_FRESH: dict = {}  # per device, stream, length and type: tensors that no call has had yet
 
 
-def _fresh(device, stream, n):
-    """A new int32 tensor [n], several to an allocation (one costs more than half
-    of a small call); in a capture one of the graph's own memory."""
+def _fresh(device, stream, n, dtype=_INT32):
+    """A new tensor [n] (a shape of more too), several to an allocation (one costs
+    more than half of a small call); in a capture one of the graph's own memory."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=_INT32, device=device)
-    key = (device.index, stream, n)
+        return torch.empty(n, dtype=dtype, device=device)
+    key = (device.index, stream, n, dtype)
     try:
         return _FRESH[key].pop()
     except (KeyError, IndexError):  # none left, maybe since another thread took the last
-        new = list(torch.empty(max(1, min(64, 65536 // n)), n, dtype=_INT32, device=device).unbind())
+        shape = n if isinstance(n, tuple) else (n,)
+        new = list(torch.empty(max(1, min(64, 65536 // max(1, math.prod(shape)))), *shape, dtype=dtype, device=device).unbind())
         first = new.pop()
         _FRESH[key] = new
         return first
@@ -834,11 +836,11 @@ def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_s
             raise ValueError("parents has one entry per token and its masks at least one word")
     n_seqs, max_pages = bt.shape
     with _on(dev):
+        stream = _raw_stream(dev)
         if out is None:
-            out = TokenSlots(torch.empty(n_seqs + 1, dtype=_INT32, device=dev),
-                             torch.empty(n_tokens, dtype=_INT32, device=dev),
-                             torch.empty(n_tokens, dtype=torch.int64, device=dev),
-                             None if parents is None else torch.empty(n_tokens, mask_words, dtype=_INT32, device=dev))
+            out = TokenSlots(_fresh(dev, stream, n_seqs + 1), _fresh(dev, stream, n_tokens),
+                             _fresh(dev, stream, n_tokens, torch.int64),
+                             None if parents is None else _fresh(dev, stream, (n_tokens, mask_words)))
         else:
             _ints(dev, out.cu_q, out.positions)
             if out.slots.dtype != torch.int64 or out.slots.device != dev or not out.slots.is_contiguous():
@@ -853,7 +855,7 @@ def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_s
             PageTableView(bt.data_ptr(), table.lens.data_ptr(), None), n_seqs, max_pages, table.refs.numel(), page_size,
             counts.data_ptr(), None if parents is None else parents.data_ptr(), mask_words, n_tokens,
             out.cu_q.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-            None if parents is None else out.mask.data_ptr(), _raw_stream(dev)))
+            None if parents is None else out.mask.data_ptr(), stream))
     return out
 
 
@@ -893,14 +895,15 @@ def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_
     _ints(dev, counts, keep, n_keep)
     with _on(dev):
         view = table._view(layers, bt.shape)
+        stream = _raw_stream(dev)
         if out is None:
-            out = torch.empty(bt.shape[0], dtype=_INT32, device=dev)
+            out = _fresh(dev, stream, bt.shape[0])
         _ints(dev, out)
         if out.numel() != bt.shape[0]:
             raise ValueError("one new length per row")
         _check("tq_pages_keep", lib().tq_pages_keep(
             view, bt.shape[0], bt.shape[1], counts.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr(),
-            out.data_ptr(), layers.views, len(layers.views), *layers.args, _raw_stream(dev)))
+            out.data_ptr(), layers.views, len(layers.views), *layers.args, stream))
     return out
 
 

@@ -1180,7 +1180,9 @@ tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const in
     const tq_status st = check_layers(layers, n_layers, Hkv, d, k_bits, v_bits);
     if (st != TQ_OK) return st;
     const int shift = page_shift_of(layers[0].page_size);
-    if (((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows || max_keep > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+    if (((int64_t)max_pages << shift) > INT32_MAX || n_seqs > kMaxRows || max_keep > (1 << 20) ||
+        (int64_t)n_seqs * Hkv > (1 << 28))  // blocks of a launch
+        return TQ_ERR_UNSUPPORTED;
     if (!table.block_table || !table.lens || !table.refs || !counts || !keep || !n_keep || !new_lens)
         return TQ_ERR_INVALID_ARG;
     if (!aligned4(table.block_table) || !aligned4(table.lens) || !aligned4(table.refs) || !aligned4(counts) ||

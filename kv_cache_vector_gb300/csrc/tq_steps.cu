@@ -41,7 +41,8 @@ struct SlotsArgs {
 };
 
 __global__ void __launch_bounds__(kSlThreads) k_pages_slots(const SlotsArgs A, int* status) {
-    __shared__ int before[kSlThreads + 1];  // tokens of the rows of the threads before this one
+    __shared__ int before[kSlThreads];  // tokens of the rows of the threads before this one
+    __shared__ int2 last[kSlThreads];   // count and length of the thread's last row
     __shared__ long long sums[kSlThreads / 32];
     __shared__ int flags[kSlThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(kSlThreads) k_pages_slots(const SlotsArgs A, i
         const int n = A.counts[b], len = A.lens[b];
         bad = bad || n < 0 || len < n || len > cap || (A.parents && n > 32 * A.words);
         mine += max(n, 0);
+        last[tid] = make_int2(n, len);
     }
     long long incl = mine;
 #pragma unroll
@@ -105,12 +107,16 @@ __global__ void __launch_bounds__(kSlThreads) k_pages_slots(const SlotsArgs A, i
             if (before[m] <= t) lo = m;
             else hi = m;
         }
-        int b = lo * each, i = (int)t - before[lo], n = A.counts[b];
-        while (i >= n) {  // (ends: the threads' rows hold the token)
-            i -= n;
-            n = A.counts[++b];
+        int b = lo * each, i = (int)t - before[lo], n = last[lo].x, base = last[lo].y - n;
+        if (each > 1) {
+            n = A.counts[b];
+            while (i >= n) {  // (ends: the threads' rows hold the token)
+                i -= n;
+                n = A.counts[++b];
+            }
+            base = A.lens[b] - n;
         }
-        const int base = A.lens[b] - n, at = base + i;
+        const int at = base + i;
         const int page = A.bt[(int64_t)b * A.max_pages + (at >> A.shift)];
         const bool ok = page >= 0 && page < A.n_pages;
         if (!ok) report_timeout(status, kStepStatusPage);
@@ -201,8 +207,16 @@ __global__ void __launch_bounds__(32 * kAsWarps) k_append_slots(const SlotRows A
 // to the place of token i.  The list ascends, so keep[b][i] >= i, and a place
 // that a token moves to is the source of no later one: a warp moves a (row,
 // layer, KV head)'s tokens a few at a time, each time reading all of them before
-// it writes.  Lists of the same row are checked by every warp alike.
+// it writes.  A CTA works out one row's places once, for kKpEach (layer, KV
+// head) pairs a warp; every CTA of a row checks its list alike.
+//
+// Bound by latency (lists, pages, then the rows): 64 rows of which 122 tokens
+// move in 32 layers, 7.5 MB in all, TIME_KEEP us in a graph.
 constexpr int kKpWarps = 8;
+constexpr int kKpThreads = 32 * kKpWarps;
+constexpr int kKpEach = 4;     // (layer, KV head) pairs of a warp
+constexpr int kKpList = 128;   // tokens whose places are known at a time
+constexpr int kKpBatch = 8;    // tokens that a warp moves at a time
 constexpr int kKpLayers = 64;  // most layers per launch
 
 template <int MAX>
@@ -219,100 +233,127 @@ struct KeepArgs {
     const int32_t* n_keep;
     int32_t* new_lens;  // nullptr: another launch writes them
     int64_t n_pages;
-    int n_seqs, max_pages, max_keep, shift, Hkv, k_bytes, v_bytes;  // bytes of a packed row
+    int n_seqs, max_pages, max_keep, shift, Hkv, k_bytes, v_bytes, slices;  // bytes of a packed row
 };
 
-// Rows of `units` T each: lanes of the batch's rows [0, n), whose places are
-// src and dst of lane r.  All loads first.
+// n rows of `units` T each, from the places src to the places dst (rows of KV
+// head 0; `up` further on): the loads, and the stores.
 template <typename T, int U>
-__device__ __forceinline__ void keep_rows(void* base, int units, int n, int64_t src, int64_t dst, int lane) {
+struct KeepRows {
     T v[U];
-    T* p = static_cast<T*>(base);
-    const int all = n * units;
+    __device__ __forceinline__ void load(const void* base, int units, int n, const long long* src, int64_t up, int lane) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int w = 32 * k + lane, r = w < all ? w / units : 0;
-        const int64_t s = __shfl_sync(0xFFFFFFFFu, src, r);
-        if (w < all) v[k] = p[s * units + (w - r * units)];
+        for (int k = 0; k < U; ++k) {
+            const int w = 32 * k + lane, r = w / units;
+            if (w < n * units) v[k] = static_cast<const T*>(base)[(src[r] + up) * units + (w - r * units)];
+        }
     }
+    __device__ __forceinline__ void store(void* base, int units, int n, const long long* dst, int64_t up, int lane) const {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int w = 32 * k + lane, r = w / units;
+            if (w < n * units) static_cast<T*>(base)[(dst[r] + up) * units + (w - r * units)] = v[k];
+        }
+    }
+};
+
+// A batch of tokens, packed rows in units of TK and TV (at most 128 bytes a row).
+template <typename TK, typename TV>
+__device__ __forceinline__ void keep_batch(void* const (&at)[4], int k_bytes, int v_bytes, int n, const long long* src,
+                                           const long long* dst, int64_t up, int lane) {
+    KeepRows<TK, sizeof(TK) == 16 ? 2 : 1> k;
+    KeepRows<TV, sizeof(TV) == 16 ? 2 : 1> v;
+    KeepRows<uint32_t, 1> kn, vn;
+    k.load(at[0], k_bytes / (int)sizeof(TK), n, src, up, lane);
+    v.load(at[2], v_bytes / (int)sizeof(TV), n, src, up, lane);
+    kn.load(at[1], 1, n, src, up, lane);
+    vn.load(at[3], 1, n, src, up, lane);
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int w = 32 * k + lane, r = w < all ? w / units : 0;
-        const int64_t t = __shfl_sync(0xFFFFFFFFu, dst, r);
-        if (w < all) p[t * units + (w - r * units)] = v[k];
-    }
+    k.store(at[0], k_bytes / (int)sizeof(TK), n, dst, up, lane);
+    v.store(at[2], v_bytes / (int)sizeof(TV), n, dst, up, lane);
+    kn.store(at[1], 1, n, dst, up, lane);
+    vn.store(at[3], 1, n, dst, up, lane);
 }
-// A batch of up to 8 packed rows of at most 128 bytes.
-__device__ __forceinline__ void keep_packed(void* base, int bytes, int n, int64_t src, int64_t dst, int lane) {
-    if (bytes % 16 == 0) keep_rows<uint4, 2>(base, bytes / 16, n, src, dst, lane);
-    else if (bytes % 8 == 0) keep_rows<uint2, 1>(base, bytes / 8, n, src, dst, lane);
-    else keep_rows<uint32_t, 1>(base, bytes / 4, n, src, dst, lane);
+template <typename TK>
+__device__ __forceinline__ void keep_batch(void* const (&at)[4], int k_bytes, int v_bytes, int n, const long long* src,
+                                           const long long* dst, int64_t up, int lane) {
+    if (v_bytes % 16 == 0) keep_batch<TK, uint4>(at, k_bytes, v_bytes, n, src, dst, up, lane);
+    else if (v_bytes % 8 == 0) keep_batch<TK, uint2>(at, k_bytes, v_bytes, n, src, dst, up, lane);
+    else keep_batch<TK, uint32_t>(at, k_bytes, v_bytes, n, src, dst, up, lane);
 }
-constexpr int kKpBatch = 8;
 
 template <int MAX>
-__global__ void __launch_bounds__(32 * kKpWarps) k_pages_keep(const __grid_constant__ KeepLayers<MAX> P, int L,
-                                                              const KeepArgs A, int* status) {
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kKpThreads) k_pages_keep(const __grid_constant__ KeepLayers<MAX> P, int L, const KeepArgs A,
+                                                           int* status) {
+    __shared__ long long s_src[kKpList], s_dst[kKpList];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / A.slices, slice = blockIdx.x - b * A.slices;
     griddep_wait();
     griddep_launch();
+    const int n = A.counts[b], len = A.lens[b], k = A.n_keep[b];
+    const int32_t* keep = A.keep + (int64_t)b * A.max_keep;
+    const int32_t* row = A.bt + (int64_t)b * A.max_pages;
+    bool ok = n >= 0 && len >= n && len <= ((int64_t)A.max_pages << A.shift) && k >= 0 && k <= n && k <= A.max_keep;
+    const int base = len - n;
+    // token i of the list: where it is and where it goes, as rows of KV head 0
+    auto find = [&](int i, bool& moves) {
+        moves = false;
+        if (i >= k) return true;
+        const int x = keep[i];
+        if (x < i || x >= n || (i > 0 && x <= keep[i - 1])) return false;
+        if (x == i) return true;
+        moves = true;
+        const int a = base + x, z = base + i, m = (1 << A.shift) - 1;
+        const int pa = row[a >> A.shift], pz = row[z >> A.shift];
+        if (pa < 0 || pa >= A.n_pages || pz < 0 || pz >= A.n_pages || A.refs[pa] > 1 || A.refs[pz] > 1) return false;
+        s_src[i % kKpList] = (((int64_t)pa * A.Hkv) << A.shift) + (a & m);
+        s_dst[i % kKpList] = (((int64_t)pz * A.Hkv) << A.shift) + (z & m);
+        return true;
+    };
+    int moving = 0;
+    if (ok) {
+        for (int i0 = 0; i0 < k; i0 += kKpList) {
+            bool moves = false, fine = true;
+            if (tid < kKpList) fine = find(i0 + tid, moves);
+            moving += __syncthreads_count(moves);
+            ok = __syncthreads_and(fine) && ok;
+        }
+    }
+    if (slice == 0 && tid == 0 && A.new_lens) {
+        A.new_lens[b] = ok ? base + k : len;
+        if (!ok) report_timeout(status, kStepStatusKeep);
+    }
+    if (!ok || moving == 0) return;
+    const int first = k - moving;  // all behind the first that moves do
     const int LH = L * A.Hkv;
-    const int64_t items = (int64_t)A.n_seqs * LH;
-    for (int64_t it = (int64_t)blockIdx.x * kKpWarps + (threadIdx.x >> 5); it < items;
-         it += (int64_t)gridDim.x * kKpWarps) {
-        const int b = (int)(it / LH), lh = (int)(it - (int64_t)b * LH), l = lh / A.Hkv, h = lh - l * A.Hkv;
-        const int n = A.counts[b], len = A.lens[b], k = A.n_keep[b];
-        const int32_t* keep = A.keep + (int64_t)b * A.max_keep;
-        const int32_t* row = A.bt + (int64_t)b * A.max_pages;
-        bool ok = n >= 0 && len >= n && len <= ((int64_t)A.max_pages << A.shift) && k >= 0 && k <= n && k <= A.max_keep;
-        const int base = len - n;
-        // lane r's token of the list from i on: where it is and where it goes, as rows of head 0
-        auto find = [&](int i, int64_t& src, int64_t& dst, bool& moves) {
-            const int x = i < k ? keep[i] : n + i;
-            const int below = i > 0 && i < k ? keep[i - 1] : -1;
-            moves = false;
-            if (i >= k) return true;
-            if (x < i || x >= n || x <= below) return false;
-            moves = x != i;
-            if (!moves) return true;
-            const int a = base + x, z = base + i;
-            const int pa = row[a >> A.shift], pz = row[z >> A.shift];
-            if (pa < 0 || pa >= A.n_pages || pz < 0 || pz >= A.n_pages || A.refs[pa] > 1 || A.refs[pz] > 1) return false;
-            const int m = (1 << A.shift) - 1;
-            src = (((int64_t)pa * A.Hkv + h) << A.shift) + (a & m);
-            dst = (((int64_t)pz * A.Hkv + h) << A.shift) + (z & m);
-            return true;
-        };
-        int64_t src = 0, dst = 0;
-        bool moves = false, any = false;
-        int first = k;  // the first token that moves: all behind it do
-        if (ok)
-            for (int i0 = 0; i0 < k; i0 += 32) {
-                const bool fine = find(i0 + lane, src, dst, moves);
-                ok = __all_sync(0xFFFFFFFFu, fine) && ok;
-                const unsigned who = __ballot_sync(0xFFFFFFFFu, moves);
-                if (who && !any) first = i0 + __ffs(who) - 1;
-                any = any || who;
+    for (int i0 = k <= kKpList ? first : first / kKpList * kKpList; i0 < k; i0 += kKpList) {
+        int end = k;
+        if (k > kKpList) {  // the list in pieces: their places once more
+            __syncthreads();
+            bool moves;
+            if (tid < kKpList) find(i0 + tid, moves);
+            end = min(k, i0 + kKpList);
+            __syncthreads();
+        }
+        for (int e = 0; e < kKpEach; ++e) {
+            const int lh = (slice * kKpEach + e) * kKpWarps + warp;
+            if (lh >= LH) break;
+            const int l = lh / A.Hkv, h = lh - l * A.Hkv;
+            const int64_t up = (int64_t)h << A.shift;
+            for (int i = max(i0, first); i < end; i += kKpBatch) {
+                const int m = min(kKpBatch, end - i);
+                const long long *src = s_src + i % kKpList, *dst = s_dst + i % kKpList;
+                if (A.k_bytes % 16 == 0) keep_batch<uint4>(P.at[l], A.k_bytes, A.v_bytes, m, src, dst, up, lane);
+                else if (A.k_bytes % 8 == 0) keep_batch<uint2>(P.at[l], A.k_bytes, A.v_bytes, m, src, dst, up, lane);
+                else keep_batch<uint32_t>(P.at[l], A.k_bytes, A.v_bytes, m, src, dst, up, lane);
             }
-        if (lh == 0 && A.new_lens && lane == 0) {
-            A.new_lens[b] = ok ? base + k : len;
-            if (!ok) report_timeout(status, kStepStatusKeep);
         }
-        if (!ok || !any) continue;
-        for (int i = first; i < k; i += kKpBatch) {
-            const int m = min(kKpBatch, k - i);
-            find(lane < m ? i + lane : k, src, dst, moves);
-            keep_packed(P.at[l][0], A.k_bytes, m, src, dst, lane);
-            keep_packed(P.at[l][2], A.v_bytes, m, src, dst, lane);
-            keep_rows<uint32_t, 1>(P.at[l][1], 1, m, src, dst, lane);
-            keep_rows<uint32_t, 1>(P.at[l][3], 1, m, src, dst, lane);
-        }
+        if (k <= kKpList) break;
     }
 }
 
 template <int MAX>
-static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, const KeepArgs& A, cudaStream_t s) {
+static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, KeepArgs A, cudaStream_t s) {
     KeepLayers<MAX> P;
     for (int l = 0; l < L; ++l) {
         const tq_paged_cache& x = c.layers[l0 + l];
@@ -321,10 +362,8 @@ static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, const KeepA
         P.at[l][2] = x.v_packed;
         P.at[l][3] = x.v_norm;
     }
-    const int64_t items = (int64_t)A.n_seqs * L * A.Hkv, want = (items + kKpWarps - 1) / kKpWarps;
-    const int64_t most = (int64_t)num_sms() * 64;
-    return launch_pdl(k_pages_keep<MAX>, dim3((unsigned)(want < most ? want : most)), dim3(32 * kKpWarps), 0, s, P, L, A,
-                      status_word());
+    A.slices = (L * A.Hkv + kKpWarps * kKpEach - 1) / (kKpWarps * kKpEach);
+    return launch_pdl(k_pages_keep<MAX>, dim3((unsigned)A.n_seqs * A.slices), dim3(kKpThreads), 0, s, P, L, A, status_word());
 }
 
 }  // namespace dev
