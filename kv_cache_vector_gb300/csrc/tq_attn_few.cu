@@ -61,7 +61,7 @@ struct FwGeo {
     static constexpr int kStreams = 1;
     static constexpr int kCostPair = 1, kCostSplit = 1, kCostItem = 4;  // of a block and an item (pp_start)
     // registers: the output takes D / 4 NT, the queries D / 8 NT
-    static constexpr int kWarps = D * NT >= 256 ? 8 : 12;
+        static constexpr int kWarps = D * NT >= 256 ? 8 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kQuads = kWarps / 4;
     static constexpr int kStages = 2;
@@ -146,11 +146,13 @@ __device__ __forceinline__ void fw_field(uint32_t row, int at, uint32_t (&w)[(BI
         fw_words<N>(row + at * (BITS / 8), w);
     } else {
         const uint32_t off = (uint32_t)at * BITS, sh = off & 31, a = row + (off >> 5) * 4;
-        uint32_t r[N + 1];
+        // a field starts at a multiple of the power of two in BITS: the words that it touches
+        constexpr int STEP = BITS & -BITS, M = (BITS + 32 - STEP + 31) / 32;
+        uint32_t r[M];
 #pragma unroll
-        for (int i = 0; i <= N; ++i) r[i] = fw_word(a + 4 * i);
+        for (int i = 0; i < M; ++i) r[i] = fw_word(a + 4 * i);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], sh);
+        for (int i = 0; i < N; ++i) w[i] = i + 1 < M ? __funnelshift_r(r[i], r[i + 1 < M ? i + 1 : i], sh) : r[i] >> sh;
     }
 }
 // Pair q of a field: the byte that holds the pair's first bit (of the field, or
@@ -247,7 +249,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
            int* status) {
     using Z = FwGeo<D, NT>;
     constexpr int W = Z::kWarps, S = Z::kStages, KK = D / 16;
-    constexpr bool QREG = NT <= 2;
+    constexpr bool QREG = NT == 2 || D == 256;  // queries in registers, where they cost no warps
     constexpr uint32_t kAll = 0xFFFFFFFFu;
     extern __shared__ __align__(16) unsigned char fw_smem[];
     const uint32_t base = smem_addr(fw_smem);
@@ -346,71 +348,95 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
         if (nj == 0) break;
 
         // The quad's blocks: numbers quad, quad + kQuads, ... of every part's, and then
-        // a record without one.  Its warps bring them in turn, S ahead.
-        int pj = -1, pc = 0, pn = 0;  // of the next block: its part, number, and the part's blocks
-        auto bring = [&]() {
-            if (pj >= nj || bad) return;
-            while (pc >= pn) {
-                if (++pj >= nj) break;
-                pc = quad, pn = jobs[pj].nb;
+        // a record without one.  Its warps bring them in turn, each the fourth after its
+        // last, whose page ids it looks up that long before.
+        const int blocks = (int)__reduce_add_sync(
+            kAll, lane < nj ? (unsigned)max(0, (jobs[lane].nb - quad + Z::kQuads - 1) / Z::kQuads) : 0u);
+        const uint32_t put0 = put;
+        int mj = -1, mc = 0, mn = 0, m_t0 = 0, m_page = INT_MIN;  // this warp's next: part, block, the part's blocks; position, page
+        auto look = [&](int steps) {
+            for (; steps > 0 && mj < nj; --steps) {
+                mc += Z::kQuads;
+                while (mc >= mn && ++mj < nj) mc = quad, mn = jobs[mj].nb;
             }
+            m_page = INT_MIN;
+            if (mj >= nj) return;
+            const FwJob& x = jobs[mj];
+            m_t0 = pp_block_at<Z, MODE>(A, x.kv_lo, x.kv_end, x.blk + mc) * Z::kN;
+            const int pos = m_t0 + seg_at;
+            if (seg_at < Z::kN && pos < x.kv_end && (pos + seg > x.kv_lo || (MODE == kPpSinks && pos < A.sinks)))
+                m_page = A.bt[(int64_t)x.b * A.max_pages + (pos >> A.shift)];
+        };
+        look(1 + (int)((sub - put0) & 3));
+        auto bring = [&]() {
+            if (bad || (int)(put - put0) > blocks) return;
             const uint32_t st = put % S;
             if ((put & 3) == (uint32_t)sub) {
-                const FwJob& x = jobs[min(pj, nj - 1)];
-                const int t0 = pp_block_at<Z, MODE>(A, x.kv_lo, x.kv_end, x.blk + pc) * Z::kN, pos = t0 + seg_at;
-                int page = INT_MIN;
-                if (pj < nj && seg_at < Z::kN && pos < x.kv_end && (pos + seg > x.kv_lo || (MODE == kPpSinks && pos < A.sinks)))
-                    page = A.bt[(int64_t)x.b * A.max_pages + (pos >> A.shift)];
-                const bool have = page >= 0 && page < A.c.n_pages;
-                if (page != INT_MIN && !have) report_timeout(status, kPpStatusPage);
+                const bool have = m_page >= 0 && m_page < A.c.n_pages;
+                if (m_page != INT_MIN && !have) report_timeout(status, kPpStatusPage);
                 const uint32_t mask = __ballot_sync(kAll, have && (lane & 3) == 0);
                 // (a wait that gives up is noticed at the block's own)
                 if (put >= (uint32_t)S) pp_wait(free_ + st, (put / S - 1) & 1, abort_f, status);
                 __syncwarp();
                 if (lane == 0) {
-                    recs[st].x = t0;
-                    recs[st].y = pj;
+                    recs[st].x = m_t0;
+                    recs[st].y = mj;
                     recs[st].z = (int)mask;
                     mbar_arrive_expect_tx(full + st, __popc(mask) * seg * (k_row + v_row + 8));
                 }
                 __syncwarp();
                 if (have && *abort_f == 0) {
-                    const int64_t row = (((int64_t)page * A.Hkv + x.h) << A.shift) + (pos & ((1 << A.shift) - 1));
+                    const int pos = m_t0 + seg_at;
+                    const int64_t row = (((int64_t)m_page * A.Hkv + jobs[mj].h) << A.shift) + (pos & ((1 << A.shift) - 1));
                     fence_async_smem();  // earlier reads of this stage come first
                     bulk_load(stage_at(st) + my_dst, my_src + row * my_row, seg * my_row, full + st);
                 }
+                look(4);
             }
             ++put;
-            pc += Z::kQuads;
         };
         for (int i = 0; i < S; ++i) bring();
 
+        // this warp's rows of a part's queries, looked up a part ahead
+        constexpr int E = D / 32, RW = (Z::kRows + W - 1) / W;
+        uint32_t raw[RW][E < 2 ? 1 : E / 2];
+        auto fetch = [&](int j) {
+            if (j >= nj) return;
+            const FwJob& x = jobs[j];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const int r = warp + W * i;
+                if (r >= x.rows) break;
+                const int at_row = x.rest + r, tok = at_row / G;
+                const __nv_bfloat16* src =
+                    A.q + (((int64_t)x.q0 + x.tok0 + tok) * A.Hq + (int64_t)x.h * G + (at_row - tok * G)) * D + E * lane;
+                if constexpr (E == 1) raw[i][0] = *reinterpret_cast<const uint16_t*>(src);
+                else if constexpr (E == 2) raw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                else if constexpr (E == 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    raw[i][0] = v.x, raw[i][1] = v.y;
+                } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    raw[i][0] = v.x, raw[i][1] = v.y, raw[i][2] = v.z, raw[i][3] = v.w;
+                }
+            }
+        };
+        fetch(0);
+
         for (int j = 0; j < nj; ++j) {
-            const FwJob x = jobs[j];
+            const FwJob& x = jobs[j];  // (not copied: registers)
             // ---- queries: a warp rotates a row, rounds it to fp16 under a power of
             // two and stores it in the order of the B fragments
             if (x.nb > 0) {
-                constexpr int E = D / 32;
-#pragma unroll 1
-                for (int r = warp; r < Z::kRows; r += W) {
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = warp + W * i;
+                    if (r >= Z::kRows) break;
                     float y[E];
                     if (r < x.rows) {
-                        const int i = x.rest + r, tok = i / G;
-                        const __nv_bfloat16* src =
-                            A.q + (((int64_t)x.q0 + x.tok0 + tok) * A.Hq + (int64_t)x.h * G + (i - tok * G)) * D + E * lane;
-                        uint32_t raw[E < 2 ? 1 : E / 2];
-                        if constexpr (E == 1) raw[0] = *reinterpret_cast<const uint16_t*>(src);
-                        else if constexpr (E == 2) raw[0] = *reinterpret_cast<const uint32_t*>(src);
-                        else if constexpr (E == 4) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(src);
-                            raw[0] = v.x, raw[1] = v.y;
-                        } else {
-                            const uint4 v = *reinterpret_cast<const uint4*>(src);
-                            raw[0] = v.x, raw[1] = v.y, raw[2] = v.z, raw[3] = v.w;
-                        }
 #pragma unroll
                         for (int k = 0; k < E; ++k) {
-                            const uint32_t bits = E == 1 ? raw[0] << 16 : k & 1 ? raw[k / 2] & 0xFFFF0000u : raw[k / 2] << 16;
+                            const uint32_t bits = E == 1 ? raw[i][0] << 16 : k & 1 ? raw[i][k / 2] & 0xFFFF0000u : raw[i][k / 2] << 16;
                             y[k] = __uint_as_float(bits ^ sign_mask(P.sgnb, E * lane + k));
                         }
 #pragma unroll
@@ -451,6 +477,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 }
             }
             __syncthreads();
+            fetch(j + 1);
             uint32_t qf[QREG ? NT : 1][QREG ? KK : 1][2];
             const uint32_t qs = Z::kQ + 8u * lane;
             if constexpr (QREG) {
@@ -635,14 +662,16 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                             l[nt][1] += p[u][nt][2 * h + 1];
                             pb[u][nt][h] = fw_transpose(pb[u][nt][h]);
                         }
+                // the next block but one: by now the other warps have read the last
+                if (put - taken < (uint32_t)S) bring();
                 if (A.v_bits == 4) fw_output<D, NT, 4>(s_v, vslot, pb, g, t, O);
                 else if (A.v_bits == 3) fw_output<D, NT, 3>(s_v, vslot, pb, g, t, O);
                 else fw_output<D, NT, 2>(s_v, vslot, pb, g, t, O);
                 }
+                if (put - taken < (uint32_t)S) bring();  // (this block's sub-chunk was not worked on)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(free_ + st);
                 ++taken;
-                bring();
             }
 
             // ---- the warps' rows put together
