@@ -378,8 +378,9 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
 /* The same with first positions that stay visible ("sinks") while a sliding
  * window moves on, for conversations longer than the window: the token at
  * position p attends over positions j <= p with j > p - window or j < sinks.
- * A window of 0 is none, and with 0 sinks this is tq_attn_prefill_paged.  Prompt
- * chunks, drafts and single tokens, ragged in one batch.  Pages between the
+ * A window of 0 is none (sinks then add nothing).  Prompt chunks, drafts and
+ * single tokens, ragged in one batch; batches of few rows (n_q Hq / Hkv <= 16 B)
+ * have a kernel of their own, which reads long contexts twice as fast.  Pages between the
  * sinks and the window of a sequence's first token are not looked at.
  * Arguments, accuracy, status words and errors as tq_attn_prefill_paged
  * (TQ_ERR_INVALID_ARG also for sinks < 0). */
@@ -555,7 +556,8 @@ tq_status tq_append_slots(const tq_plan *plan, int k_bits, int v_bits, const voi
  * (refs above 1) or out of range, stays as it is (new_lens[b] = lens[b]) and sets
  * the device status word to 66.
  * layers, alignment and errors as for the calls above (no workspace; new_lens
- * overlaps none of the inputs). */
+ * overlaps none of the inputs; no layer is given twice; n_seqs Hkv at most
+ * 2^28). */
 tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const int32_t *counts, const int32_t *keep,
                         int max_keep, const int32_t *n_keep, int32_t *new_lens, const tq_paged_cache *layers,
                         int n_layers, int Hkv, int d, int k_bits, int v_bits, tq_stream_t stream);

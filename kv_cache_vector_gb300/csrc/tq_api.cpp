@@ -1188,6 +1188,19 @@ tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const in
     if (!aligned4(table.block_table) || !aligned4(table.lens) || !aligned4(table.refs) || !aligned4(counts) ||
         !aligned4(keep) || !aligned4(n_keep) || !aligned4(new_lens))
         return TQ_ERR_ALIGNMENT;
+    // a layer given twice would be moved twice
+    {
+        constexpr int kAt = 256;
+        const void* at[kAt];
+        const int m = n_layers < kAt ? n_layers : kAt;
+        for (int l = 0; l < m; ++l) at[l] = layers[l].k_packed;
+        std::sort(at, at + m);
+        for (int l = 1; l < m; ++l)
+            if (at[l] == at[l - 1]) return TQ_ERR_INVALID_ARG;
+        for (int l = kAt; l < n_layers; ++l)
+            for (int i = 0; i < l; ++i)
+                if (layers[l].k_packed == layers[i].k_packed) return TQ_ERR_INVALID_ARG;
+    }
     auto span = [](const void* p, uint64_t n) { return Span{reinterpret_cast<uintptr_t>(p), 4 * n}; };
     const uint64_t n = (uint64_t)n_seqs;
     const Span wr = span(new_lens, n);
@@ -1324,8 +1337,14 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
     c.sinks = (int)(seen.sinks < cap ? seen.sinks : cap);
     c.mask = seen.mask;
     c.mask_words = seen.words;
-    // without a window (or without sinks) there is nothing that the sinks add
-    const int mode = seen.mode == tq::kPpSinks && (c.window == 0 || c.sinks == 0) ? (int)tq::kPpCausal : seen.mode;
+    // Few query rows per sequence and KV head (as an average: the lengths are on the
+    // device) have a kernel of their own.  32 sequences of 6000 positions, 32 / 8 heads,
+    // K4/V3, d = 128: 4 rows 75 us here and 167 us in the multi-token kernel, 16 rows 108
+    // and 167, 24 rows (two items) 216 and 167; d = 256: 8 rows 127 and 289, 16 rows
+    // (two items) 244 and 301.
+    const bool few = seen.mode != tq::kPpCausal && n_q * (Hq / Hkv) <= (int64_t)16 * B;
+    // in the multi-token kernel sinks without a window (or none) are the causal mode
+    const int mode = seen.mode == tq::kPpSinks && !few && (c.window == 0 || c.sinks == 0) ? (int)tq::kPpCausal : seen.mode;
     c.k_bits = k_bits;
     c.v_bits = v_bits;
     c.out_bf16 = out_dtype == TQ_BF16;
@@ -1335,7 +1354,6 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
         c.k_cen[i] = level_half(*P, k_bits, i);
         c.v_cen[i] = level_half(*P, v_bits, i);
     }
-    const bool few = n_q * (Hq / Hkv) <= (int64_t)(P->d == 256 ? 8 : 16) * B;  // query rows per sequence and KV head
     const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
         constexpr int d = decltype(D)::value;
         auto st = reinterpret_cast<cudaStream_t>(stream);

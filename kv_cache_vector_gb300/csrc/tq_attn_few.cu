@@ -3,8 +3,7 @@
 //
 // With few rows the packed rows are what there is to read, and expanding them is
 // the work: tiles in shared memory for the 5th-generation tensor cores take
-// 512 bytes of writes and as many of operand reads per position, three times the
-// time of the copy itself.  Here the products are mma.sync m16n8k16 with
+// 512 bytes of writes and as many of operand reads per position (d = 128).  Here the products are mma.sync m16n8k16 with
 // positions (scores) and dims (output) as rows and query rows as the 8 columns,
 // and the packed rows go from shared memory straight into their A fragments: a
 // pair of indices is one lookup in a table of fp16 pairs, replicated for the 32
@@ -27,6 +26,19 @@
 // positions it does not attend to hold.  The query, the levels and P are rounded
 // to fp16 (2^-11 relative each).  A non-finite norm makes the scores of its
 // position NaN, for the rows that attend to it, and its V row zero.
+//
+// What bounds it.  32 sequences of 6000 positions, 32 / 8 heads, one query token
+// (4 rows), d = 128, K4/V3: 75 us, 2.47 TB/s of packed rows; 16 rows 108 us; d = 64
+// 61 us; d = 256, K4/V4 127 us, 3.2 TB/s.  About 960 instructions a chunk and warp,
+// half of them byte permutes and shifts: the ALU is 45% busy, the lookups' pipe 44%,
+// an issue slot in two is used, and 12 warps of 168 registers leave 0.8 of 3 ready.
+// Measured and not kept: 16 warps of 128 registers (86 us, spills), chunks of 64
+// positions in 8 warps (88), V by byte permutes instead of lookups (87), a warp that
+// copies for the others (82: a bulk copy costs it some 100 cycles), rings of 3 blocks
+// with 10 warps (96).  Tiles of 32 rows take 5800 cycles a block of positions, where
+// the multi-token kernel takes 3500 for up to 128.  The same products transposed on
+// tcgen05 (positions on the lanes) took 236 us at 24 rows: a row's factors come to
+// every lane by shared-memory reads, and those and the tiles' own fill that pipe.
 //
 // Every wait is bounded; one that gives up sets the device status word and a
 // flag, and the warps go on without computing, so that the block's barriers stay
@@ -552,7 +564,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                             r0 = max(0, min(first, Z::kRows + 1)) * G - x.rest;
                             r1 = Z::kRows;
                             if (A.window > 0 && !(MODE == kPpSinks && p < A.sinks))
-                                r1 = max(0, min(first + A.window, Z::kRows + 1)) * G - x.rest;
+                                r1 = max(0, min(min(first, Z::kRows + 1) + A.window, Z::kRows + 1)) * G - x.rest;
                         }
                         uint32_t w = 0;
                         const int node = p - x.pos0;
@@ -571,7 +583,8 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 }
                 // ---- probabilities, as B fragments.  Turn 0 takes the maxima as they are; if a
                 // score is 8 above m, a P above 2^15, or a norm not finite, they move and
-                // turn 1 follows, and where the factor of P leaves fp32 turn 2, by exponents
+                // turn 1 follows, and where the factor of P is above 2^100 (a p that is lost
+                // could count) turn 2, by exponents
                 float p[2][NT][4], lv[2][2];
                 uint32_t pb[2][NT][2];
 #pragma unroll 1
@@ -596,7 +609,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                                     const float e = pp_exp2(x[k]), w = vn[u][h] * cc[nt][k];
                                     p[u][nt][2 * h + k] = e;
                                     y[k] = e * w;
-                                    ymax = pp_max3(ymax, fabsf(y[k]), fabsf(w) * 1e-33f);
+                                    ymax = pp_max3(ymax, fabsf(y[k]), fabsf(w) * 0x1p-85f);
                                     if (turn == 2) {  // (no M: no V norm but 0)
                                         const float d = M[nt][k] == -INFINITY ? 0.f : -nm[nt][k] - M[nt][k];
                                         y[k] = copysignf(pp_exp2(x[k] + (lv[u][h] + d)), vn[u][h]);
@@ -814,7 +827,10 @@ static cudaError_t launch_few(const PagedPrefillCall& c, cudaStream_t s) {
 
 template <int D, int MODE>
 cudaError_t launch_attn_few(const PagedPrefillCall& c, cudaStream_t s) {
-    // rows of a sequence and KV head, as an average
+    // One tile of 8 rows, or two for more than 8 rows (of a sequence and KV head, as an
+    // average), which read the positions once: 32 sequences of 6000 positions, 8 rows 79
+    // us, 12 rows 108 us.  At d = 256 two tiles leave no registers (the output alone takes
+    // 128).
     const int64_t rows = c.n_q * (c.Hq / c.Hkv);
     if (D == 256 || rows <= (int64_t)8 * c.B) return dev::launch_few<D, 1, MODE>(c, s);
     return dev::launch_few<D, D == 256 ? 1 : 2, MODE>(c, s);

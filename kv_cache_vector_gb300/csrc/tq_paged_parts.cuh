@@ -39,7 +39,7 @@ struct PpArgs {
     int32_t* meta;  // [shares][kPpMeta]
     int64_t n_q;
     int B, Hq, Hkv, max_pages, shift, window, k_bits, v_bits, out_bf16;
-    int sinks;             // kPpSinks (window > 0)
+    int sinks;             // kPpSinks
     const uint32_t* mask;  // kPpTree: [n_q][words]
     int words;
     uint32_t khi[4], klo[4], vhi[4], vlo[4];  // level bytes (see expand)
@@ -93,7 +93,7 @@ struct PpSeq {
         tiles = (rows + Z::kRows - 1) / Z::kRows;
         base = ctx > n ? (int64_t)(ctx - n) * G : 0;
         cap = A.window > 0 ? (int64_t)A.window * G + Z::kRows : INT64_MAX;
-        if (MODE == kPpSinks) cap += (int64_t)A.sinks * G;
+        if (MODE == kPpSinks && A.window > 0) cap += (int64_t)A.sinks * G;
         if (MODE == kPpTree) base = cap = (int64_t)ctx * G;  // every tile reads all positions
         // tiles before the window's cap binds: base + (k + 1) kRows < cap
         kstar = cap == INT64_MAX ? INT32_MAX : (cap - base - 1) / Z::kRows;

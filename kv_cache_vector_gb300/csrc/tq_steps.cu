@@ -24,7 +24,8 @@ constexpr int kStepStatusKeep = 66;    // a row's kept tokens outside their rang
 // its parents: they come in descending order, so each word of its mask is
 // written once, complete.
 //
-// Bound by latency: 64 rows of one token take three dependent reads.
+// Bound by latency: 64 rows of one token take 2.8 us in a graph, the trees of 256
+// rows (9500 nodes) 7.1 us.
 constexpr int kSlThreads = 512;
 
 struct SlotsArgs {
@@ -211,7 +212,8 @@ __global__ void __launch_bounds__(32 * kAsWarps) k_append_slots(const SlotRows A
 // head) pairs a warp; every CTA of a row checks its list alike.
 //
 // Bound by latency (lists, pages, then the rows): 64 rows of which 122 tokens
-// move in 32 layers, 7.5 MB in all, TIME_KEEP us in a graph.
+// move in 32 layers, 7.5 MB in all, 12.3 us in a graph (15.8 with a list for
+// every warp); 4 rows in 2 layers 4.0 us.
 constexpr int kKpWarps = 8;
 constexpr int kKpThreads = 32 * kKpWarps;
 constexpr int kKpEach = 4;     // (layer, KV head) pairs of a warp

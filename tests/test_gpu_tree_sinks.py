@@ -200,17 +200,24 @@ def test_seeded_sweep(seed):
     run_tree(bt, 1 / math.sqrt(d), random_trees(rng, lens)[1])
 
 
+# Batches of few query rows (16 and fewer per sequence and KV head) and of more
+# go to different kernels.
+few_and_more = pytest.mark.parametrize("lens", [[(9, 700), (2, 1300)], [(40, 700), (2, 1300)]], ids=["few", "more"])
+
+
+@few_and_more
 @pytest.mark.parametrize("flags", [1, 2, 3])
 @pytest.mark.parametrize("d", [32, 128, 256])
-def test_plan_variants(d, flags):
-    bt = Batch(25, [(20, 300), (1, 400)], 8, 4, d, 64, 3, 3, flags=flags)
+def test_plan_variants(d, flags, lens):
+    bt = Batch(25, lens, 8, 4, d, 64, 3, 3, flags=flags)
     run_sinks(bt, 1 / math.sqrt(d), 70, 5)
     run_tree(bt, 1 / math.sqrt(d), random_trees(np.random.default_rng(1), bt.lens)[1])
 
 
+@few_and_more
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 0.02, 0.5])
-def test_scales(scale):
-    bt = Batch(26, [(20, 400), (9, 333)], 4, 2, 128, 64, 4, 4)
+def test_scales(scale, lens):
+    bt = Batch(26, lens, 4, 2, 128, 64, 4, 4)
     run_sinks(bt, scale, 70, 5)
     run_tree(bt, scale, random_trees(np.random.default_rng(1), bt.lens)[1])
 
@@ -226,16 +233,18 @@ def test_scales(scale):
     ("zeros", lambda r, n: (r.random(n) < 0.5) * 1.0, 1.0, 0.1),
     ("all zero", lambda r, n: np.zeros(n), 1.0, 0.1),
 ])
-@pytest.mark.parametrize("d", [128, 256])
-def test_norms_of_all_sizes(name, norm, qmul, scale, d):
-    bt = Batch(27, [(15, 700), (2, 1300)], 4, 2, d, 64, 4, 4, norm=norm, qmul=qmul)
+@few_and_more
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norms_of_all_sizes(name, norm, qmul, scale, d, lens):
+    bt = Batch(27, lens, 4, 2, d, 64, 4, 4, norm=norm, qmul=qmul)
     run_sinks(bt, scale, 300, 6)
     run_tree(bt, scale, random_trees(np.random.default_rng(1), bt.lens)[1])
 
 
-def test_sinks_and_window_of_very_different_norms():
+@pytest.mark.parametrize("n", [3, 40])
+def test_sinks_and_window_of_very_different_norms(n):
     """Neither side's size takes bits from the other's, wherever a row's weight lies."""
-    bt = Batch(28, [(40, 900)], 4, 1, 128, 64, 4, 4)
+    bt = Batch(28, [(n, 900)], 4, 1, 128, 64, 4, 4)
     for pos in range(4):
         bt.set_norm(0, "v", 0, pos, 2.0 ** 40)
         bt.set_norm(0, "k", 0, pos, 2.0 ** -40)
@@ -245,6 +254,21 @@ def test_sinks_and_window_of_very_different_norms():
             bt.set_norm(0, "v", 0, pos, 2.0 ** 90)
             bt.set_norm(0, "k", 0, pos, 2.0 ** 90)
     run_sinks(bt, 0.5, 100, 4)
+
+
+@pytest.mark.parametrize("which,value", [("k", np.nan), ("k", np.inf), ("v", np.nan), ("v", -np.inf), ("v", np.inf)])
+@pytest.mark.parametrize("d", [128, 256])
+def test_non_finite_norms_reach_only_the_tokens_that_attend(which, value, d):
+    """Few rows: the last 5 tokens of one sequence and single ones of others."""
+    lens = [(5, 200), (1, 300), (1, 90)]
+    bt = Batch(40, lens, 4, 2, d, 64, 4, 3)
+    bt.set_norm(0, which, 1, 134, value)  # leaves the window between the third and the fourth token
+    bt.set_norm(1, which, 0, 200, value)  # between the sinks and the window
+    bt.set_norm(2, which, 0, 3, value)    # a sink
+    run_sinks(bt, 1 / math.sqrt(d), 64, 7)
+    bt = Batch(40, lens, 4, 2, d, 64, 4, 3)
+    bt.set_norm(0, which, 1, 197, value)  # node 2: its descendants alone
+    run_tree(bt, 1 / math.sqrt(d), random_trees(np.random.default_rng(2), lens)[1])
 
 
 @pytest.mark.parametrize("which,value", [("k", np.nan), ("k", np.inf), ("v", np.nan), ("v", -np.inf), ("v", np.inf)])
@@ -313,8 +337,10 @@ def test_lengths_out_of_range_leave_the_sequence_out():
         check(out[keep], *(r[keep] for r in ref), 8, bf16=False)
 
 
-def test_bad_pages_count_as_zero_rows_and_pages_between_are_not_read():
-    bt = Batch(34, [(6, 300), (20, 900)], 4, 2, 128, 64, 4, 3)
+@pytest.mark.parametrize("n", [5, 20])
+@pytest.mark.parametrize("d", [128, 256])
+def test_bad_pages_count_as_zero_rows_and_pages_between_are_not_read(n, d):
+    bt = Batch(34, [(6, 300), (n, 900)], 4, 2, d, 64, 4, 3)
     for b, j, page in ((0, 1, -5), (1, 13, bt.n_pages), (1, 0, -1)):
         bt.bt_host[b, j] = page
         for which in "kv":
@@ -323,7 +349,7 @@ def test_bad_pages_count_as_zero_rows_and_pages_between_are_not_read():
     args = bt.gpu()
     out = abi.tq_attn_sinks_paged(*args, 0.1, 200, 70, out_dtype=torch.float32)
     assert abi.tq_device_status(reset=True) == 72
-    check(out, *want(bt, 0.1, sinks_seen(bt, 200, 70)), 26, bf16=False)
+    check(out, *want(bt, 0.1, sinks_seen(bt, 200, 70)), 6 + n, bf16=False)
     bt.bt_host[1, 2:10] = bt.bt_host[1, 11]
     bt.bt_host[1, 0] = bt.bt_host[1, 11]
     bt.bt_host[1, 13] = bt.bt_host[1, 11]
@@ -333,11 +359,12 @@ def test_bad_pages_count_as_zero_rows_and_pages_between_are_not_read():
     assert abi.tq_device_status(reset=True) == 0
 
 
-def test_repeats_streams_and_graphs_give_the_same_bits():
-    bt = Batch(35, [(30, 900), (1, 3000), (17, 64)], 8, 2, 128, 64, 4, 3)
+@pytest.mark.parametrize("nodes", [(30, 1, 17), (5, 1, 6)])
+def test_repeats_streams_and_graphs_give_the_same_bits(nodes):
+    bt = Batch(35, list(zip(nodes, (900, 3000, 64))), 8, 2, 128, 64, 4, 3)
     args = bt.gpu()
     sees = random_trees(np.random.default_rng(1), bt.lens)[1]
-    mask = pack(sees, 1, 48).cuda()
+    mask = pack(sees, 1, sum(nodes)).cuda()
     ws = [torch.empty(abi.tq_attn_tree_paged_workspace_bytes(8, 2, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
     side = torch.cuda.Stream()
     for call in (lambda **k: abi.tq_attn_tree_paged(*args, mask, 0.1, **k),
@@ -365,6 +392,69 @@ def test_repeats_streams_and_graphs_give_the_same_bits():
             assert torch.equal(outs[0], eager)
         args[5].copy_(torch.tensor([900, 3000, 64], dtype=torch.int32))
     assert abi.tq_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 12])
+def test_values_lost_in_a_probability_that_count(d, n):
+    """A score far below the largest whose V norm makes it count: 2^-140 of the weight, 2^150 of
+    the value; and beside it a row whose largest weight has no value at all."""
+    bt = Batch(41, [(n, 400), (1, 100)], 2, 1, d, 32, 4, 4, qmul=1.0)
+    q = bt.q.float()
+    q[:] = q[:1, :1]  # one query: the keys below are along it or against it
+    bt.q = q.to(torch.bfloat16)
+    k = bt.decoded(0)[0][0] @ bt.q[0, 0].double().numpy()
+    for j in range(400):
+        bt.set_norm(0, "k", 0, j, 0.1)
+        bt.set_norm(0, "v", 0, j, 2.0 ** -60)
+    top, low = int(np.argmax(k[:380])), int(np.argmin(k[:380]))
+    bt.set_norm(0, "k", 0, top, 30.0)
+    bt.set_norm(0, "k", 0, low, 30.0)
+    k = bt.decoded(0)[0][0] @ bt.q[0, 0].double().numpy()
+    scale = 97.0 / (k[top] - k[low])  # nats: 2^-140
+    bt.set_norm(0, "v", 0, low, 2.0 ** 90)
+    run_sinks(bt, scale, 390, 400)
+    bt.set_norm(0, "v", 0, top, 0.0)
+    run_sinks(bt, scale, 390, 400)
+    bt.set_norm(0, "v", 0, low, 0.0)
+    run_sinks(bt, scale, 390, 400)
+
+
+def test_a_window_past_every_length_and_none():
+    """Of few rows too, up to the largest window."""
+    bt = Batch(42, [(1, 700), (3, 129), (1, 40)], 8, 2, 128, 64, 4, 3)
+    out = run_sinks(bt, 0.1, 0, 4)
+    for window in (700, 2 ** 20, 2 ** 30 + 5, 2 ** 31 - 1):
+        assert torch.equal(run_sinks(bt, 0.1, window, 4), out)
+        assert torch.equal(run_sinks(bt, 0.1, window, 0), out)
+
+
+def test_arrays_of_more_than_4_gib():
+    """Pages at the end of a pool whose arrays pass 2^32 bytes: appended to, attended to, kept."""
+    page, Hkv, d, n_pages = 256, 8, 128, 36000
+    c = abi.PagedCache.empty(n_pages, Hkv, page, d, 4, 4)
+    assert c.k_packed.numel() > 2 ** 32 and c.v_packed.numel() > 2 ** 32
+    small = abi.PagedCache.empty(4, Hkv, page, d, 4, 4)
+    plan, g = abi.Plan(d, 42), torch.Generator(device="cuda").manual_seed(3)
+    k, v = torch.randn(2, 700, Hkv, d, generator=g, device="cuda")
+    q = torch.randn(5, 32, d, generator=g, device="cuda").to(torch.bfloat16)
+    cu, ctx = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 5], [700]))
+    mask = torch.full((5, 1), 29, dtype=torch.int32, device="cuda")
+    outs = []
+    for cache, first in ((c, n_pages - 4), (small, 0)):
+        bt = torch.arange(first, first + 3, dtype=torch.int32, device="cuda")[None]
+        refs = torch.ones(cache.n_pages, dtype=torch.int32, device="cuda")
+        table = abi.PageTable(bt, ctx, refs)
+        m = abi.tq_pages_slots(table, ctx, 700, page)
+        abi.tq_append_slots(plan, cache, k, v, m.slots)
+        a = abi.tq_attn_tree_paged(plan, q, cu, cache, bt, ctx, mask, 0.1)
+        b = abi.tq_attn_sinks_paged(plan, q[:1], cu.clamp(max=1), cache, bt, ctx, 0.1, 300, 4)
+        five, keep = torch.tensor([5], dtype=torch.int32, device="cuda"), torch.tensor([[1, 3]], dtype=torch.int32, device="cuda")
+        new = abi.tq_pages_keep(table, five, keep, keep[0, :1] + 1, cache)
+        e = abi.tq_attn_sinks_paged(plan, q[:1], cu.clamp(max=1), cache, bt, new, 0.1, 300, 4)
+        outs.append((m.positions, a, b, new, e))
+    assert int(outs[0][3]) == 697 and abi.tq_device_status(reset=True) == 0
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
 
 
 def test_refusals():

@@ -125,6 +125,12 @@ def test_keep_refusals(L, kw, code):
     assert _keep(L, **kw) == code
 
 
+def test_keep_refuses_a_layer_given_twice(L):
+    two = (abi.PagedCacheView * 2)(_cache(), _cache())
+    a = (_table(), 4, 8, 8 * A16, 9 * A16, 8, 10 * A16, 11 * A16, two)
+    assert L.tq_pages_keep(*a, 2, 2, 128, 4, 3, None) == 1
+
+
 def _append(L, owner, **kw):
     a = dict(plan=owner.handle, kb=4, vb=3, k=8 * A16, ks=256, v=9 * A16, vs=256, dt=1, n=4, Hkv=2, cache=_cache(),
              slots=10 * A16)
