@@ -8,7 +8,6 @@ kernels.  There is no fallback: if ``libtq.so`` is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from contextlib import nullcontext
 from dataclasses import dataclass
@@ -657,10 +656,11 @@ _INT32 = torch.int32
 
 def _ints(device, *ts):
     """Contiguous int32 CUDA tensors on `device`."""
+    at = device.index
     for t in ts:
         if t.dtype is not _INT32:
             raise TypeError("expected int32 tensors")
-        if t.device != device or not t.is_contiguous():
+        if t.get_device() != at or not t.is_contiguous():
             raise ValueError("expected contiguous CUDA tensors on one device")
 
 
@@ -670,8 +670,9 @@ def _raw_stream(device):
 
 
 def _same_device(device, *ts):
+    at = device.index
     for t in ts:
-        if t.device != device:
+        if t.get_device() != at:
             raise ValueError("all tensors must be on one device")
 
 
@@ -680,7 +681,7 @@ _STAY = nullcontext()
 
 def _on(device):
     """The device made current for a call, where it is not."""
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else _STAY
+    return torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else _STAY
 
 
 def _layers(x) -> PagedLayers:
@@ -728,20 +729,19 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
             _raw_stream(dst.device)))
 
 
-_FRESH: dict = {}  # per device, stream, length and type: tensors that no call has had yet
+_FRESH: dict = {}  # per device, stream and length: int32 tensors that no call has had yet
 
 
-def _fresh(device, stream, n, dtype=_INT32):
-    """A new tensor [n] (a shape of more too), several to an allocation (one costs
-    more than half of a small call); in a capture one of the graph's own memory."""
+def _fresh(device, stream, n):
+    """A new int32 tensor [n], several to an allocation (one costs more than half
+    of a small call); in a capture one of the graph's own memory."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=dtype, device=device)
-    key = (device.index, stream, n, dtype)
+        return torch.empty(n, dtype=_INT32, device=device)
+    key = (device.index, stream, n)
     try:
         return _FRESH[key].pop()
     except (KeyError, IndexError):  # none left, maybe since another thread took the last
-        shape = n if isinstance(n, tuple) else (n,)
-        new = list(torch.empty(max(1, min(64, 65536 // max(1, math.prod(shape)))), *shape, dtype=dtype, device=device).unbind())
+        new = list(torch.empty(max(1, min(64, 65536 // max(1, n))), n, dtype=_INT32, device=device).unbind())
         first = new.pop()
         _FRESH[key] = new
         return first
@@ -824,39 +824,65 @@ def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_s
     parents [n_tokens] int32 (the number within its row of the node that a node
     follows, -1: none) also the trees' masks of mask_words words, and positions by
     depth.  All on the device."""
-    bt, dev = table.block_table, table.block_table.device
-    if bt.dim() != 2 or table.lens.numel() != bt.shape[0] or counts.numel() != bt.shape[0]:
-        raise ValueError("block_table [n_seqs, max_pages], lens and counts [n_seqs] expected")
+    bt, lens = table.block_table, table.lens
     if not bt.is_cuda:
         raise ValueError("expected CUDA tensors")
-    _ints(dev, bt, table.lens, counts)
-    if parents is not None:
-        _ints(dev, parents)
-        if parents.numel() != n_tokens or mask_words < 1:
-            raise ValueError("parents has one entry per token and its masks at least one word")
-    n_seqs, max_pages = bt.shape
+    dev, shape = bt.device, bt.shape
+    if len(shape) != 2 or lens.numel() != shape[0] or counts.numel() != shape[0]:
+        raise ValueError("block_table [n_seqs, max_pages], lens and counts [n_seqs] expected")
+    n_seqs, max_pages = shape
+    tree = parents is not None
+    _ints(dev, bt, lens, counts, *((parents,) if tree else ()))
+    if tree and (parents.numel() != n_tokens or mask_words < 1):
+        raise ValueError("parents has one entry per token and its masks at least one word")
     with _on(dev):
         stream = _raw_stream(dev)
         if out is None:
-            out = TokenSlots(_fresh(dev, stream, n_seqs + 1), _fresh(dev, stream, n_tokens),
-                             _fresh(dev, stream, n_tokens, torch.int64),
-                             None if parents is None else _fresh(dev, stream, (n_tokens, mask_words)))
+            out = _step(dev, stream, n_seqs, n_tokens, mask_words if tree else 0)
         else:
             _ints(dev, out.cu_q, out.positions)
             if out.slots.dtype != torch.int64 or out.slots.device != dev or not out.slots.is_contiguous():
                 raise ValueError("slots must be a contiguous int64 tensor on the table's device")
             if out.cu_q.numel() != n_seqs + 1 or out.positions.numel() != n_tokens or out.slots.numel() != n_tokens:
                 raise ValueError("cu_q [n_seqs + 1], positions and slots [n_tokens] expected")
-            if parents is not None:
+            if tree:
                 if out.mask is None or out.mask.shape != (n_tokens, mask_words):
                     raise ValueError("mask must be [n_tokens, mask_words]")
                 _ints(dev, out.mask)
         _check("tq_pages_slots", lib().tq_pages_slots(
-            PageTableView(bt.data_ptr(), table.lens.data_ptr(), None), n_seqs, max_pages, table.refs.numel(), page_size,
-            counts.data_ptr(), None if parents is None else parents.data_ptr(), mask_words, n_tokens,
-            out.cu_q.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-            None if parents is None else out.mask.data_ptr(), stream))
+            PageTableView(bt.data_ptr(), lens.data_ptr(), None), n_seqs, max_pages, table.refs.numel(), page_size,
+            counts.data_ptr(), parents.data_ptr() if tree else None, mask_words, n_tokens, out.cu_q.data_ptr(),
+            out.positions.data_ptr(), out.slots.data_ptr(), out.mask.data_ptr() if tree else None, stream))
     return out
+
+
+_STEPS: dict = {}  # per device and stream: the last step's sizes, and TokenSlots of them that no call has had yet
+
+
+def _step(device, stream, n_seqs, n_tokens, words):
+    """New TokenSlots.  Where a step has the sizes of the one before it, several to
+    an allocation (as _fresh; other sizes give up what is left, so that steps of
+    many sizes hold no memory)."""
+    def empty(*lead):
+        return [torch.empty(*lead, n, dtype=t, device=device) for n, t in
+                ((n_seqs + 1, _INT32), (n_tokens, _INT32), (n_tokens, torch.int64))] + \
+            ([torch.empty(*lead, n_tokens, words, dtype=_INT32, device=device)] if words else [])
+
+    size = 4 * (n_seqs + 1 + n_tokens * (3 + words))
+    if size > 65536 or torch._C._cuda_isCurrentStreamCapturing():  # (1 MB at most is held)
+        return TokenSlots(*empty())
+    key = (n_seqs, n_tokens, words)
+    last, left = _STEPS.get((device.index, stream), (None, None))
+    if last != key:
+        _STEPS[device.index, stream] = key, []
+        return TokenSlots(*empty())
+    try:
+        return TokenSlots(*left.pop())
+    except IndexError:
+        new = list(zip(*(t.unbind() for t in empty(16))))
+        first = new.pop()
+        _STEPS[device.index, stream] = key, new
+        return TokenSlots(*first)
 
 
 def tq_append_slots(plan: Plan, cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor):
@@ -887,23 +913,25 @@ def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_
     (int32, ascending) stay: their rows move to the front of the counts[b] in
     every layer.  Returns the new lengths [n_seqs], for tq_pages_resize."""
     layers = _layers(layers)
-    dev = layers.device
-    bt = table.block_table
-    if bt.dim() != 2 or keep.dim() != 2 or keep.shape[0] != bt.shape[0] or counts.numel() != bt.shape[0] or \
-            n_keep.numel() != bt.shape[0]:
+    dev, shape, lists = layers.device, table.block_table.shape, keep.shape
+    if len(shape) != 2:
+        raise ValueError("block_table must be [n_seqs, max_pages]")
+    n_seqs, max_pages = shape
+    if len(lists) != 2 or lists[0] != n_seqs or counts.numel() != n_seqs or n_keep.numel() != n_seqs:
         raise ValueError("keep [n_seqs, max_keep], counts and n_keep [n_seqs] expected")
     _ints(dev, counts, keep, n_keep)
     with _on(dev):
-        view = table._view(layers, bt.shape)
+        view = table._view(layers, shape)
         stream = _raw_stream(dev)
         if out is None:
-            out = _fresh(dev, stream, bt.shape[0])
-        _ints(dev, out)
-        if out.numel() != bt.shape[0]:
-            raise ValueError("one new length per row")
+            out = _fresh(dev, stream, n_seqs)
+        else:
+            _ints(dev, out)
+            if out.numel() != n_seqs:
+                raise ValueError("one new length per row")
         _check("tq_pages_keep", lib().tq_pages_keep(
-            view, bt.shape[0], bt.shape[1], counts.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr(),
-            out.data_ptr(), layers.views, len(layers.views), *layers.args, stream))
+            view, n_seqs, max_pages, counts.data_ptr(), keep.data_ptr(), lists[1], n_keep.data_ptr(), out.data_ptr(),
+            layers.views, len(layers.views), *layers.args, stream))
     return out
 
 

@@ -267,6 +267,10 @@ cudaError_t dispatch_attn_d(int d, F&& f) {
     return cudaErrorInvalidValue;
 }
 
+// The scale s under which the levels are kept in fp16: the plan's where it has
+// one (then every c * s is close to an fp16 value).
+double level_scale(const tq::Plan& P, int bits) { return P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0; }
+
 // QJL residual keys: head dimensions whose matrix fits in shared memory.
 bool qjl_d(int d) { return d == 32 || d == 64 || d == 128; }
 
@@ -418,6 +422,13 @@ tq_status tq_plan_create_ex(int d, uint64_t seed, uint32_t flags, tq_plan** out)
             return TQ_ERR_UNSUPPORTED;
         }
         if (bits >= 2 && d == 128) half_scale(P->c32[bits], L, &P->hscale[bits], P->hcen[bits]);
+        for (int i = 0; i < L; ++i)
+            P->hlev[bits][i] = __half_as_ushort(__float2half_rn((float)((double)P->c32[bits][i] * level_scale(*P, bits))));
+    }
+    for (int i = 0; i < d; ++i) {
+        P->sgnb[i >> 5] |= (P->signs[i] < 0 ? 1u : 0u) << (i & 31);
+        P->sgn2b[i >> 5] |= (P->signs2[i] < 0 ? 1u : 0u) << (i & 31);
+        P->sgnh[i >> 1] |= (P->signs[i] < 0 ? 0x8000u : 0u) << (16 * (i & 1));
     }
     *out = reinterpret_cast<tq_plan*>(P);
     return TQ_OK;
@@ -1238,22 +1249,12 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d) {
 }
 
 namespace {
-// The scale s under which the levels are kept in fp16: the plan's where it has
-// one (then every c * s is close to an fp16 value).
-double level_scale(const tq::Plan& P, int bits) { return P.hscale[bits] > 0.0f ? P.hscale[bits] : 1.0; }
-
-// Level c * s as fp16 (0 past the last).
-uint16_t level_half(const tq::Plan& P, int bits, int i) {
-    return i < 1 << bits ? __half_as_ushort(__float2half_rn((float)((double)P.c32[bits][i] * level_scale(P, bits)))) : 0;
-}
-
 // The levels c * s as fp16 bytes for the byte-permute lookups.
 void level_bytes(const tq::Plan& P, int bits, uint32_t* w) {
-    const double s = level_scale(P, bits);
     const int first = bits == 4 ? 8 : 0, n = bits == 2 ? 4 : 8;
     for (int i = 0; i < 8; ++i) w[i] = 0u;
     for (int i = 0; i < n; ++i) {
-        const uint32_t h = __half_as_ushort(__float2half_rn((float)((double)P.c32[bits][first + i] * s)));
+        const uint32_t h = P.hlev[bits][first + i];
         w[i >> 2] |= (h >> 8) << (8 * (i & 3));
         w[4 + (i >> 2)] |= (h & 0xFFu) << (8 * (i & 3));
     }
@@ -1308,11 +1309,9 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
         !paged_accessible(cache) || (tree && !device_accessible(seen.mask)))
         return TQ_ERR_INVALID_ARG;
     tq::PagedPrefillCall c = {};
-    for (int i = 0; i < P->d; ++i) {
-        c.consts.sgnb[i >> 5] |= (P->signs[i] < 0 ? 1u : 0u) << (i & 31);
-        c.consts.sgn2b[i >> 5] |= (P->signs2[i] < 0 ? 1u : 0u) << (i & 31);
-        c.consts.sgnh[i >> 1] |= (P->signs[i] < 0 ? 0x8000u : 0u) << (16 * (i & 1));
-    }
+    std::memcpy(c.consts.sgnb, P->sgnb, sizeof(P->sgnb));
+    std::memcpy(c.consts.sgn2b, P->sgn2b, sizeof(P->sgn2b));
+    std::memcpy(c.consts.sgnh, P->sgnh, sizeof(P->sgnh));
     const double sd = std::sqrt((double)P->d);
     c.consts.two_sided = (P->flags & TQ_PLAN_TWO_SIDED_SIGNS) ? 1 : 0;
     c.consts.q_mul = (float)((double)scale * 1.4426950408889634 / (sd * level_scale(*P, k_bits)));
@@ -1350,10 +1349,8 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
     c.out_bf16 = out_dtype == TQ_BF16;
     level_bytes(*P, k_bits, c.k_levels);
     level_bytes(*P, v_bits, c.v_levels);
-    for (int i = 0; i < 16; ++i) {
-        c.k_cen[i] = level_half(*P, k_bits, i);
-        c.v_cen[i] = level_half(*P, v_bits, i);
-    }
+    std::memcpy(c.k_cen, P->hlev[k_bits], sizeof(c.k_cen));
+    std::memcpy(c.v_cen, P->hlev[v_bits], sizeof(c.v_cen));
     const cudaError_t e = dispatch_attn_d(P->d, [&](auto D) {
         constexpr int d = decltype(D)::value;
         auto st = reinterpret_cast<cudaStream_t>(stream);

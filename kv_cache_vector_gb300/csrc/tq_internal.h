@@ -77,6 +77,10 @@ struct Plan {
     // value, and those fp16 values (the fp16 tensor-core attention).
     float hscale[5];
     float hcen[5][16];
+    // what the multi-token paged attention passes at every call: the levels c * s as
+    // fp16 (0 past the last), and the signs as in PagedPrefillConsts
+    uint16_t hlev[5][16];
+    uint32_t sgnb[kMaxD / 32], sgn2b[kMaxD / 32], sgnh[kMaxD / 2];
 };
 
 void fill_attn_params(const Plan& P, int k_bits, int v_bits, float scale, float sparse_thr,

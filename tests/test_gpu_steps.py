@@ -107,6 +107,23 @@ def test_slots_out_of_range(change, status):
     same_slots(m, steps.slots(table, lens, counts, 32, 6, T, parents, 1), status)
 
 
+def test_results_of_steps_are_their_own():
+    """Steps of the sizes of the one before, of others and of no tokens."""
+    rng = np.random.default_rng(8)
+    made = []
+    for n, new, words in [(5, 6, 0)] * 40 + [(5, 6, 1), (9, 6, 0), (9, 6, 1), (9, 6, 1), (5, 6, 1)] * 8 + [(5, 0, 0), (5, 0, 1)] * 3:
+        table, lens, refs, counts = books(rng, n, new, 200, 32)
+        T = n * new
+        parents = [-1] * T if words else None
+        m = abi.tq_pages_slots(gpu_table(table, lens, refs), t32(counts), T, 32,
+                               parents=t32(parents) if words else None, mask_words=max(1, words))
+        made.append((m, steps.slots(table, lens, counts, 32, len(refs), T, parents, words)))
+    for m, ref in made:
+        same_slots(m, ref, 0)
+    at = [t.data_ptr() for m, _ in made for t in (m.cu_q, m.positions, m.slots, m.mask) if t is not None and t.numel()]
+    assert len(set(at)) == len(at)
+
+
 def test_slots_into_given_tensors_and_graphs():
     rng = np.random.default_rng(8)
     table, lens, refs, counts = books(rng, 30, 6, 200, 32)
