@@ -710,8 +710,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                 const unsigned char* stg = sm + Z::kStg + st * Z::kStage;
                 const float* fac = reinterpret_cast<const float*>(stg + N * D);
                 const uint32_t slk = (2 * tc) & 3, slv = (2 * tc + 1) & 3;
-                ok = pp_wait(&stage_full[st], (tc / NS) & 1, abort_f, status) &&
-                     pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status) &&
+                // (whoever wrote the factors has seen the rows land)
+                ok = pp_wait(&meta_full[tc & 7], (tc >> 3) & 1, abort_f, status) &&
                      (tc < 2 || pp_wait(&kv_free[slk], ((tc >> 1) - 1) & 1, abort_f, status));
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
@@ -898,20 +898,8 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                     // read the slot at different times
                     const bool wide = __any_sync(0xFFFFFFFFu, meta.x == 0.f);
                     if (kWide != wide) break;
-                    pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
-                    ++ns[buf];
-                    __syncwarp();
-                    lastb = buf;
-                    if (!rows_here) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (kWide && lane <= (split ? 1 : 0)) mbar_arrive(cols_free);
-                        if (lane == 0) mbar_arrive(&p_full[buf]);
-                        ++npv[buf];
-                        continue;
-                    }
-                    tc_fence_after();
-                    const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
+                    // what the step sees, ahead of its scores (behind the wait it cost 260 to 530
+                    // cycles of a step's 4400)
                     const int t0 = pp_block_at<Z, MODE>(A, p.kv_lo, p.kv_end, p.blk + j) * N;
                     PpVis<MODE> vis;  // the columns of the block that are this row's
                     bool all = true;
@@ -930,6 +918,20 @@ k_prefill_paged(const __grid_constant__ PpArgs A, const __grid_constant__ PagedP
                         all = vis.c1 == N && vis.c0 == 0;
                     }
                     const bool full = __all_sync(0xFFFFFFFFu, !rvalid || all);
+                    pp_wait(&s_full[buf], ns[buf] & 1, abort_f, status);
+                    ++ns[buf];
+                    __syncwarp();
+                    lastb = buf;
+                    if (!rows_here) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (kWide && lane <= (split ? 1 : 0)) mbar_arrive(cols_free);
+                        if (lane == 0) mbar_arrive(&p_full[buf]);
+                        ++npv[buf];
+                        continue;
+                    }
+                    tc_fence_after();
+                    const uint32_t t_s = t_lane + Z::kTmemS + N * buf;
                     // not 0, which a masked score of -inf would make NaN: tiny queries over tiny norms
                     float cs = fmaxf(cq * meta.x, FLT_MIN), ev = meta.y;
                     float2 w2;  // a wide block's
