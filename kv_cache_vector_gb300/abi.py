@@ -868,8 +868,8 @@ def _step(device, stream, n_seqs, n_tokens, words):
                 ((n_seqs + 1, _INT32), (n_tokens, _INT32), (n_tokens, torch.int64))] + \
             ([torch.empty(*lead, n_tokens, words, dtype=_INT32, device=device)] if words else [])
 
-    size = 4 * (n_seqs + 1 + n_tokens * (3 + words))
-    if size > 65536 or torch._C._cuda_isCurrentStreamCapturing():  # (1 MB at most is held)
+    several = min(16, 2 ** 20 // (4 * (n_seqs + 1 + n_tokens * (3 + words))))  # (1 MB at most is held)
+    if several < 2 or torch._C._cuda_isCurrentStreamCapturing():
         return TokenSlots(*empty())
     key = (n_seqs, n_tokens, words)
     last, left = _STEPS.get((device.index, stream), (None, None))
@@ -879,7 +879,7 @@ def _step(device, stream, n_seqs, n_tokens, words):
     try:
         return TokenSlots(*left.pop())
     except IndexError:
-        new = list(zip(*(t.unbind() for t in empty(16))))
+        new = list(zip(*(t.unbind() for t in empty(several))))
         first = new.pop()
         _STEPS[device.index, stream] = key, new
         return TokenSlots(*first)

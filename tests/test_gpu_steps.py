@@ -111,7 +111,7 @@ def test_results_of_steps_are_their_own():
     """Steps of the sizes of the one before, of others and of no tokens."""
     rng = np.random.default_rng(8)
     made = []
-    for n, new, words in [(5, 6, 0)] * 40 + [(5, 6, 1), (9, 6, 0), (9, 6, 1), (9, 6, 1), (5, 6, 1)] * 8 + [(5, 0, 0), (5, 0, 1)] * 3:
+    for n, new, words in [(5, 6, 0)] * 40 + [(5, 6, 1), (9, 6, 0), (9, 6, 1), (9, 6, 1), (5, 6, 1)] * 8 + [(5, 0, 0), (5, 0, 1)] * 3 + [(100, 100, 4)] * 6:
         table, lens, refs, counts = books(rng, n, new, 200, 32)
         T = n * new
         parents = [-1] * T if words else None
