@@ -72,6 +72,7 @@ struct FwGeo {
     static constexpr int kRows = 8 * NT;  // query rows of an item
     static constexpr int kStreams = 1;
     static constexpr int kCostPair = 1, kCostSplit = 1, kCostItem = 4;  // of a block and an item (pp_start)
+    static constexpr bool kWhole = true;  // shares may be items
     // registers: the output takes D / 4 NT, the queries D / 8 NT
         static constexpr int kWarps = D * NT >= 256 ? 8 : 12;
     static constexpr int kThreads = 32 * kWarps;
@@ -802,8 +803,23 @@ template <int D, int NT, int MODE>
 static cudaError_t launch_few(const PagedPrefillCall& c, cudaStream_t s) {
     using Z = FwGeo<D, NT>;
     static_assert(Z::kRows <= PagedPrefillGeo<D>::kRows, "the workspace holds the parts");
-    const int shares = num_sms();
-    const PpArgs A = pp_args(c, shares, (size_t)(D + 3) * Z::kRows);
+    const int shares = num_sms(), G = c.Hq / c.Hkv;
+    PpArgs A = pp_args(c, shares, (size_t)(D + 3) * Z::kRows);
+    // Few items of few blocks (a short window, a small table): one CTA takes all of an
+    // item, and no join follows.  By the most items and blocks that there can be, as the
+    // lengths are on the device.  4 sequences, 8 KV heads, windows of 256 (5 blocks), 512
+    // (7) and 768 (9), us in parts and whole: d = 128, 4 rows 13.9 12.2, 13.8 12.8 and 14.0
+    // 14.4, 16 rows 16.4 14.5, 16.4 16.6 and 16.7 18.4; d = 64 13.2 11.1, 13.2 11.5 and 13.2
+    // 12.8; d = 256 15.8 15.1, 16.2 17.1 and 16.7 19.5.  The host saves a launch.  (A cu_q that steps back can give more items than
+    // CTAs; with the sequences out of range some of the others are left out then.  Going on
+    // to them cost the short windows 1.1 us.)
+    const int64_t items = (c.n_q * G / Z::kRows + c.B) * c.Hkv;
+    int64_t blocks = ((int64_t)c.max_pages << c.page_shift) / Z::kN + 1;
+    if (MODE == kPpSinks && c.window > 0) {
+        const int64_t reach = ((int64_t)c.window + Z::kRows / G) / Z::kN + 2 + (c.sinks + Z::kN - 1) / Z::kN;
+        if (reach < blocks) blocks = reach;
+    }
+    A.whole = items <= shares && blocks <= (NT == 1 && D <= 128 ? 7 : 5);
     FwLevels L;
     for (int i = 0; i < 16; ++i) L.k[i] = c.k_cen[i], L.v[i] = c.v_cen[i];
     static int attr_done[64] = {};
@@ -815,9 +831,10 @@ static cudaError_t launch_few(const PagedPrefillCall& c, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
-    e = launch_pdl(k_attn_few<D, NT, MODE>, dim3(shares), dim3(Z::kThreads), Z::kEnd, s, A, c.consts, L, status_word());
+    e = launch_pdl(k_attn_few<D, NT, MODE>, dim3(A.whole ? (unsigned)items : shares), dim3(Z::kThreads), Z::kEnd, s, A, c.consts, L, status_word());
     if (e != cudaSuccess) return e;
-    const int64_t rows = c.n_q * (c.Hq / c.Hkv);
+    if (A.whole) return e;  // no parts to join
+    const int64_t rows = c.n_q * G;
     const unsigned groups = (unsigned)((rows < Z::kRows ? rows : Z::kRows) + 31) / 32;
     return launch_pdl(k_prefill_paged_join<D, D < 256 ? 4 : 2, Z::kRows>, dim3(shares, groups), dim3(256), 0, s, A,
                       c.consts);

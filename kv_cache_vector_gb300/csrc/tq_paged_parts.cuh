@@ -42,6 +42,7 @@ struct PpArgs {
     int sinks;             // kPpSinks
     const uint32_t* mask;  // kPpTree: [n_q][words]
     int words;
+    int whole;             // (kernel for few rows) a share is an item
     uint32_t khi[4], klo[4], vhi[4], vlo[4];  // level bytes (see expand)
 };
 // what a share left: bit 0 a part of the item it starts in, bit 1 one of the
@@ -276,120 +277,122 @@ __device__ __forceinline__ void pp_write_job(volatile PpJob* m, bool more, const
 template <class Z, int MODE>
 __device__ __forceinline__ void pp_start(const PpArgs& A, long long* red, PpCursor* start, long long* share, int* status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-            const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
-            const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
-            PpSeq<Z, MODE> q;
-            long long mine = 0;
-            int items = 0;
-            float most = 0.f;  // the largest item's work
-            for (int b = b0; b < b1; ++b) {
-                q.load(A, b, blockIdx.x == 0 ? status : nullptr);
-                mine += (long long)A.Hkv * q.before(q.tiles);
-                if (q.tiles) most = fmaxf(most, fmaxf((float)q.work(q.tiles - 1), (float)q.work(max(0, q.tiles - 2))));
-                items += (int)min((int64_t)1 << 10, (int64_t)A.Hkv * q.tiles);  // exact where it counts: below the CTAs
+    const int each = (A.B + Z::kThreads - 1) / Z::kThreads;
+    const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
+    PpSeq<Z, MODE> q;
+    long long mine = 0;
+    int items = 0;
+    float most = 0.f;  // the largest item's work
+    for (int b = b0; b < b1; ++b) {
+        q.load(A, b, blockIdx.x == 0 ? status : nullptr);
+        mine += (long long)A.Hkv * q.before(q.tiles);
+        if (q.tiles) most = fmaxf(most, fmaxf((float)q.work(q.tiles - 1), (float)q.work(max(0, q.tiles - 2))));
+        items += (int)min((int64_t)1 << 10, (int64_t)A.Hkv * q.tiles);  // exact where it counts: below the CTAs
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) red[warp] = incl;
+    uint32_t* red2 = reinterpret_cast<uint32_t*>(red + Z::kWarps);
+    const uint32_t wi = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)items);
+    const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+    if (lane == 0) red2[2 * warp] = wi, red2[2 * warp + 1] = wm;
+    __syncthreads();
+    long long total = 0, before = 0;
+    uint32_t all = 0, top = 0;
+#pragma unroll
+    for (int w = 0; w < Z::kWarps; ++w) {
+        if (w < warp) before += red[w];
+        total += red[w];
+        all += red2[2 * w];
+        top = max(top, red2[2 * w + 1]);
+    }
+    before += incl - mine;
+    const float sum = (float)total, grid = (float)gridDim.x;
+    // a little over total / grid: the last CTA's share may be smaller
+    const long long per = (long long)(sum * (1.000001f / grid)) + 1;
+    if (tid == 0) *share = per;
+    // Shares along the line of all items cross from one item into the next, and
+    // then pay for two items' rotations and outputs.  With few items a share is
+    // a part of one item instead: an item gets (work / cut) + 1 shares, no more
+    // than there are CTAs in all.  Taken where the largest of them is no more
+    // than a share of the line: the drafts of 4 sequences over 400-2000
+    // positions took 24.7 us along the line, 20.8 us so.
+    float cut = 0.f;
+    if (Z::kWhole && A.whole) {
+        cut = 1e30f;  // one part each
+    } else if (each == 1 && all > 0 && all < gridDim.x) {
+        const float over = (float)Z::kCostItem * Z::kN * (A.Hq / A.Hkv);
+        const float c = fmaxf(1.f, __fdividef((sum - (float)all * over) * 1.000002f, grid - (float)all));
+        if (fminf(c, __uint_as_float(top)) * grid <= sum) cut = c;
+    }
+    if (cut > 0.f) {
+        auto parts = [&](int i) { return (int)__fdividef((float)q.work(i), cut) + 1; };
+        int sums = 0;
+        for (int i = 0; i < q.tiles; ++i) sums += A.Hkv * parts(i);
+        int ins = sums;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, ins, o);
+            if (lane >= o) ins += u;
+        }
+        __syncthreads();  // red2 is free
+        if (lane == 31) red2[warp] = ins;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) ins += red2[w];
+        int v = (int)blockIdx.x - (ins - sums);
+        if (v >= 0 && v < sums) {  // this thread's sequence holds this CTA's share
+            int i = 0, n;
+            for (;; ++i) {
+                n = parts(i);
+                if (v < A.Hkv * n) break;
+                v -= A.Hkv * n;
             }
-            long long incl = mine;
-    #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += u;
+            start->b = b0;
+            start->i = i;
+            start->h = v / n;
+            start->off = v % n;
+            start->parts = n;
+            start->n = q.n;
+            start->ctx = q.ctx;
+            start->q0 = q.q0;
+        }
+        return;
+    }
+    const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+    if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
+        long long v = u0 - before;
+        int b = b0;
+        if (each > 1)
+            for (;; ++b) {
+                q.load(A, b, nullptr);
+                const long long w = (long long)A.Hkv * q.before(q.tiles);
+                if (v < w) break;
+                v -= w;
             }
-            if (lane == 31) red[warp] = incl;
-            uint32_t* red2 = reinterpret_cast<uint32_t*>(red + Z::kWarps);
-            const uint32_t wi = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)items);
-            const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-            if (lane == 0) red2[2 * warp] = wi, red2[2 * warp + 1] = wm;
-            __syncthreads();
-            long long total = 0, before = 0;
-            uint32_t all = 0, top = 0;
-    #pragma unroll
-            for (int w = 0; w < Z::kWarps; ++w) {
-                if (w < warp) before += red[w];
-                total += red[w];
-                all += red2[2 * w];
-                top = max(top, red2[2 * w + 1]);
-            }
-            before += incl - mine;
-            const float sum = (float)total, grid = (float)gridDim.x;
-            // a little over total / grid: the last CTA's share may be smaller
-            const long long per = (long long)(sum * (1.000001f / grid)) + 1;
-            if (tid == 0) *share = per;
-            // Shares along the line of all items cross from one item into the next, and
-            // then pay for two items' rotations and outputs.  With few items a share is
-            // a part of one item instead: an item gets (work / cut) + 1 shares, no more
-            // than there are CTAs in all.  Taken where the largest of them is no more
-            // than a share of the line: the drafts of 4 sequences over 400-2000
-            // positions took 24.7 us along the line, 20.8 us so.
-            float cut = 0.f;
-            if (each == 1 && all > 0 && all < gridDim.x) {
-                const float over = (float)Z::kCostItem * Z::kN * (A.Hq / A.Hkv);
-                const float c = fmaxf(1.f, __fdividef((sum - (float)all * over) * 1.000002f, grid - (float)all));
-                if (fminf(c, __uint_as_float(top)) * grid <= sum) cut = c;
-            }
-            if (cut > 0.f) {
-                auto parts = [&](int i) { return (int)__fdividef((float)q.work(i), cut) + 1; };
-                int sums = 0;
-                for (int i = 0; i < q.tiles; ++i) sums += A.Hkv * parts(i);
-                int ins = sums;
-    #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int u = __shfl_up_sync(0xFFFFFFFFu, ins, o);
-                    if (lane >= o) ins += u;
-                }
-                __syncthreads();  // red2 is free
-                if (lane == 31) red2[warp] = ins;
-                __syncthreads();
-                for (int w = 0; w < warp; ++w) ins += red2[w];
-                int v = (int)blockIdx.x - (ins - sums);
-                if (v >= 0 && v < sums) {  // this thread's sequence holds this CTA's share
-                    int i = 0, n;
-                    for (;; ++i) {
-                        n = parts(i);
-                        if (v < A.Hkv * n) break;
-                        v -= A.Hkv * n;
-                    }
-                    start->b = b0;
-                    start->i = i;
-                    start->h = v / n;
-                    start->off = v % n;
-                    start->parts = n;
-                    start->n = q.n;
-                    start->ctx = q.ctx;
-                    start->q0 = q.q0;
-                }
-            } else {
-            const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-            if (u0 < u1 && u0 >= before && u0 < before + mine) {  // this thread's sequences hold the start
-                long long v = u0 - before;
-                int b = b0;
-                if (each > 1)
-                    for (;; ++b) {
-                        q.load(A, b, nullptr);
-                        const long long w = (long long)A.Hkv * q.before(q.tiles);
-                        if (v < w) break;
-                        v -= w;
-                    }
-                int lo = 0, hi = q.tiles - 1;  // the last tile whose units start at or before v
-                while (lo < hi) {
-                    const int m = (lo + hi + 1) / 2;
-                    if ((long long)A.Hkv * q.before(m) <= v) lo = m;
-                    else hi = m - 1;
-                }
-                v -= (long long)A.Hkv * q.before(lo);
-                const long long w = q.weight(lo);
-                start->b = b;
-                start->i = lo;
-                int h = (int)((float)v / (float)w);  // v / w, to within one
-                h -= (long long)h * w > v;
-                h += (long long)(h + 1) * w <= v;
-                start->h = h;
-                start->off = v - (long long)h * w;
-                start->left = u1 - u0;
-                start->n = q.n;
-                start->ctx = q.ctx;
-                start->q0 = q.q0;
-            }
-            }
+        int lo = 0, hi = q.tiles - 1;  // the last tile whose units start at or before v
+        while (lo < hi) {
+            const int m = (lo + hi + 1) / 2;
+            if ((long long)A.Hkv * q.before(m) <= v) lo = m;
+            else hi = m - 1;
+        }
+        v -= (long long)A.Hkv * q.before(lo);
+        const long long w = q.weight(lo);
+        start->b = b;
+        start->i = lo;
+        int h = (int)((float)v / (float)w);  // v / w, to within one
+        h -= (long long)h * w > v;
+        h += (long long)(h + 1) * w <= v;
+        start->h = h;
+        start->off = v - (long long)h * w;
+        start->left = u1 - u0;
+        start->n = q.n;
+        start->ctx = q.ctx;
+        start->q0 = q.q0;
+    }
 }
 
 // Which parts this share left, and the item it owns: the one that starts in this

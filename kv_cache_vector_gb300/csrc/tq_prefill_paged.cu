@@ -104,6 +104,7 @@ struct PpGeo {
     // d = 256, 5 chunks with a window of 1024, 4 blocks 95 us and 5 blocks 98 us.
     static constexpr int kCostPair = kStreams == 2 ? 6 : 1, kCostSplit = kStreams == 2 ? 5 : 1;
     static constexpr int kCostItem = kStreams == 2 ? 5 * kCostPair : 4;
+    static constexpr bool kWhole = false;  // (pp_start)
     static constexpr int kSoftWarps = 4 * kStreams;
     static constexpr int kDeqWarps = 8;
     static constexpr int kWarps = kSoftWarps + kDeqWarps + 3;

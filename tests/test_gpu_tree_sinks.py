@@ -483,3 +483,36 @@ def test_refusals():
         abi.tq_attn_sinks_paged(*args, float("inf"), 16, 4)
     with pytest.raises(ValueError):
         abi.tq_attn_sinks_paged(*args, 0.1, 16, 4, out=torch.empty(3, 4, 128, device="cuda"))
+
+
+@pytest.mark.parametrize("d", [128, 64, 256, 32])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (130, 0), (250, 5), (200, 130), (256, 0)])
+@pytest.mark.parametrize("lens,Hq,Hkv", [
+    ([(1, 700)], 4, 1), ([(1, 3000), (1, 1), (1, 0), (1, 129), (0, 50)], 32, 8), ([(4, 900), (1, 256), (3, 3)], 32, 8),
+    ([(1, 300 + 60 * i) for i in range(19)], 8, 8)])
+def test_short_windows_of_few_rows(lens, Hq, Hkv, window, sinks, d):
+    """Items that one CTA takes whole."""
+    run_sinks(Batch(51, lens, Hq, Hkv, d, 64, 4, 3), 0.1, window, sinks)
+
+
+@pytest.mark.parametrize("d", [128, 64, 256])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([(2, 9)], 2, 1), ([(7, 200), (1, 1), (0, 0), (3, 400), (5, 4 * 32)], 8, 8), ([(16, 300)], 1, 1)])
+def test_trees_over_small_tables(lens, Hq, Hkv, d):
+    rng = np.random.default_rng(52)
+    bt = Batch(52, lens, Hq, Hkv, d, 32, 3, 4)
+    run_tree(bt, 0.1, random_trees(rng, lens)[1])
+
+
+@pytest.mark.parametrize("window", [100, 0])
+def test_sequences_between_lengths_that_step_back(window):
+    """cu_q 0 10 0 10 ...: every second sequence is out of range, and the others, of the same rows,
+    are more items than the number of rows lets one expect; the first is there at least."""
+    bt = Batch(53, [(10, 200)], 8, 2, 128, 32, 4, 3)
+    plan, q, cu, cache, table, ctx = bt.gpu()
+    ref = want(bt, 0.1, sinks_seen(bt, window, 3))
+    n = 7
+    cu = torch.tensor([0, 10] * ((n + 1) // 2), dtype=torch.int32).cuda()
+    out = abi.tq_attn_sinks_paged(plan, q, cu, cache, table.repeat(n, 1), ctx.repeat(n), 0.1, window, 3,
+                                  out_dtype=torch.float32)
+    assert abi.tq_device_status(reset=True) == 71
+    check(out, *ref, 10, bf16=False)
