@@ -519,7 +519,9 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 }
             }
 
-            bool zero = false;  // a row of the lane's has attended to V norms of 0 alone: its factor is 0
+            // a row of the lane's has attended to V norms of 0 alone (its factor is 0), or leads them
+            // so far that its factor has left fp32 (times a V norm of 0 it would be NaN)
+            bool lost = false;
             const int first_p = x.pos0 + x.tok0, last_p = x.pos0 + (x.row0 + x.rows - 1) / G;  // the rows' positions
             for (;;) {
                 const uint32_t st = taken % S;
@@ -585,7 +587,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                 // ---- probabilities, as B fragments.  Turn 0 takes the maxima as they are; if a
                 // score is 8 above m, a P above 2^15, or a norm not finite, they move and
                 // turn 1 follows, and where the factor of P is above 2^100 (a p that is lost
-                // could count) turn 2, by exponents
+                // could count) or is lost itself turn 2, by exponents
                 float p[2][NT][4], lv[2][2];
                 uint32_t pb[2][NT][2];
 #pragma unroll 1
@@ -620,7 +622,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                                 pb[u][nt][h] = *reinterpret_cast<const uint32_t*>(&hh);
                             }
                         }
-                    if (turn == 2 || !__any_sync(kAll, top > 8.f || ymax > 32768.f || odd != 0.f || zero)) break;
+                    if (turn == 2 || !__any_sync(kAll, top > 8.f || ymax > 32768.f || odd != 0.f || lost)) break;
                     if (turn == 1) continue;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
@@ -630,7 +632,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                                 kn[u][h] = __uint_as_float(0x7FFFFFFFu), vn[u][h] = 0.f;
                             lv[u][h] = __log2f(fabsf(vn[u][h]));
                         }
-                    zero = false;
+                    lost = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -663,7 +665,7 @@ k_attn_few(const __grid_constant__ PpArgs A, const __grid_constant__ PagedPrefil
                                 O[nt][mt][2 + k] *= fo;
                             }
                             cc[nt][k] = m1 == -INFINITY || M1 == -INFINITY ? 0.f : pp_exp2(m1 - M1);
-                            zero = zero || (M1 == -INFINITY && m1 > -INFINITY);
+                            lost = lost || (m1 > -INFINITY && (M1 == -INFINITY || cc[nt][k] > FLT_MAX));
                         }
                 }
 #pragma unroll
