@@ -732,16 +732,30 @@ def tq_pages_copy(src, dst, src_ids: torch.Tensor, dst_ids: torch.Tensor,
 _FRESH: dict = {}  # per device, stream and length: int32 tensors that no call has had yet
 
 
+def _results(device, several, *want):
+    """New tensors of each (dtype, size), or so many sets of them with one allocation
+    for each.  They may be written in any mode (a shared allocation outlives the call
+    and its inference_mode), and no two share the version counter that autograd
+    checks (as views would)."""
+    if torch.is_inference_mode_enabled():
+        with torch.inference_mode(False):
+            return _results(device, several, *want)
+    if not several:
+        return [torch.empty(*n, dtype=t, device=device) for t, *n in want]
+    return list(zip(*(torch.empty(several * n, *more, dtype=t, device=device).unsafe_split(n) if n else
+                      [torch.empty(0, *more, dtype=t, device=device) for _ in range(several)] for t, n, *more in want)))
+
+
 def _fresh(device, stream, n):
     """A new int32 tensor [n], several to an allocation (one costs more than half
     of a small call); in a capture one of the graph's own memory."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=_INT32, device=device)
+        return _results(device, 0, (_INT32, n))[0]
     key = (device.index, stream, n)
     try:
         return _FRESH[key].pop()
     except (KeyError, IndexError):  # none left, maybe since another thread took the last
-        new = list(torch.empty(max(1, min(64, 65536 // max(1, n))), n, dtype=_INT32, device=device).unbind())
+        new = [t for t, in _results(device, max(1, min(64, 65536 // max(1, n))), (_INT32, n))]
         first = new.pop()
         _FRESH[key] = new
         return first
@@ -863,23 +877,21 @@ def _step(device, stream, n_seqs, n_tokens, words):
     """New TokenSlots.  Where a step has the sizes of the one before it, several to
     an allocation (as _fresh; other sizes give up what is left, so that steps of
     many sizes hold no memory)."""
-    def empty(*lead):
-        return [torch.empty(*lead, n, dtype=t, device=device) for n, t in
-                ((n_seqs + 1, _INT32), (n_tokens, _INT32), (n_tokens, torch.int64))] + \
-            ([torch.empty(*lead, n_tokens, words, dtype=_INT32, device=device)] if words else [])
-
+    want = (_INT32, n_seqs + 1), (_INT32, n_tokens), (torch.int64, n_tokens)
+    if words:
+        want += (_INT32, n_tokens, words),
     several = min(16, 2 ** 20 // (4 * (n_seqs + 1 + n_tokens * (3 + words))))  # (1 MB at most is held)
     if several < 2 or torch._C._cuda_isCurrentStreamCapturing():
-        return TokenSlots(*empty())
+        return TokenSlots(*_results(device, 0, *want))
     key = (n_seqs, n_tokens, words)
     last, left = _STEPS.get((device.index, stream), (None, None))
     if last != key:
         _STEPS[device.index, stream] = key, []
-        return TokenSlots(*empty())
+        return TokenSlots(*_results(device, 0, *want))
     try:
         return TokenSlots(*left.pop())
     except IndexError:
-        new = list(zip(*(t.unbind() for t in empty(several))))
+        new = _results(device, several, *want)
         first = new.pop()
         _STEPS[device.index, stream] = key, new
         return TokenSlots(*first)
