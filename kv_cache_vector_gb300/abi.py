@@ -748,7 +748,8 @@ def _results(device, several, *want):
 
 def _fresh(device, stream, n):
     """A new int32 tensor [n], several to an allocation (one costs more than half
-    of a small call); in a capture one of the graph's own memory."""
+    of a small call); in a capture one of the graph's own memory.  For sizes that a
+    program has few of."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return _results(device, 0, (_INT32, n))[0]
     key = (device.index, stream, n)
@@ -758,6 +759,30 @@ def _fresh(device, stream, n):
         new = [t for t, in _results(device, max(1, min(64, 65536 // max(1, n))), (_INT32, n))]
         first = new.pop()
         _FRESH[key] = new
+        return first
+
+
+_LAST: dict = {}  # per device, stream and use: the last call's sizes, and results of them that no call has had yet
+
+
+def _again(device, stream, use, size, want):
+    """New tensors of each (dtype, size) of `want`, `size` bytes in all.  Where a use
+    has the sizes of its call before, several to an allocation (as _fresh); other
+    sizes give up what is left, so that calls of many sizes hold no memory."""
+    several = min(64 // len(want), 2 ** 20 // max(1, size))  # (1 MB at most is held)
+    if several < 2 or torch._C._cuda_isCurrentStreamCapturing():
+        return _results(device, 0, *want)
+    key = (device.index, stream, use)
+    last, left = _LAST.get(key, (None, None))
+    if last != want:
+        _LAST[key] = want, []
+        return _results(device, 0, *want)
+    try:
+        return left.pop()
+    except IndexError:
+        new = _results(device, several, *want)
+        first = new.pop()
+        _LAST[key] = want, new
         return first
 
 
@@ -870,31 +895,11 @@ def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_s
     return out
 
 
-_STEPS: dict = {}  # per device and stream: the last step's sizes, and TokenSlots of them that no call has had yet
-
-
 def _step(device, stream, n_seqs, n_tokens, words):
-    """New TokenSlots.  Where a step has the sizes of the one before it, several to
-    an allocation (as _fresh; other sizes give up what is left, so that steps of
-    many sizes hold no memory)."""
     want = (_INT32, n_seqs + 1), (_INT32, n_tokens), (torch.int64, n_tokens)
     if words:
         want += (_INT32, n_tokens, words),
-    several = min(16, 2 ** 20 // (4 * (n_seqs + 1 + n_tokens * (3 + words))))  # (1 MB at most is held)
-    if several < 2 or torch._C._cuda_isCurrentStreamCapturing():
-        return TokenSlots(*_results(device, 0, *want))
-    key = (n_seqs, n_tokens, words)
-    last, left = _STEPS.get((device.index, stream), (None, None))
-    if last != key:
-        _STEPS[device.index, stream] = key, []
-        return TokenSlots(*_results(device, 0, *want))
-    try:
-        return TokenSlots(*left.pop())
-    except IndexError:
-        new = _results(device, several, *want)
-        first = new.pop()
-        _STEPS[device.index, stream] = key, new
-        return TokenSlots(*first)
+    return TokenSlots(*_again(device, stream, "step", 4 * (n_seqs + 1 + n_tokens * (3 + words)), want))
 
 
 def tq_append_slots(plan: Plan, cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor):
@@ -936,7 +941,7 @@ def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_
         view = table._view(layers, shape)
         stream = _raw_stream(dev)
         if out is None:
-            out = _fresh(dev, stream, n_seqs)
+            out, = _again(dev, stream, "keep", 4 * n_seqs, ((_INT32, n_seqs),))
         else:
             _ints(dev, out)
             if out.numel() != n_seqs:

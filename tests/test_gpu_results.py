@@ -47,3 +47,28 @@ def test_results_of_a_loop_in_two_modes(first):
         loss.backward()
         assert weight.grad.sum() == 4 * T
     assert abi.tq_device_status(reset=True) == 0
+
+
+def test_batches_of_many_sizes_hold_no_memory():
+    """Each call of tq_pages_keep has another number of rows than the one before."""
+    most = 600
+    layers = abi.PagedLayers(pool(np.random.default_rng(1), 1, 4, 1, 32, 32, 4, 2))
+    table, zeros = abi.PageTable.empty(most, 1, 4), torch.zeros(most, dtype=torch.int32, device="cuda")
+    lists = zeros[:, None]
+
+    def all_sizes():
+        for n in range(1, most + 1):
+            part = abi.PageTable(table.block_table[:n], table.lens[:n], table.refs)
+            new = abi.tq_pages_keep(part, zeros[:n], lists[:n], zeros[:n], layers)
+            assert new.numel() == n
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        before = torch.cuda.memory_allocated()
+        all_sizes()
+        assert torch.cuda.memory_allocated() - before <= 2 ** 20
+        new = [abi.tq_pages_keep(table, zeros, lists, zeros, layers) for _ in range(100)]
+        assert len({t.data_ptr() for t in new}) == 100
+    side.synchronize()
+    assert abi.tq_device_status(reset=True) == 0
