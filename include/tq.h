@@ -383,8 +383,7 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
  * have a kernel of their own, which reads long contexts twice as fast.  Pages between the
  * sinks and the window of a sequence's first token are not looked at.
  * Arguments, accuracy, status words and errors as tq_attn_prefill_paged
- * (TQ_ERR_INVALID_ARG also for sinks < 0; where cu_q steps back, status 71, other
- * sequences may be left out too). */
+ * (TQ_ERR_INVALID_ARG also for sinks < 0). */
 size_t tq_attn_sinks_paged_workspace_bytes(int Hq, int Hkv, int d);
 tq_status tq_attn_sinks_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
                               tq_paged_cache cache, const int32_t *block_table, int max_pages,
@@ -404,8 +403,7 @@ tq_status tq_attn_sinks_paged(const tq_plan *plan, const void *q, int64_t n_q, i
  * A sequence with more tokens than positions or than 32 mask_words is left out
  * (its rows are not written) and sets the device status word to 75.
  * Other arguments, accuracy, status words and errors as tq_attn_prefill_paged
- * (TQ_ERR_INVALID_ARG also for a mask that overlaps out or the workspace; where
- * cu_q steps back, status 71, other sequences may be left out too). */
+ * (TQ_ERR_INVALID_ARG also for a mask that overlaps out or the workspace). */
 #define TQ_TREE_MAX_WORDS 32
 size_t tq_attn_tree_paged_workspace_bytes(int Hq, int Hkv, int d);
 tq_status tq_attn_tree_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,

@@ -813,8 +813,7 @@ static cudaError_t launch_few(const PagedPrefillCall& c, cudaStream_t s) {
     // (7) and 768 (9), us in parts and whole: d = 128, 4 rows 13.9 12.2, 13.8 12.8 and 14.0
     // 14.4, 16 rows 16.4 14.5, 16.4 16.6 and 16.7 18.4; d = 64 13.2 11.1, 13.2 11.5 and 13.2
     // 12.8; d = 256 15.8 15.1, 16.2 17.1 and 16.7 19.5.  The host saves a launch.  (A cu_q that steps back can give more items than
-    // CTAs; with the sequences out of range some of the others are left out then.  Going on
-    // to them cost the short windows 1.1 us.)
+    // CTAs: pp_start gives each a few.)
     const int64_t items = (c.n_q * G / Z::kRows + c.B) * c.Hkv;
     int64_t blocks = ((int64_t)c.max_pages << c.page_shift) / Z::kN + 1;
     if (MODE == kPpSinks && c.window > 0) {

@@ -322,8 +322,11 @@ __device__ __forceinline__ void pp_start(const PpArgs& A, long long* red, PpCurs
     // than a share of the line: the drafts of 4 sequences over 400-2000
     // positions took 24.7 us along the line, 20.8 us so.
     float cut = 0.f;
+    int each_cta = 1;  // items of a CTA, of which each is whole where they are more than one
     if (Z::kWhole && A.whole) {
         cut = 1e30f;  // one part each
+        // (sequences of rows that others have too, as a cu_q that steps back gives)
+        if (all > gridDim.x) each_cta = (all + gridDim.x - 1) / gridDim.x;
     } else if (each == 1 && all > 0 && all < gridDim.x) {
         const float over = (float)Z::kCostItem * Z::kN * (A.Hq / A.Hkv);
         const float c = fmaxf(1.f, __fdividef((sum - (float)all * over) * 1.000002f, grid - (float)all));
@@ -343,7 +346,7 @@ __device__ __forceinline__ void pp_start(const PpArgs& A, long long* red, PpCurs
         if (lane == 31) red2[warp] = ins;
         __syncthreads();
         for (int w = 0; w < warp; ++w) ins += red2[w];
-        int v = (int)blockIdx.x - (ins - sums);
+        int v = (int)blockIdx.x * each_cta - (ins - sums);
         if (v >= 0 && v < sums) {  // this thread's sequence holds this CTA's share
             int i = 0, n;
             for (;; ++i) {
@@ -359,6 +362,18 @@ __device__ __forceinline__ void pp_start(const PpArgs& A, long long* red, PpCurs
             start->n = q.n;
             start->ctx = q.ctx;
             start->q0 = q.q0;
+            if (Z::kWhole && each_cta > 1) {  // along the line, from this item's start to the end of the last
+                long long units = 0;
+                int b = b0, h = v;
+                for (int k = 0; k < each_cta; ++k, ++h) {
+                    if (h >= A.Hkv) h = 0, ++i;
+                    while (i >= q.tiles && ++b < A.B) q.load(A, b, nullptr), i = h = 0;
+                    if (b >= A.B) break;
+                    units += q.weight(i);
+                }
+                start->parts = 0;
+                start->left = units;
+            }
         }
         return;
     }
