@@ -8,6 +8,7 @@ kernels.  There is no fallback: if ``libtq.so`` is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from contextlib import nullcontext
 from dataclasses import dataclass
@@ -765,25 +766,28 @@ def _fresh(device, stream, n):
 _LAST: dict = {}  # per device, stream and use: the last call's sizes, and results of them that no call has had yet
 
 
-def _again(device, stream, use, size, want):
-    """New tensors of each (dtype, size) of `want`, `size` bytes in all.  Where a use
-    has the sizes of its call before, several to an allocation (as _fresh); other
-    sizes give up what is left, so that calls of many sizes hold no memory."""
-    several = min(64 // len(want), 2 ** 20 // max(1, size))  # (1 MB at most is held)
-    if several < 2 or torch._C._cuda_isCurrentStreamCapturing():
-        return _results(device, 0, *want)
-    key = (device.index, stream, use)
+def _again(device, stream, kinds, *sizes):
+    """New tensors of each (dtype, size) of kinds(*sizes).  Where the call before had
+    these sizes, several to an allocation (as _fresh); other sizes give up what is
+    left, so that calls of many sizes hold no memory."""
+    key, captured = (device.index, stream, kinds), torch._C._cuda_isCurrentStreamCapturing()
     last, left = _LAST.get(key, (None, None))
-    if last != want:
-        _LAST[key] = want, []
+    if last == sizes and not captured:
+        try:
+            return left.pop()
+        except IndexError:  # none left, maybe since another thread took the last
+            pass
+    want = kinds(*sizes)
+    several = min(64 // len(want), 2 ** 21 // max(1, sum(t.itemsize * math.prod(n) for t, *n in want)))  # (2 MB at most)
+    if captured or several < 2:
         return _results(device, 0, *want)
-    try:
-        return left.pop()
-    except IndexError:
-        new = _results(device, several, *want)
-        first = new.pop()
-        _LAST[key] = want, new
-        return first
+    if last != sizes:
+        _LAST[key] = sizes, []
+        return _results(device, 0, *want)
+    new = _results(device, several, *want)
+    first = new.pop()
+    _LAST[key] = sizes, new
+    return first
 
 
 def _pages(fn, table: PageTable, arg, layers, out, moved, info, workspace):
@@ -895,11 +899,13 @@ def tq_pages_slots(table: PageTable, counts: torch.Tensor, n_tokens: int, page_s
     return out
 
 
-def _step(device, stream, n_seqs, n_tokens, words):
+def _step_kinds(n_seqs, n_tokens, words):
     want = (_INT32, n_seqs + 1), (_INT32, n_tokens), (torch.int64, n_tokens)
-    if words:
-        want += (_INT32, n_tokens, words),
-    return TokenSlots(*_again(device, stream, "step", 4 * (n_seqs + 1 + n_tokens * (3 + words)), want))
+    return (*want, (_INT32, n_tokens, words)) if words else want
+
+
+def _step(device, stream, n_seqs, n_tokens, words):
+    return TokenSlots(*_again(device, stream, _step_kinds, n_seqs, n_tokens, words))
 
 
 def tq_append_slots(plan: Plan, cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor):
@@ -924,6 +930,10 @@ def tq_append_slots(plan: Plan, cache: PagedCache, k_new: torch.Tensor, v_new: t
             v_new.stride(0), _dt(k_new), n, Hkv, cache.view(), slots.data_ptr(), _raw_stream(dev)))
 
 
+def _keep_kinds(n_seqs):
+    return (_INT32, n_seqs),
+
+
 def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor, layers,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """Of row b's last counts[b] tokens those with the numbers keep[b, :n_keep[b]]
@@ -941,7 +951,7 @@ def tq_pages_keep(table: PageTable, counts: torch.Tensor, keep: torch.Tensor, n_
         view = table._view(layers, shape)
         stream = _raw_stream(dev)
         if out is None:
-            out, = _again(dev, stream, "keep", 4 * n_seqs, ((_INT32, n_seqs),))
+            out, = _again(dev, stream, _keep_kinds, n_seqs)
         else:
             _ints(dev, out)
             if out.numel() != n_seqs:
