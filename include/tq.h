@@ -556,8 +556,8 @@ tq_status tq_append_slots(const tq_plan *plan, int k_bits, int v_bits, const voi
  * (refs above 1) or out of range, stays as it is (new_lens[b] = lens[b]) and sets
  * the device status word to 66.
  * layers, alignment and errors as for the calls above (no workspace; new_lens
- * overlaps none of the inputs; no layer is given twice; n_seqs Hkv at most
- * 2^28). */
+ * overlaps none of the inputs; the arrays of all layers lie apart, and from the
+ * other arguments; n_seqs Hkv at most 2^28). */
 tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const int32_t *counts, const int32_t *keep,
                         int max_keep, const int32_t *n_keep, int32_t *new_lens, const tq_paged_cache *layers,
                         int n_layers, int Hkv, int d, int k_bits, int v_bits, tq_stream_t stream);

@@ -941,34 +941,67 @@ Span layer_span(const tq_paged_cache& c, int a, int Hkv, int d, int k_bits, int 
     return {reinterpret_cast<uintptr_t>(p), rows * (a == 0 ? d * k_bits / 8 : a == 2 ? d * v_bits / 8 : 4)};
 }
 
-// The arrays of n layers in the order of their addresses.
+// The arrays of n layers in the order of their addresses: as they come where layer
+// follows layer, or each kind's arrays one another; sorted otherwise (32 layers 1 us).
 int sorted_spans(const tq_paged_cache* layers, int n, int Hkv, int d, int k_bits, int v_bits, Span* out) {
+    auto before = [](const Span& x, const Span& y) { return x.at < y.at; };
     for (int i = 0; i < 4 * n; ++i) out[i] = layer_span(layers[i >> 2], i & 3, Hkv, d, k_bits, v_bits);
-    std::sort(out, out + 4 * n, [](const Span& x, const Span& y) { return x.at < y.at; });
+    if (std::is_sorted(out, out + 4 * n, before)) return 4 * n;
+    for (int a = 0; a < 4; ++a)
+        for (int l = 0; l < n; ++l) out[a * n + l] = layer_span(layers[l], a, Hkv, d, k_bits, v_bits);
+    if (!std::is_sorted(out, out + 4 * n, before)) std::sort(out, out + 4 * n, before);
     return 4 * n;
 }
 
-// Do an array of a and one of b overlap?  (Sorted 64 layers at a time and compared
-// group by group: past 64 layers the time grows with their square.)
+// Does a span of one sorted set overlap one of the other?
+bool spans_meet(const Span* x, int nx, const Span* y, int ny) {
+    // along both: a span that starts before the other side's furthest end overlaps it
+    uint64_t ex = 0, ey = 0;
+    for (int i = 0, j = 0; i < nx || j < ny;) {
+        const bool of_x = j == ny || (i < nx && x[i].at <= y[j].at);
+        const Span& s = of_x ? x[i++] : y[j++];
+        if (s.at < (of_x ? ey : ex)) return true;
+        uint64_t& e = of_x ? ex : ey;
+        if (s.at + s.bytes > e) e = s.at + s.bytes;
+    }
+    return false;
+}
+
+constexpr int kSortLayers = 64;  // layers sorted at a time; past them the time grows with their square
+
+// Do an array of a and one of b overlap?
 bool layers_overlap(const tq_paged_cache* a, const tq_paged_cache* b, int n, int Hkv, int d, int k_bits, int v_bits) {
-    constexpr int kAt = 64;  // layers at a time
+    constexpr int kAt = kSortLayers;
     Span x[4 * kAt], y[4 * kAt];
     for (int l = 0; l < n; l += kAt) {
         const int nx = sorted_spans(a + l, n - l < kAt ? n - l : kAt, Hkv, d, k_bits, v_bits, x);
         for (int m = 0; m < n; m += kAt) {
             const int ny = sorted_spans(b + m, n - m < kAt ? n - m : kAt, Hkv, d, k_bits, v_bits, y);
-            // along both: a span that starts before the other side's furthest end overlaps it
-            uint64_t ex = 0, ey = 0;
-            for (int i = 0, j = 0; i < nx || j < ny;) {
-                const bool of_x = j == ny || (i < nx && x[i].at <= y[j].at);
-                const Span& s = of_x ? x[i++] : y[j++];
-                if (s.at < (of_x ? ey : ex)) return true;
-                uint64_t& e = of_x ? ex : ey;
-                if (s.at + s.bytes > e) e = s.at + s.bytes;
-            }
+            if (spans_meet(x, nx, y, ny)) return true;
         }
     }
     return false;
+}
+
+// Are all arrays of the layers apart, and from the `others`?
+bool layers_apart(const tq_paged_cache* a, int n, int Hkv, int d, int k_bits, int v_bits, const Span* others,
+                  int n_others) {
+    constexpr int kAt = kSortLayers;
+    Span x[4 * kAt], y[4 * kAt];
+    for (int l = 0; l < n; l += kAt) {
+        const int nx = sorted_spans(a + l, n - l < kAt ? n - l : kAt, Hkv, d, k_bits, v_bits, x);
+        for (int i = 1; i < nx; ++i)
+            if (x[i].at < x[i - 1].at + x[i - 1].bytes) return false;
+        for (int o = 0; o < n_others; ++o) {  // the first array that ends behind its start
+            const Span* e = std::upper_bound(x, x + nx, others[o].at, [](uintptr_t at, const Span& s) { return at < s.at + s.bytes; });
+            if (e < x + nx && overlap(*e, others[o])) return false;
+        }
+        for (int m = l + kAt; m < n; m += kAt) {
+            const int ny = sorted_spans(a + m, n - m < kAt ? n - m : kAt, Hkv, d, k_bits, v_bits, y);
+            if (spans_meet(x, nx, y, ny)) return false;
+        }
+    }
+    return true;
 }
 
 // Fork, resize and compaction: the checks they share, then the launch.
@@ -1196,29 +1229,18 @@ tq_status tq_pages_keep(tq_page_table table, int n_seqs, int max_pages, const in
         return TQ_ERR_UNSUPPORTED;
     if (!table.block_table || !table.lens || !table.refs || !counts || !keep || !n_keep || !new_lens)
         return TQ_ERR_INVALID_ARG;
+    auto span = [](const void* p, uint64_t n) { return Span{reinterpret_cast<uintptr_t>(p), 4 * n}; };
+    const uint64_t n = (uint64_t)n_seqs;
+    const Span books[7] = {span(new_lens, n), span(table.block_table, n * max_pages), span(table.lens, n),
+                           span(table.refs, (uint64_t)layers[0].n_pages), span(counts, n), span(keep, n * max_keep),
+                           span(n_keep, n)};
+    for (int i = 1; i < 7; ++i)
+        if (overlap(books[0], books[i])) return TQ_ERR_INVALID_ARG;
+    // an array that two layers share would be moved twice; nothing that is read may be moved over
+    if (!layers_apart(layers, n_layers, Hkv, d, k_bits, v_bits, books, 7)) return TQ_ERR_INVALID_ARG;
     if (!aligned4(table.block_table) || !aligned4(table.lens) || !aligned4(table.refs) || !aligned4(counts) ||
         !aligned4(keep) || !aligned4(n_keep) || !aligned4(new_lens))
         return TQ_ERR_ALIGNMENT;
-    // a layer given twice would be moved twice
-    {
-        constexpr int kAt = 256;
-        const void* at[kAt];
-        const int m = n_layers < kAt ? n_layers : kAt;
-        for (int l = 0; l < m; ++l) at[l] = layers[l].k_packed;
-        std::sort(at, at + m);
-        for (int l = 1; l < m; ++l)
-            if (at[l] == at[l - 1]) return TQ_ERR_INVALID_ARG;
-        for (int l = kAt; l < n_layers; ++l)
-            for (int i = 0; i < l; ++i)
-                if (layers[l].k_packed == layers[i].k_packed) return TQ_ERR_INVALID_ARG;
-    }
-    auto span = [](const void* p, uint64_t n) { return Span{reinterpret_cast<uintptr_t>(p), 4 * n}; };
-    const uint64_t n = (uint64_t)n_seqs;
-    const Span wr = span(new_lens, n);
-    for (const Span& rd : {span(table.block_table, n * max_pages), span(table.lens, n),
-                           span(table.refs, (uint64_t)layers[0].n_pages), span(counts, n), span(keep, n * max_keep),
-                           span(n_keep, n)})
-        if (overlap(wr, rd)) return TQ_ERR_INVALID_ARG;
     if (!device_accessible(table.block_table) || !device_accessible(table.lens) || !device_accessible(table.refs) ||
         !device_accessible(counts) || !device_accessible(keep) || !device_accessible(n_keep) ||
         !device_accessible(new_lens) || !layers_accessible(layers, n_layers))
