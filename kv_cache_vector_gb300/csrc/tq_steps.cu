@@ -216,14 +216,16 @@ __global__ void __launch_bounds__(32 * kAsWarps) k_append_slots(const SlotRows A
 // every warp); 4 rows in 2 layers 4.0 us.
 constexpr int kKpWarps = 8;
 constexpr int kKpThreads = 32 * kKpWarps;
-constexpr int kKpEach = 4;     // (layer, KV head) pairs of a warp
+// (layer, KV head) pairs of a warp, us with 1 / 2 / 4 / 8: 4 rows in 2 layers 3.0 3.9 4.0 4.0,
+// 64 rows in 4 layers 3.5 4.4 6.2 6.2 and in 32 layers 16.9 12.7 12.4 11.1, 128 rows in 64
+// layers 56 40 32 31: the places are worked out once for them, and they follow one another
+constexpr int kKpEach = 4;
 constexpr int kKpList = 128;   // tokens whose places are known at a time
 constexpr int kKpBatch = 8;    // tokens that a warp moves at a time
 constexpr int kKpLayers = 64;  // most layers per launch
 
-template <int MAX>
 struct KeepLayers {
-    void* at[MAX][4];  // packed K, K norms, packed V, V norms
+    void* at[kKpLayers][4];  // packed K, K norms, packed V, V norms
 };
 
 struct KeepArgs {
@@ -284,8 +286,7 @@ __device__ __forceinline__ void keep_batch(void* const (&at)[4], int k_bytes, in
     else keep_batch<TK, uint32_t>(at, k_bytes, v_bytes, n, src, dst, up, lane);
 }
 
-template <int MAX>
-__global__ void __launch_bounds__(kKpThreads) k_pages_keep(const __grid_constant__ KeepLayers<MAX> P, int L, const KeepArgs A,
+__global__ void __launch_bounds__(kKpThreads) k_pages_keep(const __grid_constant__ KeepLayers P, int L, const KeepArgs A,
                                                            int* status) {
     __shared__ long long s_src[kKpList], s_dst[kKpList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -354,9 +355,8 @@ __global__ void __launch_bounds__(kKpThreads) k_pages_keep(const __grid_constant
     }
 }
 
-template <int MAX>
 static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, KeepArgs A, cudaStream_t s) {
-    KeepLayers<MAX> P;
+    KeepLayers P;
     for (int l = 0; l < L; ++l) {
         const tq_paged_cache& x = c.layers[l0 + l];
         P.at[l][0] = x.k_packed;
@@ -365,7 +365,7 @@ static cudaError_t launch_keep(const StepKeepCall& c, int l0, int L, KeepArgs A,
         P.at[l][3] = x.v_norm;
     }
     A.slices = (L * A.Hkv + kKpWarps * kKpEach - 1) / (kKpWarps * kKpEach);
-    return launch_pdl(k_pages_keep<MAX>, dim3((unsigned)A.n_seqs * A.slices), dim3(kKpThreads), 0, s, P, L, A, status_word());
+    return launch_pdl(k_pages_keep, dim3((unsigned)A.n_seqs * A.slices), dim3(kKpThreads), 0, s, P, L, A, status_word());
 }
 
 }  // namespace dev
@@ -434,7 +434,7 @@ cudaError_t launch_keep(const StepKeepCall& c, cudaStream_t s) {
     for (int l0 = 0; l0 < c.n_layers; l0 += kKpLayers) {
         const int L = c.n_layers - l0 < kKpLayers ? c.n_layers - l0 : kKpLayers;
         A.new_lens = l0 == 0 ? c.new_lens : nullptr;
-        const cudaError_t e = L <= 4 ? launch_keep<4>(c, l0, L, A, s) : launch_keep<kKpLayers>(c, l0, L, A, s);
+        const cudaError_t e = launch_keep(c, l0, L, A, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
