@@ -362,7 +362,8 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and
  * the device status word is set to 72 (entries of pages wholly in front of the
  * window of a sequence's first token are not looked at).  73: a bounded wait
- * gave up.
+ * gave up.  74: the driver placed the kernel's shared memory where it cannot
+ * work; nothing is written.
  * workspace: tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte
  * aligned like q, out and every array of the cache; calls that overlap on the
  * GPU need one each.
@@ -379,11 +380,20 @@ tq_status tq_attn_prefill_paged(const tq_plan *plan, const void *q, int64_t n_q,
  * window moves on, for conversations longer than the window: the token at
  * position p attends over positions j <= p with j > p - window or j < sinks.
  * A window of 0 is none (sinks then add nothing).  Prompt chunks, drafts and
- * single tokens, ragged in one batch; batches of few rows (n_q Hq / Hkv <= 16 B)
- * have a kernel of their own, which reads long contexts twice as fast.  Pages between the
- * sinks and the window of a sequence's first token are not looked at.
+ * single tokens, ragged in one batch.  Pages between the sinks and the window of
+ * a sequence's first token are not looked at.
+ * Batches of few rows (n_q Hq / Hkv <= 16 B) have a kernel of their own, which
+ * reads long contexts up to twice as fast; results are as accurate.  The choice
+ * is made on the host and knows averages only.  Rows of q behind cu_q's last
+ * entry count in n_q, and sequences without tokens in B: a buffer with much room
+ * leaves that kernel (64 single tokens, window 4096: 106 us, in a buffer of 1024
+ * rows 227 us), and a long tree or chunk among many single tokens stays in it,
+ * where its context is read again for every 16 of its rows (8 at d = 256): 160
+ * nodes over 32000 positions beside 63 single tokens take 637 us, where the other
+ * kernel needs 231.  Calls by themselves for such sequences, and n_q near the
+ * number of tokens, keep both fast.
  * Arguments, accuracy, status words and errors as tq_attn_prefill_paged
- * (TQ_ERR_INVALID_ARG also for sinks < 0). */
+ * (TQ_ERR_INVALID_ARG also for sinks < 0; status 76 as 74 there). */
 size_t tq_attn_sinks_paged_workspace_bytes(int Hq, int Hkv, int d);
 tq_status tq_attn_sinks_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,
                               tq_paged_cache cache, const int32_t *block_table, int max_pages,
@@ -402,8 +412,9 @@ tq_status tq_attn_sinks_paged(const tq_plan *plan, const void *q, int64_t n_q, i
  *     mask_words up to TQ_TREE_MAX_WORDS
  * A sequence with more tokens than positions or than 32 mask_words is left out
  * (its rows are not written) and sets the device status word to 75.
- * Other arguments, accuracy, status words and errors as tq_attn_prefill_paged
- * (TQ_ERR_INVALID_ARG also for a mask that overlaps out or the workspace). */
+ * Other arguments, accuracy, the kernel for few rows, status words and errors as
+ * tq_attn_sinks_paged (TQ_ERR_INVALID_ARG also for a mask that overlaps out or the
+ * workspace). */
 #define TQ_TREE_MAX_WORDS 32
 size_t tq_attn_tree_paged_workspace_bytes(int Hq, int Hkv, int d);
 tq_status tq_attn_tree_paged(const tq_plan *plan, const void *q, int64_t n_q, int B, int Hq, int Hkv,

@@ -1360,9 +1360,13 @@ tq_status attn_tokens_paged(const tq_plan* plan, const void* q, int64_t n_q, int
     c.mask_words = seen.words;
     // Few query rows per sequence and KV head (as an average: the lengths are on the
     // device) have a kernel of their own.  32 sequences of 6000 positions, 32 / 8 heads,
-    // K4/V3, d = 128: 4 rows 75 us here and 159 us in the multi-token kernel, 16 rows 108
-    // and 161, 24 rows (two items) 216 and 162; d = 256: 8 rows 131 and 284, 16 rows
-    // (two items) 236 and 283.
+    // K4/V3, d = 128: 4 rows 76 us here and 162 us in the multi-token kernel, 16 rows 110
+    // and 160, 24 rows (two items) 216 and 162; d = 256: 8 rows 135 and 271, 16 rows
+    // (two items) 245 and 272.
+    // The average is a bad guide for batches of very unequal sequences and of buffers with
+    // room: 63 single tokens over 2000 positions and a tree of 160 nodes over 32000 take
+    // 637 us here and 231 in the other kernel; 64 single tokens with a window of 4096 take
+    // 106 us in a buffer of 64 rows and 227 in one of 1024.
     const bool few = seen.mode != tq::kPpCausal && n_q * (Hq / Hkv) <= (int64_t)16 * B;
     // in the multi-token kernel sinks without a window (or none) are the causal mode
     const int mode = seen.mode == tq::kPpSinks && !few && (c.window == 0 || c.sinks == 0) ? (int)tq::kPpCausal : seen.mode;

@@ -28,11 +28,11 @@
 // position NaN, for the rows that attend to it, and its V row zero.
 //
 // What bounds it.  32 sequences of 6000 positions, 32 / 8 heads, one query token
-// (4 rows), d = 128, K4/V3: 75 us, 2.47 TB/s of packed rows; 16 rows 108 us; d = 64
+// (4 rows), d = 128, K4/V3: 76 us, 2.43 TB/s of packed rows; 16 rows 109 us; d = 64
 // 61 us; d = 256, K4/V4 127 us, 3.2 TB/s.  About 960 instructions a chunk and warp,
 // half of them byte permutes and shifts: the ALU is 45% busy, the lookups' pipe 44%,
 // an issue slot in two is used, and 12 warps of 168 registers leave 0.8 of 3 ready.
-// Measured and not kept: 16 warps of 128 registers (86 us, spills), chunks of 64
+// Measured and not kept: 16 warps of 128 registers (87 us, spills), chunks of 64
 // positions in 8 warps (88), V by byte permutes instead of lookups (87), a warp that
 // copies for the others (82: a bulk copy costs it some 100 cycles), rings of 3 blocks
 // with 10 warps (96).  Tiles of 32 rows take 5800 cycles a block of positions, where
@@ -810,10 +810,11 @@ static cudaError_t launch_few(const PagedPrefillCall& c, cudaStream_t s) {
     // Few items of few blocks (a short window, a small table): one CTA takes all of an
     // item, and no join follows.  By the most items and blocks that there can be, as the
     // lengths are on the device.  4 sequences, 8 KV heads, windows of 256 (5 blocks), 512
-    // (7) and 768 (9), us in parts and whole: d = 128, 4 rows 13.9 12.2, 13.8 12.8 and 14.0
-    // 14.4, 16 rows 16.4 14.5, 16.4 16.6 and 16.7 18.4; d = 64 13.2 11.1, 13.2 11.5 and 13.2
-    // 12.8; d = 256 15.8 15.1, 16.2 17.1 and 16.7 19.5.  The host saves a launch.  (A cu_q that steps back can give more items than
-    // CTAs: pp_start gives each a few.)
+    // (7) and 768 (9), us in parts and whole: d = 128, 4 rows 13.8 12.2, 13.7 12.8 and 13.9
+    // 14.3, 16 rows 16.4 15.2, 16.7 17.0 and 17.0 19.3; d = 64, 4 rows 13.1 11.1, 13.0 11.5
+    // and 13.2 12.5; d = 256, 4 rows 16.0 15.1, 16.5 17.4 and 16.9 19.8.  The host saves a
+    // launch.  (A cu_q that steps back can give more items than CTAs: pp_start gives each a
+    // few.)
     const int64_t items = (c.n_q * G / Z::kRows + c.B) * c.Hkv;
     int64_t blocks = ((int64_t)c.max_pages << c.page_shift) / Z::kN + 1;
     if (MODE == kPpSinks && c.window > 0) {
@@ -847,7 +848,7 @@ template <int D, int MODE>
 cudaError_t launch_attn_few(const PagedPrefillCall& c, cudaStream_t s) {
     // One tile of 8 rows, or two for more than 8 rows (of a sequence and KV head, as an
     // average), which read the positions once: 32 sequences of 6000 positions, 8 rows 79
-    // us, 12 rows 108 us.  At d = 256 two tiles leave no registers (the output alone takes
+    // us, 12 rows 109 us.  At d = 256 two tiles leave no registers (the output alone takes
     // 128).
     const int64_t rows = c.n_q * (c.Hq / c.Hkv);
     if (D == 256 || rows <= (int64_t)8 * c.B) return dev::launch_few<D, 1, MODE>(c, s);
