@@ -362,8 +362,8 @@ size_t tq_attn_prefill_paged_workspace_bytes(int Hq, int Hkv, int d);
  * outside [0, n_pages) is not read: its positions count as rows of norm 0 and
  * the device status word is set to 72 (entries of pages wholly in front of the
  * window of a sequence's first token are not looked at).  73: a bounded wait
- * gave up.  74: the driver placed the kernel's shared memory where it cannot
- * work; nothing is written.
+ * gave up.  74: the kernel's shared memory does not start where its layout needs
+ * it; nothing is written.
  * workspace: tq_attn_prefill_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte
  * aligned like q, out and every array of the cache; calls that overlap on the
  * GPU need one each.
